@@ -20,6 +20,16 @@ library has not been built, every call raises.
                      err_word=None, silu=True)
     gdn_conv_commit(conv_state, state_indices, records, accept_len, err_word=None)
 
+and, for the softmax-attention layers between the recurrent ones, over a paged 4-bit K/V cache (``Kv4Cache``):
+
+    gdn_page_plan(kv_lens, new_lens, page_size, block_tables, held, free_pages, taken, plan, ticket, err_word=None)
+    gdn_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out=None, *, v=None, cache=None,
+                     slot_map=None, err_word=None, eps=1e-6, interleaved=False)
+    gdn_kv4_read(cache, slot_map, k_out, v_out, err_word=None)
+    gdn_kv4_attention(q, cache, block_tables, kv_lens, o, workspace, *, cu_seqlens=None, max_q=None, lse=None,
+                      scale=None, err_word=None)
+    kv4_attention_workspace(B, max_q, HQ, HK, D, device=None)
+
 Shapes and semantics are those of ``include/gdn.h``: q, k ``[B,T,HK,DK]``; v, o ``[B,T,HV,DV]``; a, b
 ``[B,T,HV]``; A_log, dt_bias ``[HV]`` fp32; state_pool ``[num_slots,HV,DV,DK]``; state_indices, accept_len
 ``[B]`` int32; intermediate_states ``[B,T,HV,DV,DK]``; err_word a 1-element int32 device tensor.  Prefill takes
@@ -39,7 +49,9 @@ from .build import LIB_PATH
 __all__ = ["gdn_decode", "gdn_decode_gated", "gdn_mtp_verify", "gdn_commit", "gdn_commit_replay", "gdn_mtp_verify_commit", "ReplayTokens",
            "gdn_mtp_verify_gated", "GatedNorm",
            "gdn_prefill", "gdn_gated_rmsnorm", "gdn_in_proj_conv", "gdn_conv_commit", "InProjOut", "GdnError", "GdnDims", "lib", "STATUS", "ERRBIT_INDEX", "ERRBIT_ACCEPT_LEN", "ERRBIT_TIMEOUT",
-           "ERRBIT_SEQLEN", "MAX_T", "EXPORTS"]
+           "ERRBIT_SEQLEN", "ERRBIT_PAGES", "ERRBIT_NONFINITE", "MAX_T", "EXPORTS",
+           "gdn_page_plan", "gdn_qk_norm_rope", "gdn_kv4_read", "gdn_kv4_attention", "kv4_attention_workspace", "Kv4Cache",
+           "PagePlan"]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_DTYPE", 4: "GDN_ERR_ALIGN",
           5: "GDN_ERR_UNSUPPORTED", 6: "GDN_ERR_CUDA", 7: "GDN_ERR_VALUE"}
@@ -47,12 +59,15 @@ ERRBIT_INDEX = 1
 ERRBIT_ACCEPT_LEN = 2
 ERRBIT_TIMEOUT = 4
 ERRBIT_SEQLEN = 8
+ERRBIT_PAGES = 16
+ERRBIT_NONFINITE = 32
 MAX_T = 16
 F32, BF16 = 0, 1
 EXPORTS = ("gdn_decode", "gdn_decode_gated", "gdn_mtp_verify", "gdn_commit", "gdn_commit_replay",
            "gdn_mtp_verify_commit", "gdn_mtp_verify_gated", "gdn_prefill",
-           "gdn_gated_rmsnorm", "gdn_in_proj_conv", "gdn_conv_commit", "gdn_status_string", "gdn_last_cuda_error",
-           "gdn_abi_version")
+           "gdn_gated_rmsnorm", "gdn_in_proj_conv", "gdn_conv_commit", "gdn_page_plan", "gdn_qk_norm_rope",
+           "gdn_kv4_read", "gdn_kv4_attention", "gdn_kv4_attention_workspace", "gdn_status_string",
+           "gdn_last_cuda_error", "gdn_abi_version")
 
 
 class GdnDims(ctypes.Structure):
@@ -107,6 +122,69 @@ class InProjOut:
         self.q, self.k, self.v, self.z, self.b, self.a = q, k, v, z, b, a
 
 
+class _Kv4CacheC(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("HK", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Kv4Cache:
+    """The paged 4-bit K/V cache of one attention layer: ``codes`` ``[num_pages, 2, HK, page_size, D / 2]`` and ``scales``
+    ``[num_pages, 2, HK, page_size, D / 16]``, uint8 on one GPU (keys 0, values 1; two e2m1 codes a byte, an e4m3 scale for
+    each 16 dimensions); ``k_scale`` and ``v_scale`` (powers of two) multiply every number."""
+
+    def __init__(self, codes, scales, k_scale=1.0, v_scale=1.0):
+        import torch
+
+        if codes.dim() != 5 or scales.dim() != 5:
+            raise ValueError("codes is [num_pages,2,HK,page_size,D/2], scales [num_pages,2,HK,page_size,D/16]")
+        num_pages, two, HK, page_size, half = codes.shape
+        _shape(codes, (num_pages, 2, HK, page_size, half), "codes")
+        _shape(scales, (num_pages, 2, HK, page_size, half // 8), "scales")
+        self.device = _common_device([("codes", codes), ("scales", scales)])
+        self.codes, self.scales = codes, scales
+        self.num_pages, self.page_size, self.HK, self.D = num_pages, page_size, HK, 2 * half
+        self.c = _Kv4CacheC(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8), num_pages, page_size,
+                            HK, 2 * half, float(k_scale), float(v_scale))
+        self.ref = ctypes.byref(self.c)
+
+
+class _PagePlanC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu_seqlens", "positions", "slot_map", "total_lens", "held", "taken")]
+
+
+class PagePlan:
+    """What ``gdn_page_plan`` writes, int32 on one GPU: ``cu_seqlens`` ``[B+1]``, ``positions`` and ``slot_map`` ``[N]``,
+    ``total_lens`` and ``held`` ``[B]``, ``taken`` ``[1]`` (``held`` and ``taken`` may be the call's inputs)."""
+
+    def __init__(self, cu_seqlens, positions, slot_map, total_lens, held, taken):
+        import torch
+
+        B, N = cu_seqlens.numel() - 1, positions.numel()
+        named = (("cu_seqlens", cu_seqlens, B + 1), ("positions", positions, N), ("slot_map", slot_map, N),
+                 ("total_lens", total_lens, B), ("held", held, B), ("taken", taken, 1))
+        for name, t, n in named:
+            _shape(t, (n,), name)
+        self.device = _common_device([(name, t) for name, t, _ in named])
+        self.B, self.N = B, N
+        self.cu_seqlens, self.positions, self.slot_map = cu_seqlens, positions, slot_map
+        self.total_lens, self.held, self.taken = total_lens, held, taken
+        self.c = _PagePlanC(*(_dev(t, name, torch.int32) for name, t, _ in named))
+        self.ref = ctypes.byref(self.c)
+
+
+class _QkDimsC(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("HQ", ctypes.c_int32), ("HK", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("R", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
+
+
+class _Kv4AttentionDimsC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("max_q", ctypes.c_int32), ("HQ", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -143,7 +221,15 @@ def lib() -> ctypes.CDLL:
         L.gdn_in_proj_conv.argtypes = [cdp, vp, vp, vp, vp, vp, ip, ctypes.c_int32, ctypes.POINTER(_InProjOutC), vp,
                                        ip, vp]
         L.gdn_conv_commit.argtypes = [cdp, vp, ip, vp, ip, ip, vp]
-        for f in (L.gdn_in_proj_conv, L.gdn_conv_commit):
+        i32 = ctypes.c_int32
+        L.gdn_page_plan.argtypes = [i32] * 5 + [vp] * 9
+        L.gdn_qk_norm_rope.argtypes = [vp] * 14
+        L.gdn_kv4_read.argtypes = [vp, i32] + [vp] * 5
+        L.gdn_kv4_attention.argtypes = [vp] * 9 + [ctypes.c_int64, vp, vp]
+        L.gdn_kv4_attention_workspace.argtypes = [i32] * 5
+        L.gdn_kv4_attention_workspace.restype = ctypes.c_int64
+        for f in (L.gdn_in_proj_conv, L.gdn_conv_commit, L.gdn_page_plan, L.gdn_qk_norm_rope, L.gdn_kv4_read,
+                  L.gdn_kv4_attention):
             f.restype = ctypes.c_int
         for f in (L.gdn_decode, L.gdn_decode_gated, L.gdn_mtp_verify, L.gdn_commit, L.gdn_commit_replay, L.gdn_mtp_verify_commit,
                   L.gdn_mtp_verify_gated, L.gdn_prefill, L.gdn_gated_rmsnorm):
@@ -600,3 +686,170 @@ def gdn_conv_commit(conv_state, state_indices, records, accept_len, err_word=Non
             (ctypes.byref(d), _dev(conv_state, "conv_state"), _dev(state_indices, "state_indices"),
              _dev(records, "records"), _dev(accept_len, "accept_len"), _dev(err_word, "err_word", torch.int32)),
             "gdn_conv_commit")
+
+
+# ---- attention over the paged 4-bit cache ------------------------------------------------------------
+# These calls take a few microseconds on the GPU, so their marshalling is kept as short as its checks allow.
+def _ptr(t, name: str, dtype, shape, dev: int):
+    """Address of a contiguous CUDA tensor of this dtype and shape on GPU `dev` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}, as the other tensors of the call are: it is on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _run(dev: int, stream, fn, args, what: str) -> None:
+    """One library call on GPU `dev`'s given or current stream, with that GPU current."""
+    import torch
+
+    if stream is not None:
+        s = _stream(stream, torch.device("cuda", dev))
+    else:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != 0:
+        raise GdnError(status, what)
+
+
+def _gpu(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def gdn_page_plan(kv_lens, new_lens, page_size, block_tables, held, free_pages, taken, plan, ticket, err_word=None, *,
+                  stream=None) -> None:
+    """Block tables, slot map, positions and offsets of a step: lane b has ``kv_lens[b]`` cached tokens in ``held[b]``
+    pages and brings ``new_lens[b]`` more.  New pages come from ``free_pages[taken:]`` into ``block_tables``
+    ``[B, max_pages]``; the rest goes into ``plan`` (a ``PagePlan``).  ``ticket`` is one int32, 0 before the first call."""
+    import torch
+
+    L = lib()
+    dev = _gpu(kv_lens, "kv_lens")
+    if block_tables.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_tables is [B,max_pages], free_pages [num_pages]")
+    i32, B = torch.int32, plan.B
+    if plan.device.index != dev:
+        raise ValueError(f"plan is on {plan.device}, kv_lens on GPU {dev}")
+    max_pages, num_pages = block_tables.shape[1], free_pages.shape[0]
+    _run(dev, stream, L.gdn_page_plan,
+         (B, plan.N, page_size, max_pages, num_pages, _ptr(kv_lens, "kv_lens", i32, (B,), dev),
+          _ptr(new_lens, "new_lens", i32, (B,), dev), _ptr(block_tables, "block_tables", i32, (B, max_pages), dev),
+          _ptr(held, "held", i32, (B,), dev), _ptr(free_pages, "free_pages", i32, (num_pages,), dev),
+          _ptr(taken, "taken", i32, (1,), dev), plan.ref, _ptr(ticket, "ticket", i32, (1,), dev),
+          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_page_plan")
+
+
+def _rows(t, name: str, dtype, shape, dev: int):
+    """Address and token stride of a tensor ``[N, heads, D]`` whose tokens are without gaps in themselves."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}, as the other tensors of the call are: it is on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    step, head, one = t.stride()
+    if (one != 1 and shape[2] > 1) or (head != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), step if shape[0] > 1 else shape[1] * shape[2]
+
+
+def gdn_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out=None, *, v=None, cache=None,
+                     slot_map=None, err_word=None, eps=1e-6, interleaved=False, stream=None) -> None:
+    """RMS norm of every head of q ``[N,HQ,D]`` and k ``[N,HK,D]`` (any token stride) and the rotation of its first
+    ``2 * len(inv_freq)`` dimensions by ``positions[n] * inv_freq`` into ``q_out`` and ``k_out``.  With ``cache`` (a
+    ``Kv4Cache``), v ``[N,HK,D]`` and ``slot_map`` ``[N]``, the keys and values are stored there; k_out may be None."""
+    import torch
+
+    L = lib()
+    dev = _gpu(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or inv_freq.dim() != 1:
+        raise ValueError("q is [N,HQ,D], k [N,HK,D], inv_freq [R/2]")
+    N, HQ, D = q.shape
+    HK, half = k.shape[1], inv_freq.shape[0]
+    dt, f32, i32 = q.dtype, torch.float32, torch.int32
+    code = _code(q, "q")
+    qp, qs = _rows(q, "q", dt, (N, HQ, D), dev)
+    kp, ks = _rows(k, "k", dt, (N, HK, D), dev)
+    vp, vs = (None, 0) if v is None else _rows(v, "v", dt, (N, HK, D), dev)
+    if cache is not None and cache.device.index != dev:
+        raise ValueError(f"cache is on {cache.device}, q on GPU {dev}")
+    d = _QkDimsC(N, HQ, HK, D, 2 * half, 1 if interleaved else 0, code, qs, ks, vs, eps)
+    _run(dev, stream, L.gdn_qk_norm_rope,
+         (ctypes.byref(d), qp, kp, _ptr(q_weight, "q_weight", f32, (D,), dev), _ptr(k_weight, "k_weight", f32, (D,), dev),
+          _ptr(positions, "positions", i32, (N,), dev), _ptr(inv_freq, "inv_freq", f32, (half,), dev),
+          _ptr(q_out, "q_out", dt, (N, HQ, D), dev), _ptr(k_out, "k_out", dt, (N, HK, D), dev), vp,
+          None if cache is None else cache.ref, _ptr(slot_map, "slot_map", i32, (N,), dev),
+          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_qk_norm_rope")
+
+
+def gdn_kv4_read(cache, slot_map, k_out, v_out, err_word=None, *, stream=None) -> None:
+    """The cached rows of ``slot_map`` ``[N]`` as numbers: ``k_out``, ``v_out`` ``[N,HK,D]`` bf16."""
+    import torch
+
+    L = lib()
+    dev, N, bf16 = _gpu(slot_map, "slot_map"), slot_map.shape[0], torch.bfloat16
+    if cache.device.index != dev:
+        raise ValueError(f"cache is on {cache.device}, slot_map on GPU {dev}")
+    shape = (N, cache.HK, cache.D)
+    _run(dev, stream, L.gdn_kv4_read,
+         (cache.ref, N, _ptr(slot_map, "slot_map", torch.int32, (N,), dev), _ptr(k_out, "k_out", bf16, shape, dev),
+          _ptr(v_out, "v_out", bf16, shape, dev), _ptr(err_word, "err_word", torch.int32, (1,), dev)), "gdn_kv4_read")
+
+
+def kv4_attention_workspace(B, max_q, HQ, HK, D, device=None):
+    """A workspace for ``gdn_kv4_attention`` calls of up to B lanes and max_q tokens a lane (one call at a time)."""
+    import torch
+
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        n = lib().gdn_kv4_attention_workspace(B, max_q, HQ, HK, D)
+    if n < 0:
+        raise ValueError(f"kv4_attention_workspace: sizes out of range (B {B}, max_q {max_q}, HQ {HQ}, HK {HK}, D {D})")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def gdn_kv4_attention(q, cache, block_tables, kv_lens, o, workspace, *, cu_seqlens=None, max_q=None, lse=None, scale=None,
+                      err_word=None, stream=None) -> None:
+    """Causal attention of q ``[N,HQ,D]`` bf16 over each lane's cached tokens (``kv_lens`` ``[B]``, the step's own
+    included) into ``o`` and, if given, ``lse`` ``[N,HQ]`` fp32.  Lane b's rows are ``cu_seqlens[b] .. cu_seqlens[b+1]-1``
+    (then ``max_q``, the most of any lane, has to be given), or N / B rows each.  ``scale`` is 1 / sqrt(D) by default."""
+    import torch
+
+    L = lib()
+    dev = _gpu(q, "q")
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q is [N,HQ,D], block_tables [B,max_pages]")
+    N, HQ, D = q.shape
+    B, max_pages = block_tables.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    if cu_seqlens is None:
+        if B > 0 and N % B != 0:
+            raise ValueError(f"q: {N} rows are not the same number for each of {B} lanes: give cu_seqlens")
+        max_q = max(1, N // B) if B > 0 else 1
+    elif max_q is None:
+        raise ValueError("max_q, the most tokens of a lane, goes with cu_seqlens")
+    if cache.device.index != dev:
+        raise ValueError(f"cache is on {cache.device}, q on GPU {dev}")
+    if D != cache.D:
+        raise ValueError(f"q: head dimension {D}, the cache's is {cache.D}")
+    d = _Kv4AttentionDimsC(B, N, max_q, HQ, max_pages, D ** -0.5 if scale is None else scale)
+    _run(dev, stream, L.gdn_kv4_attention,
+         (ctypes.byref(d), cache.ref, _ptr(q, "q", bf16, (N, HQ, D), dev),
+          _ptr(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev), _ptr(block_tables, "block_tables", i32, (B, max_pages), dev),
+          _ptr(kv_lens, "kv_lens", i32, (B,), dev), _ptr(o, "o", bf16, (N, HQ, D), dev),
+          _ptr(lse, "lse", torch.float32, (N, HQ), dev),
+          _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel(),
+          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_kv4_attention")

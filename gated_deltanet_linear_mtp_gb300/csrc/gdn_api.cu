@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "gdn.h"
 #include "gdn_internal.h"
@@ -81,6 +82,24 @@ gdn_status check_io(const gdn_dims* d, const void* q, const void* k, const void*
     if (!aligned(A_log, 4) || !aligned(dt_bias, 4) || !aligned(idx, 4)) return GDN_ERR_ALIGN;
     if (!aligned(o, dtype_bytes(d->out_dtype))) return GDN_ERR_ALIGN;
     if (err && !aligned(err, 4)) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+// The cache of the attention calls: sizes, scales that are powers of two (a multiplication by them is exact), pointers.
+gdn_status check_cache(const gdn_kv4_cache* c, Kv4* out) {
+    if (c == nullptr) return GDN_ERR_NULL;
+    if (c->num_pages < 1 || c->HK < 1 || c->HK > 1024) return GDN_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return GDN_ERR_SHAPE;
+    if ((int64_t)c->num_pages * c->page_size >= (int64_t)1 << 31) return GDN_ERR_SHAPE;
+    if (c->D != 64 && c->D != 128 && c->D != 256) return GDN_ERR_UNSUPPORTED;
+    for (const float s : {c->k_scale, c->v_scale}) {
+        int e = 0;
+        if (!std::isfinite(s) || !(s > 0.f) || std::frexp(s, &e) != 0.5f || e < -31 || e > 33) return GDN_ERR_VALUE;
+    }
+    if (!c->codes || !c->scales) return GDN_ERR_NULL;
+    if (!aligned(c->codes, 16) || !aligned(c->scales, 16)) return GDN_ERR_ALIGN;
+    *out = Kv4{static_cast<uint8_t*>(c->codes), static_cast<uint8_t*>(c->scales), c->num_pages, c->page_size, c->HK, c->D,
+               c->k_scale, c->v_scale};
     return GDN_OK;
 }
 
@@ -486,6 +505,148 @@ gdn_status gdn_conv_commit(const gdn_conv_dims* dims, void* conv_state, const in
     return finish(launch_conv_commit(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+gdn_status gdn_page_plan(int32_t B, int32_t N, int32_t page_size, int32_t max_pages, int32_t num_pages,
+                         const int32_t* kv_lens, const int32_t* new_lens, int32_t* block_tables, const int32_t* held,
+                         const int32_t* free_pages, const int32_t* taken, const gdn_page_plan_out* out, int32_t* ticket,
+                         int32_t* err_word, gdn_stream_t stream) {
+    if (B < 0 || B > 8192 || N < 0 || num_pages < 1 || max_pages < 1) return GDN_ERR_SHAPE;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return GDN_ERR_SHAPE;
+    if ((int64_t)num_pages * page_size >= (int64_t)1 << 31 || (int64_t)max_pages * page_size >= (int64_t)1 << 31)
+        return GDN_ERR_SHAPE;
+    if (B == 0) return GDN_OK;
+    if (!kv_lens || !new_lens || !block_tables || !held || !free_pages || !taken || !out || !ticket) return GDN_ERR_NULL;
+    if (!out->cu_seqlens || !out->total_lens || !out->held || !out->taken) return GDN_ERR_NULL;
+    if (N > 0 && (!out->positions || !out->slot_map)) return GDN_ERR_NULL;
+    for (const void* q : {(const void*)kv_lens, (const void*)new_lens, (const void*)block_tables, (const void*)held,
+                          (const void*)free_pages, (const void*)taken, (const void*)out->cu_seqlens,
+                          (const void*)out->positions, (const void*)out->slot_map, (const void*)out->total_lens,
+                          (const void*)out->held, (const void*)out->taken, (const void*)ticket, (const void*)err_word})
+        if (!aligned(q, 4)) return GDN_ERR_ALIGN;
+    const PagePlanParams p{B,          N,     page_size,       max_pages,      num_pages,     kv_lens,         new_lens,
+                           block_tables, held, free_pages,      taken,          out->cu_seqlens, out->positions,
+                           out->slot_map, out->total_lens, out->held, out->taken, ticket,       err_word};
+    return finish(launch_page_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_qk_norm_rope(const gdn_qk_dims* dims, const void* q, const void* k, const float* q_weight,
+                            const float* k_weight, const int32_t* positions, const float* inv_freq, void* q_out,
+                            void* k_out, const void* v, const gdn_kv4_cache* cache, const int32_t* slot_map,
+                            int32_t* err_word, gdn_stream_t stream) {
+    if (dims == nullptr) return GDN_ERR_NULL;
+    if (dims->N < 0 || dims->HQ < 1 || dims->HQ > 1024 || dims->HK < 1 || dims->HK > 1024) return GDN_ERR_SHAPE;
+    if (dims->D != 64 && dims->D != 128 && dims->D != 256) return GDN_ERR_UNSUPPORTED;
+    if (dims->R < 0 || dims->R > dims->D || dims->R % 16 != 0) return GDN_ERR_SHAPE;
+    if (dims->interleaved != 0 && dims->interleaved != 1) return GDN_ERR_VALUE;
+    if (!valid_dtype(dims->dtype)) return GDN_ERR_DTYPE;
+    if (!std::isfinite(dims->eps) || dims->eps < 0.f) return GDN_ERR_VALUE;
+    const bool store = cache != nullptr;
+    if (store != (v != nullptr) || store != (slot_map != nullptr)) return GDN_ERR_NULL;
+    const int64_t sz = (int64_t)dtype_bytes(dims->dtype), D = dims->D;
+    if (dims->q_stride < dims->HQ * D || dims->k_stride < dims->HK * D || (store && dims->v_stride < dims->HK * D))
+        return GDN_ERR_SHAPE;
+    if (dims->q_stride > (int64_t)1 << 31 || dims->k_stride > (int64_t)1 << 31 || (store && dims->v_stride > (int64_t)1 << 31))
+        return GDN_ERR_SHAPE;
+    QkNormRopeParams p{};
+    if (store) {
+        const gdn_status s = check_cache(cache, &p.kv);
+        if (s != GDN_OK) return s;
+        if (cache->HK != dims->HK || cache->D != dims->D) return GDN_ERR_SHAPE;
+    }
+    if (dims->N == 0) return GDN_OK;
+    if (!q || !k || !q_weight || !k_weight || !positions || !q_out || (!k_out && !store) || (dims->R > 0 && !inv_freq))
+        return GDN_ERR_NULL;
+    if (dims->q_stride * sz % 16 || dims->k_stride * sz % 16 || (store && dims->v_stride * sz % 16)) return GDN_ERR_ALIGN;
+    for (const void* x : {q, k, (const void*)q_weight, (const void*)k_weight, (const void*)q_out, (const void*)k_out, v})
+        if (!aligned(x, 16)) return GDN_ERR_ALIGN;
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(slot_map, 4) || !aligned(err_word, 4))
+        return GDN_ERR_ALIGN;
+    p.N = dims->N;
+    p.HQ = dims->HQ;
+    p.HK = dims->HK;
+    p.D = dims->D;
+    p.R = dims->R;
+    p.interleaved = dims->interleaved;
+    p.q_stride = dims->q_stride;
+    p.k_stride = dims->k_stride;
+    p.v_stride = dims->v_stride;
+    p.eps = dims->eps;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.qw = q_weight;
+    p.kw = k_weight;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.slot_map = slot_map;
+    p.err = err_word;
+    return finish(launch_qk_norm_rope(p, dims->dtype == GDN_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv4_read(const gdn_kv4_cache* cache, int32_t N, const int32_t* slot_map, void* k_out, void* v_out,
+                        int32_t* err_word, gdn_stream_t stream) {
+    Kv4ReadParams p{};
+    const gdn_status s = check_cache(cache, &p.kv);
+    if (s != GDN_OK) return s;
+    if (N < 0) return GDN_ERR_SHAPE;
+    if (N == 0) return GDN_OK;
+    if (!slot_map || !k_out || !v_out) return GDN_ERR_NULL;
+    if (!aligned(slot_map, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(err_word, 4)) return GDN_ERR_ALIGN;
+    p.N = N;
+    p.slot_map = slot_map;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.err = err_word;
+    return finish(launch_kv4_read(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t gdn_kv4_attention_workspace(int32_t B, int32_t max_q, int32_t HQ, int32_t HK, int32_t D) {
+    if (B < 0 || B > 65535 || max_q < 1 || HK < 1 || HK > 1024 || HQ < HK || HQ % HK != 0 || HQ / HK > 64) return -1;
+    if (D != 64 && D != 128 && D != 256) return -1;
+    return kv4_attention_workspace(B, max_q, HQ, HK, D);
+}
+
+gdn_status gdn_kv4_attention(const gdn_kv4_attention_dims* dims, const gdn_kv4_cache* cache, const void* q,
+                             const int32_t* cu_seqlens, const int32_t* block_tables, const int32_t* kv_lens, void* o,
+                             float* lse, void* workspace, int64_t workspace_bytes, int32_t* err_word,
+                             gdn_stream_t stream) {
+    if (dims == nullptr) return GDN_ERR_NULL;
+    Kv4AttentionParams p{};
+    const gdn_status s = check_cache(cache, &p.kv);
+    if (s != GDN_OK) return s;
+    const int32_t HK = cache->HK;
+    if (dims->B < 0 || dims->B > 65535 || dims->N < 0 || dims->max_q < 1 || dims->max_pages < 1) return GDN_ERR_SHAPE;
+    if (dims->HQ < HK || dims->HQ % HK != 0 || dims->HQ / HK > 64) return GDN_ERR_SHAPE;
+    if ((int64_t)dims->N * dims->HQ >= (int64_t)1 << 31 || (int64_t)dims->max_pages * cache->page_size >= (int64_t)1 << 31)
+        return GDN_ERR_SHAPE;
+    if (!cu_seqlens && (int64_t)dims->B * dims->max_q != dims->N) return GDN_ERR_SHAPE;
+    if (!std::isfinite(dims->scale)) return GDN_ERR_VALUE;
+    if (dims->B == 0 || dims->N == 0) return GDN_OK;
+    if (!q || !block_tables || !kv_lens || !o || !workspace) return GDN_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16)) return GDN_ERR_ALIGN;
+    if (!aligned(cu_seqlens, 4) || !aligned(block_tables, 4) || !aligned(kv_lens, 4) || !aligned(lse, 4) ||
+        !aligned(err_word, 4))
+        return GDN_ERR_ALIGN;
+    if (workspace_bytes < kv4_attention_workspace(dims->B, dims->max_q, dims->HQ, HK, cache->D)) return GDN_ERR_SHAPE;
+    p.B = dims->B;
+    p.N = dims->N;
+    p.T = dims->max_q < dims->N ? dims->max_q : dims->N;
+    p.HQ = dims->HQ;
+    p.G = dims->HQ / HK;
+    p.max_pages = dims->max_pages;
+    p.q = q;
+    p.cu_seqlens = cu_seqlens;
+    p.block_tables = block_tables;
+    p.kv_lens = kv_lens;
+    p.o = o;
+    p.lse = lse;
+    p.workspace = workspace;
+    p.scale = dims->scale;
+    p.err = err_word;
+    return finish(launch_kv4_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char* gdn_status_string(gdn_status status) {
     switch (status) {
     case GDN_OK: return "GDN_OK";
@@ -493,9 +654,9 @@ const char* gdn_status_string(gdn_status status) {
     case GDN_ERR_SHAPE: return "GDN_ERR_SHAPE: a size is out of range or inconsistent";
     case GDN_ERR_DTYPE: return "GDN_ERR_DTYPE: unknown dtype code";
     case GDN_ERR_ALIGN: return "GDN_ERR_ALIGN: a pointer is misaligned";
-    case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: DK must be 16, 32, 64, 128 or 256";
+    case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: DK must be 16, 32, 64, 128 or 256 (attention: D 64, 128 or 256)";
     case GDN_ERR_CUDA: return "GDN_ERR_CUDA: kernel launch failed (see gdn_last_cuda_error)";
-    case GDN_ERR_VALUE: return "GDN_ERR_VALUE: scale or an epsilon not finite, or an epsilon < 0";
+    case GDN_ERR_VALUE: return "GDN_ERR_VALUE: scale or an epsilon not finite, an epsilon < 0, or a cache scale no power of two";
     }
     return "unknown gdn_status";
 }

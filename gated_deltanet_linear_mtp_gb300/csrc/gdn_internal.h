@@ -109,6 +109,83 @@ struct GatedNormParams {
     int num_slots;
 };
 
+// One step's block tables, slot map, positions and offsets from the lanes' lengths (gdn_page_plan.cu).
+struct PagePlanParams {
+    int B, N, page_size, max_pages, num_pages;
+    const int32_t* kv_lens;
+    const int32_t* new_lens;
+    int32_t* block_tables;  // [B, max_pages]
+    const int32_t* held;
+    const int32_t* free_pages;  // [num_pages]
+    const int32_t* taken;
+    int32_t* cu_seqlens;  // [B + 1]
+    int32_t* positions;   // [N]
+    int32_t* slot_map;    // [N]
+    int32_t* total_lens;  // [B]
+    int32_t* held_out;    // [B]; may be held
+    int32_t* taken_out;   // [1]; may be taken
+    int32_t* ticket;      // [1]: 0 between calls
+    int32_t* err;
+};
+
+// The paged 4-bit cache as the kernels see it (gdn_kv4.cuh): codes [num_pages, 2, HK, page_size, D / 2], scales
+// [num_pages, 2, HK, page_size, D / 16].
+struct Kv4 {
+    uint8_t* codes;
+    uint8_t* scales;
+    int num_pages, page_size, HK, D;
+    float k_scale, v_scale;
+};
+
+// Norm and rotation of query and key heads, and the store of keys and values into the cache (gdn_qk_norm_rope.cu).
+struct QkNormRopeParams {
+    int N, HQ, HK, D, R, interleaved;
+    int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+    float eps;
+    const void* q;
+    const void* k;
+    const void* v;  // nullptr: no store
+    const float* qw;
+    const float* kw;
+    const int32_t* positions;
+    const float* inv_freq;
+    void* q_out;
+    void* k_out;  // nullptr: keys go to the cache alone
+    const int32_t* slot_map;
+    Kv4 kv;
+    int32_t* err;
+};
+
+struct Kv4ReadParams {
+    int N;
+    const int32_t* slot_map;
+    void* k_out;
+    void* v_out;
+    Kv4 kv;
+    int32_t* err;
+};
+
+// Attention over the cache (gdn_kv4_attention.cu).
+struct Kv4AttentionParams {
+    int B, N, T, HQ, G, max_pages;  // T: most tokens of a lane; G: query heads per key head
+    const void* q;
+    const int32_t* cu_seqlens;  // nullptr: T tokens a lane
+    const int32_t* block_tables;
+    const int32_t* kv_lens;
+    void* o;
+    float* lse;  // nullable
+    void* workspace;
+    float scale;
+    Kv4 kv;
+    int32_t* err;
+};
+
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s);
+cudaError_t launch_qk_norm_rope(const QkNormRopeParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t s);
+cudaError_t launch_kv4_attention(const Kv4AttentionParams& p, cudaStream_t s);
+int64_t kv4_attention_workspace(int B, int T, int HQ, int HK, int D);
+
 cudaError_t launch_recurrent_f32state(const RecurrentParams& p, int B, int DK, bool qkv_bf16, cudaStream_t s);
 // A verify without intermediate states on a bf16 pool runs the chunked tensor-core kernel (which can also apply
 // the gated norm when DV <= 128) when this holds.

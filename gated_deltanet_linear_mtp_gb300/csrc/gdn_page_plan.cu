@@ -1,0 +1,182 @@
+// gdn_page_plan.cu -- block tables, slot map, positions and offsets of one step's tokens from the lanes' lengths.
+//
+//     need_b = max(0, ceil((kv_len_b + new_b) / P) - held_b)        pages lane b still wants
+//     upto_b = need_0 + .. + need_b;  lane b gets them (in this order) while taken + upto_b <= the free list's length
+//     table[b, held_b + i] = free_pages[taken + upto_b - need_b + i]
+//     slot(token at position x of lane b) = table[b, x / P] * P + x % P
+//
+// Latency bound: a step's lengths and tokens are a few KB to a few MB.  So one launch does everything: every CTA scans
+// all lanes' lengths by itself (B values from L2; cheaper than a second launch or a wait between CTAs) and then writes
+// its own slice of the lanes' tables and of the tokens, finding a token's lane by binary search in shared memory.  A
+// new page is taken from the free list directly, so no CTA reads what another one writes; held and taken, which the
+// caller may update in place, are written by the last CTA to finish, after all have read them.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 512;
+
+struct LaneNeed {
+    int64_t add;   // tokens this lane has in the packed order
+    int64_t need;  // pages it wants
+    bool ok;       // its lengths are in range
+};
+
+__device__ __forceinline__ LaneNeed lane_need(const PagePlanParams& p, int b) {
+    LaneNeed r;
+    const int64_t old = p.kv_lens[b], add = p.new_lens[b], held = p.held[b];
+    r.add = add > 0 ? add : 0;
+    r.ok = old >= 0 && add >= 0 && held >= 0 && held <= p.max_pages &&
+           old + add <= (int64_t)p.max_pages * p.page_size && held * p.page_size >= old;
+    const int64_t want = (old + add + p.page_size - 1) / p.page_size - held;
+    r.need = r.ok && want > 0 ? want : 0;
+    return r;
+}
+
+// sums over the CTA before this thread (exclusive), and over all of it
+__device__ void block_scan2(int64_t& a, int64_t& b, int64_t& sum_a, int64_t& sum_b, int64_t* sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t xa = a, xb = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t ya = __shfl_up_sync(~0u, xa, o), yb = __shfl_up_sync(~0u, xb, o);
+        if (lane >= o) xa += ya, xb += yb;
+    }
+    if (lane == 31) sh[2 * warp] = xa, sh[2 * warp + 1] = xb;
+    __syncthreads();
+    int64_t pa = 0, pb = 0;
+    sum_a = sum_b = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) pa = sum_a, pb = sum_b;
+        sum_a += sh[2 * w], sum_b += sh[2 * w + 1];
+    }
+    a = pa + xa - a;
+    b = pb + xb - b;
+}
+
+__global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams p) {
+    extern __shared__ int32_t smem[];
+    __shared__ int64_t scan_sh[2 * kThreads / 32];
+    __shared__ int last;
+    int32_t* cu = smem;             // [B + 1] first token of each lane
+    int32_t* from = smem + p.B + 1;  // [B] place of its first new page in the free list; -1: the lane gets none
+    const int tid = threadIdx.x;
+    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    const int64_t taken0 = p.taken[0];
+    const bool list_ok = taken0 >= 0 && taken0 <= p.num_pages;
+    const int64_t base = list_ok ? taken0 : 0, left = list_ok ? p.num_pages - taken0 : 0;
+
+    int64_t toks = 0, pages = 0;
+    for (int b = b0; b < b1; ++b) {
+        const LaneNeed n = lane_need(p, b);
+        toks += n.add;
+        pages += n.need;
+    }
+    int64_t all_toks, all_pages;
+    block_scan2(toks, pages, all_toks, all_pages, scan_sh);
+    uint32_t bits = list_ok ? 0u : (uint32_t)GDN_ERRBIT_INDEX;
+    if (all_toks > p.N) bits |= GDN_ERRBIT_SEQLEN;
+    for (int b = b0; b < b1; ++b) {
+        const LaneNeed n = lane_need(p, b);
+        const bool got = n.ok && (n.need == 0 || pages + n.need <= left);
+        cu[b] = (int32_t)min(toks, (int64_t)INT32_MAX);
+        from[b] = got ? (int32_t)(base + pages) : -1;
+        if (!n.ok) bits |= GDN_ERRBIT_SEQLEN;
+        else if (!got) bits |= GDN_ERRBIT_PAGES;
+        toks += n.add;
+        pages += n.need;
+    }
+    if (tid == 0) cu[p.B] = (int32_t)min(all_toks, (int64_t)INT32_MAX);
+    __syncthreads();
+
+    const int gsize = gridDim.x * kThreads, gtid = blockIdx.x * kThreads + tid;
+    // lanes: offsets, lengths, new table entries (a warp a lane: its new pages side by side)
+    for (int b = gtid; b <= p.B; b += gsize) {
+        p.cu_seqlens[b] = cu[b];
+        if (b < p.B) p.total_lens[b] = from[b] >= 0 ? p.kv_lens[b] + p.new_lens[b] : p.kv_lens[b];
+    }
+    for (int b = gtid >> 5; b < p.B; b += gsize >> 5) {
+        if (from[b] < 0) continue;
+        const int need = (int)lane_need(p, b).need, held = p.held[b];
+        for (int i = tid & 31; i < need; i += 32)
+            p.block_tables[(int64_t)b * p.max_pages + held + i] = p.free_pages[from[b] + i];
+    }
+    // tokens
+    const int64_t total = cu[p.B];
+    for (int64_t t = gtid; t < p.N; t += gsize) {
+        int32_t pos = 0, slot = -1;
+        if (t < total) {
+            int lo = 0, hi = p.B;  // the last lane whose first token is <= t: lanes without tokens are passed over
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            pos = (int32_t)((uint32_t)p.kv_lens[lo] + (uint32_t)(t - cu[lo]));
+            if (from[lo] >= 0) {
+                const int col = pos / p.page_size, held = p.held[lo];
+                const int page = col < held ? p.block_tables[(int64_t)lo * p.max_pages + col]
+                                            : p.free_pages[from[lo] + col - held];
+                if (page >= 0 && page < p.num_pages) slot = page * p.page_size + pos % p.page_size;
+                else bits |= GDN_ERRBIT_INDEX;
+            }
+        }
+        p.positions[t] = pos;
+        p.slot_map[t] = slot;
+    }
+    if (bits && p.err) atomicOr(p.err, (int32_t)bits);
+
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        last = gridDim.x == 1 || atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    // every CTA has read held and taken: they may be updated in place now
+    int64_t most = 0;
+    int64_t run = 0;
+    for (int b = b0; b < b1; ++b) {
+        const LaneNeed n = lane_need(p, b);
+        if (from[b] >= 0 && n.need > 0) run = from[b] - base + n.need;
+        p.held_out[b] = p.held[b] + (from[b] >= 0 ? (int32_t)n.need : 0);
+    }
+    most = run;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const int64_t y = __shfl_xor_sync(~0u, most, o);
+        most = y > most ? y : most;
+    }
+    if ((tid & 31) == 0) scan_sh[tid >> 5] = most;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 0; w < kThreads / 32; ++w) most = scan_sh[w] > most ? scan_sh[w] : most;
+        p.taken_out[0] = (int32_t)(taken0 + most);
+        if (gridDim.x > 1) *p.ticket = 0;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s) {
+    const size_t smem = ((size_t)2 * p.B + 1) * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(gdn_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    // a CTA for 2048 tokens or 128 lanes: fewer leave its threads with several dependent lookups each, more only
+    // repeat the scan
+    const int64_t want = ((int64_t)p.N + 2047) / 2048, lanes = (p.B + 127) / 128;
+    const int grid = (int)(want > lanes ? (want < 152 ? want : 152) : (lanes < 152 ? lanes : 152));
+    gdn_page_plan_kernel<<<grid, kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -77,14 +77,15 @@ typedef enum gdn_status {
     GDN_ERR_SHAPE = 2,       /* a size is out of range or inconsistent (HV % HK, T range, ...) */
     GDN_ERR_DTYPE = 3,       /* a dtype code is not a gdn_dtype */
     GDN_ERR_ALIGN = 4,       /* a pointer is misaligned */
-    GDN_ERR_UNSUPPORTED = 5, /* a valid but unsupported configuration (DK not in {16,32,64,128,256}) */
+    GDN_ERR_UNSUPPORTED = 5, /* a valid but unsupported configuration (DK not in {16,32,64,128,256}; D not in {64,128,256}) */
     GDN_ERR_CUDA = 6,        /* the kernel launch failed */
-    GDN_ERR_VALUE = 7        /* a scalar is not finite, or l2_eps < 0 */
+    GDN_ERR_VALUE = 7        /* a scalar is not finite, an epsilon < 0, or a cache scale no power of two */
 } gdn_status;
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 
-enum { GDN_ERRBIT_INDEX = 1, GDN_ERRBIT_ACCEPT_LEN = 2, GDN_ERRBIT_TIMEOUT = 4, GDN_ERRBIT_SEQLEN = 8 };
+enum { GDN_ERRBIT_INDEX = 1, GDN_ERRBIT_ACCEPT_LEN = 2, GDN_ERRBIT_TIMEOUT = 4, GDN_ERRBIT_SEQLEN = 8,
+       GDN_ERRBIT_PAGES = 16, GDN_ERRBIT_NONFINITE = 32 };
 
 enum { GDN_MAX_T = 16 }; /* tokens per call: decode (T >= 1), verify up to 16 (the page's MTP beyond T > 4) */
 
@@ -338,6 +339,124 @@ GDN_API gdn_status gdn_in_proj_conv(const gdn_conv_dims* dims, const void* x, co
 GDN_API gdn_status gdn_conv_commit(const gdn_conv_dims* dims, void* conv_state, const int32_t* state_indices,
                                    const void* records, const int32_t* accept_len, int32_t* err_word,
                                    gdn_stream_t stream);
+
+/*
+ * The softmax-attention layers that a hybrid model runs between its Gated DeltaNet layers, over a paged 4-bit K/V cache
+ * (the NVFP4 K/V cache of TensorRT-LLM PR #20937, GB300 Qwen3.8-Flash-Next NVFP4).  One step of such a layer:
+ *     gdn_page_plan (once a step)  ->  gdn_qk_norm_rope with the cache  ->  gdn_kv4_attention
+ * and gdn_kv4_read gives cached rows back as numbers.  The common rules above hold; a token whose slot is -1 is skipped.
+ *
+ * The cache of one layer: page_size tokens a page, keys (0) and values (1) of every key head,
+ *     codes   [num_pages, 2, HK, page_size, D / 2]   bytes: dimensions 2j (lower half) and 2j + 1 of byte j, e2m1
+ *     scales  [num_pages, 2, HK, page_size, D / 16]  bytes: one e4m3 scale for each 16 dimensions
+ * and a number is code * scale * k_scale (v_scale).  A token's slot is page * page_size + its place in the page.
+ */
+typedef struct gdn_kv4_cache {
+    void* codes;       /* 16-byte aligned */
+    void* scales;      /* 16-byte aligned */
+    int32_t num_pages; /* >= 1; num_pages * page_size < 2^31 */
+    int32_t page_size; /* 16, 32, 64, 128 or 256 */
+    int32_t HK;        /* key heads, 1 .. 1024 */
+    int32_t D;         /* head dimension: 64, 128 or 256 */
+    float k_scale;     /* a power of two, 2^-32 .. 2^32 (1.0) */
+    float v_scale;
+} gdn_kv4_cache;
+
+/* What gdn_page_plan writes; device memory, int32. */
+typedef struct gdn_page_plan_out {
+    int32_t* cu_seqlens; /* [B + 1]: lane b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the step's */
+    int32_t* positions;  /* [N]: 0 beyond the step's tokens */
+    int32_t* slot_map;   /* [N]: -1 beyond them, and for lanes without pages */
+    int32_t* total_lens; /* [B]: kv_lens + new_lens; kv_lens where the lane got no pages */
+    int32_t* held;       /* [B]: pages of each lane after the step; may be the input */
+    int32_t* taken;      /* [1]: pages taken from the free list after the step; may be the input */
+} gdn_page_plan_out;
+
+/*
+ * gdn_page_plan -- block tables, slot map, positions and offsets of a step's tokens, from the lanes' lengths.
+ *     need_b = max(0, ceil((kv_lens[b] + new_lens[b]) / page_size) - held[b]),  upto_b = need_0 + .. + need_b
+ * Lane b gets pages free_pages[taken + upto_b - need_b ..] into block_tables[b, held[b] ..] while taken + upto_b <=
+ * num_pages (a lane that needs none always goes on); the others keep their tables, their tokens get slot -1 and
+ * GDN_ERRBIT_PAGES is set.  held may be more than the cached tokens fill (pages of rejected drafts).  A lane whose lengths
+ * are negative, beyond max_pages pages or (cached) beyond its held pages is skipped likewise, with GDN_ERRBIT_SEQLEN; a
+ * step of more than N tokens sets that bit too, and its tokens beyond N are not written.  A page outside
+ * 0 .. num_pages - 1 gives slot -1 and GDN_ERRBIT_INDEX.  block_tables [B, max_pages], free_pages [num_pages].  ticket:
+ * one int32, 0 before the first call and left 0, used by one call at a time.  B 0 .. 8192.
+ */
+GDN_API gdn_status gdn_page_plan(int32_t B, int32_t N, int32_t page_size, int32_t max_pages, int32_t num_pages,
+                                 const int32_t* kv_lens, const int32_t* new_lens, int32_t* block_tables,
+                                 const int32_t* held, const int32_t* free_pages, const int32_t* taken,
+                                 const gdn_page_plan_out* out, int32_t* ticket, int32_t* err_word,
+                                 gdn_stream_t stream);
+
+typedef struct gdn_qk_dims {
+    int32_t N;           /* tokens */
+    int32_t HQ;          /* query heads, 1 .. 1024 */
+    int32_t HK;          /* key heads, 1 .. 1024 */
+    int32_t D;           /* head dimension: 64, 128 or 256 */
+    int32_t R;           /* rotated dimensions: the first R of D, a multiple of 16, 0 .. D */
+    int32_t interleaved; /* pairs (2i, 2i + 1) if 1, (i, i + R / 2) if 0 */
+    int32_t dtype;       /* gdn_dtype of q, k, v and of the outputs */
+    int64_t q_stride;    /* elements from one token of q to the next: >= HQ * D, a multiple of 16 bytes */
+    int64_t k_stride;    /* >= HK * D, likewise */
+    int64_t v_stride;    /* >= HK * D, likewise */
+    float eps;           /* finite, >= 0 */
+} gdn_qk_dims;
+
+/*
+ * gdn_qk_norm_rope -- RMS norm of every query and key head and the position rotation, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight
+ *     (y_a, y_b) = (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = positions[n] * inv_freq[i]
+ * q [N, HQ, D], k [N, HK, D] with their strides; q_weight, k_weight [D] fp32; positions [N] int32; inv_freq [R / 2] fp32
+ * (read only if R > 0); q_out [N, HQ, D], k_out [N, HK, D] without gaps, which may be q and k themselves where those have
+ * none.  With a cache, k (after norm and rotation, not rounded in between) and v [N, HK, D] are stored at slot_map[n]
+ * ([N] int32; -1 stores nothing): for each 16 dimensions the scale e4m3(max|x| / 6 / k_scale), to nearest even and at
+ * most 448, and the codes e2m1(x / (scale * k_scale)), to nearest even and at most 6.  The keys' codes are those of the
+ * exact value whatever the rounding of the sums.  k_out may then be NULL.  NaN is stored as 0 and an infinity as the largest number,
+ * and GDN_ERRBIT_NONFINITE is set; a slot below -1 or beyond the pages sets GDN_ERRBIT_INDEX and stores nothing.  Tokens of
+ * one call have distinct slots.  v, slot_map and cache go together (all or none NULL).  All tensors on 16 bytes, positions
+ * and slot_map on 4.
+ */
+GDN_API gdn_status gdn_qk_norm_rope(const gdn_qk_dims* dims, const void* q, const void* k, const float* q_weight,
+                                    const float* k_weight, const int32_t* positions, const float* inv_freq,
+                                    void* q_out, void* k_out, const void* v, const gdn_kv4_cache* cache,
+                                    const int32_t* slot_map, int32_t* err_word, gdn_stream_t stream);
+
+/* gdn_kv4_read -- the cached rows of N slots as bf16: k_out, v_out [N, HK, D] (exact while k_scale and v_scale leave the
+ * numbers in bf16's range).  Rows of slot -1 stay as they are. */
+GDN_API gdn_status gdn_kv4_read(const gdn_kv4_cache* cache, int32_t N, const int32_t* slot_map, void* k_out,
+                                void* v_out, int32_t* err_word, gdn_stream_t stream);
+
+typedef struct gdn_kv4_attention_dims {
+    int32_t B;         /* lanes, 0 .. 65535 */
+    int32_t N;         /* rows of q and o: tokens of all lanes; N * HQ < 2^31 */
+    int32_t max_q;     /* most tokens of a lane, >= 1 */
+    int32_t HQ;        /* query heads, a multiple of the cache's HK, HQ / HK <= 64 */
+    int32_t max_pages; /* columns of block_tables, >= 1; max_pages * page_size < 2^31 */
+    float scale;       /* multiplies q . k (1 / sqrt(D)) */
+} gdn_kv4_attention_dims;
+
+/*
+ * gdn_kv4_attention -- causal attention of each lane's tokens over its cached pages: token t of lane b (of n_b) sees keys
+ * 0 .. kv_lens[b] - n_b + t, its own key among them (the step's keys are stored before), query head h the key head
+ * h / (HQ / HK).
+ *     o = sum_j p_j v_j / sum_j p_j,  lse = log sum_j exp(scale q . k_j)
+ * q, o [N, HQ, D] bf16 on 16 bytes; lse [N, HQ] fp32 or NULL; cu_seqlens [B + 1] or NULL (then N = B * max_q and lane b
+ * holds rows b * max_q ..); kv_lens [B]: cached tokens, the step's included; block_tables [B, max_pages] (entries beyond a
+ * lane's tokens are not read).  A token that sees no key gets o = 0 and lse = -inf.  Softmax statistics and sums are fp32.  Bounds that are negative,
+ * decreasing, longer than max_q or beyond N, and a kv_len outside 0 .. max_pages * page_size, skip the lane
+ * (GDN_ERRBIT_SEQLEN; its rows stay as they are); the keys and values of a page outside the cache count as zeros
+ * (GDN_ERRBIT_INDEX).  workspace: at least gdn_kv4_attention_workspace bytes on 16 bytes, used by one call at a time; its
+ * contents need not be kept.
+ */
+GDN_API gdn_status gdn_kv4_attention(const gdn_kv4_attention_dims* dims, const gdn_kv4_cache* cache, const void* q,
+                                     const int32_t* cu_seqlens, const int32_t* block_tables, const int32_t* kv_lens,
+                                     void* o, float* lse, void* workspace, int64_t workspace_bytes, int32_t* err_word,
+                                     gdn_stream_t stream);
+
+/* Workspace bytes of gdn_kv4_attention on the current device for calls of up to B lanes and max_q tokens a lane; -1 if a
+ * size is out of range. */
+GDN_API int64_t gdn_kv4_attention_workspace(int32_t B, int32_t max_q, int32_t HQ, int32_t HK, int32_t D);
 
 /* Static string naming a status; never NULL. */
 GDN_API const char* gdn_status_string(gdn_status status);
