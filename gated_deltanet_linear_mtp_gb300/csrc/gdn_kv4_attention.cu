@@ -6,67 +6,72 @@
 // The T tokens and the G = HQ / HK query heads of one key head are the rows of one product: row r is token r / G, head
 // r % G, so the cached keys and values are read once for all of them.  An item is (lane, row tile, key head).
 //
-// Bound: the cache's 9/16 byte a number from HBM while an item has up to 16 rows; beyond that the tensor cores' rate for
-// mma.sync (600 TFLOP/s measured).  Nothing is dequantised into memory: the packed tiles go to shared memory by
-// cp.async (a pipeline of kStages tiles of 128 tokens), and each lane unpacks the codes of its own MMA fragments
-// (cvt e2m1x2 -> f16x2, one multiply by the group's scale; both exact).  The products' summation index may be permuted
-// freely, which makes the fragments contiguous in storage:
-//   * S = Q K^T: lane (n, c) of a warp (n = lane / 4, c = lane % 4) supplies token n's dimensions; k step s takes
-//     dimensions 4s .. 4s + 3 of the lane's own contiguous run, so one 16-byte load feeds 8 k steps.
-//   * O = P V: lane (g, c) supplies dimension run g (D / 8 contiguous dimensions) of 4 tokens; column g of output tile i
-//     is dimension g * D / 8 + i.  A pair of tokens is interleaved nibble by nibble before the conversion, so the f16x2
-//     pairs come out as the MMA wants them, and their two scales multiply as one f16x2.
-// P stays in registers: the accumulator layout of S is the A layout of P V.  Queries are scaled to f16 by a power of two
-// a row (exact but for values 2^-14 below the row's largest); P is rounded to f16 (half a step 2^-12 of a value in
-// 0 .. 1, well below the bf16 rounding of o), the sums l are those of the unrounded P in fp32, as all statistics are.
+// Bound: the cache's 9/16 byte a number from HBM, and close behind it the issue slots of the unpacking (two conversions'
+// worth of instructions a pair of numbers); with 32 rows and more the tensor cores' rate for mma.sync (600 TFLOP/s
+// measured).  Nothing is dequantised into memory: one warp brings packed tiles of 128 tokens into shared memory by TMA
+// (swizzled, a pipeline of kStages), and each lane of the others unpacks the codes of its own MMA fragments (cvt
+// e2m1x2 -> f16x2, one multiply by the group's scale; both exact).  Keys and values are the M operand and the rows are N:
+// N goes by 8, so a decode's 8 rows waste nothing.  The products' summation index may be permuted freely, which makes the
+// fragments contiguous in storage:
+//   * S^T = K Q^T: lane (g, c) of a warp (g = lane / 4, c = lane % 4) supplies tokens g and g + 8 of a tile of 16; k step s
+//     takes dimensions 4s .. 4s + 3 of the lane's own contiguous run, so one 16-byte load feeds 8 k steps.
+//   * O^T = V^T P^T: lane (g, c) supplies dimension run g (D / 8 contiguous dimensions) of 4 tokens; rows g and g + 8 of
+//     output tile i are dimensions 2i and 2i + 1 of that run.  A pair of tokens is interleaved nibble by nibble before the
+//     conversion, so the f16x2 pairs come out as the MMA wants them, and their two scales multiply as one f16x2.
+// P goes from accumulator to operand layout by one movmatrix for each 8 x 8.  Queries are scaled to f16 by a power of two
+// a row (exact but for values 2^-14 below the row's largest); P is rounded to f16 (half a step 2^-11 of a value, well
+// below the bf16 rounding of o), the sums l are those of the unrounded P in fp32, as all statistics are.  The running
+// maximum is moved only where a score passes it by more than 8 (in units of log 2): until then p is at most 2^8, which f16
+// and fp32 hold as well as 1, and the step needs no exchange between lanes.
 //
 // Work split: all tiles of all items are numbered item by item and each CTA takes an equal run of them, so one long lane
 // fills the GPU as well as many short ones.  A run ends in an item's middle on most CTAs: such parts (m, l, O in fp32) go
 // to the workspace, two at most a CTA, and a second kernel, launched programmatically behind the first, joins them in
-// order.  The four warps of a CTA take 32 tokens each of a tile, or with more than kMT * 16 rows half the warps take
-// other rows.
+// order.  The four warps of a CTA take 32 tokens each of a tile and join their parts in shared memory.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "gdn_common.cuh"
 #include "gdn_kv4.cuh"
+#include "gdn_tcgen05.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // a score may pass the running maximum by 2^kSlack before that moves
 
-// MT: m16 row tiles of a warp; WR: warps side by side along the rows; the other kWarps / WR share a tile's tokens
-template <int D_, int MT_, int WR_>
+// NR: groups of 8 rows of an item; W: warps that compute (one of four more copies, and those four give their registers to
+// the others: LREG a thread at launch, then CREG and PREG); WT: tokens of a warp's step; TILE: tokens of a
+// tile; STAGES: tiles in the pipeline; CTAS: of an SM, at least
+template <int D_, int NR_, int W_, int WT_, int TILE_, int STAGES_, int CTAS_>
 struct Cfg {
-    static constexpr int D = D_, MT = MT_, WR = WR_, WK = kWarps / WR;
-    static constexpr int ROWS = 16 * MT * WR;      // of an item
-    static constexpr int WT = D == 256 ? 16 : 32;  // tokens of a warp's step
-    static constexpr int KT = 128;                 // tokens of a tile
-    static constexpr int STEPS = KT / (WT * WK);   // steps of a warp in a tile
-    static constexpr int STAGES = D == 256 ? 2 : 3;
+    static constexpr int D = D_, NR = NR_, W = W_, WT = WT_, TILE = TILE_, STAGES = STAGES_, CTAS = CTAS_;
+    static constexpr int ROWS = 8 * NR, THREADS = 32 * (W + 4), STEPS = TILE / W / WT;
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a token's codes and scales
-    static constexpr int STAGE = 2 * KT * (CB + SB);
-    static constexpr int QFRAG = ROWS / 16 * (D / 16) * 512;  // Q as MMA fragments
-    static constexpr int MERGE = WK * ROWS * D * 4;           // the warps' O before they are joined
-    static constexpr int POOL = STAGES * STAGE > MERGE ? STAGES * STAGE : MERGE;
-    static constexpr int SMEM = POOL + QFRAG + WK * ROWS * 8 + ROWS * 4;
-    static_assert(STEPS * WT * WK == KT, "tile split");
+    static constexpr int STAGE = 2 * TILE * (CB + SB);
+    static constexpr bool QREG = D / 8 * NR <= 32;  // Q's fragments stay in registers
+    static constexpr int QBYTES = ROWS * D * 2;
+    static constexpr int OROW = D + 4;  // floats of a row while the warps' parts are joined
+    static constexpr int MERGE = W * 8 * OROW * 4;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + QBYTES + MERGE + W * 64 + ROWS * 4;
+    static constexpr int LREG = CTAS == 1 ? 168 : 80, CREG = CTAS == 1 ? 232 : 104, PREG = CTAS == 1 ? 40 : 32;
+    static_assert(W == 8 && 2 * CREG + PREG <= 3 * LREG, "the block's registers");
+    static_assert(STEPS * W * WT == TILE && TILE % 128 == 0 && WT % 16 == 0, "tile split");
 };
 
-// Byte offset of 16-byte chunk c of token row r in a tile of codes: chunks XORed so that the fragment loads of K (rows
-// 2j, 2j+1 together) and of V (rows 0, 3, 4, 7 or 1, 2, 5, 6 together) meet no bank twice
+// Byte offset of 16-byte chunk c of token row r in a tile of codes, as TMA's swizzle of the row's size leaves it
 template <int D>
 __device__ __forceinline__ int code_off(int r, int c) {
-    if (D == 64) return r * 32 + c * 16;
-    if (D == 128) return r * 64 + ((c ^ (((r >> 2) & 1) << 1)) << 4);
-    return r * 128 + ((c ^ (((r & 1) << 2) ^ (((r >> 2) & 1) << 1))) << 4);
+    if (D == 64) return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+    if (D == 128) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return r * 128 + ((c ^ (r & 7)) << 4);
 }
 
 // A part's place in the workspace: O [rows][D], then m, l [rows]
@@ -82,179 +87,242 @@ struct PartDesc {
     int32_t pad[3];
 };
 
-struct Item {
-    int b, rt, hk;
-    int q0, qlen, kv;  // the lane's first row in q, tokens, cached tokens
+struct Lane {
+    int q0, qlen, kv;  // first row in q, tokens (0: nothing to do), cached tokens
 };
 
-// One lane's extent; qlen 0: nothing to do
-__device__ __forceinline__ void lane_extent(const Kv4AttentionParams& p, int b, int& q0, int& qlen, int& kv, uint32_t& bits) {
+__device__ __forceinline__ Lane lane_extent(const Kv4AttentionParams& p, int b, uint32_t& bits) {
     int64_t a = (int64_t)b * p.T, n = p.T;
     if (p.cu_seqlens) {
         a = p.cu_seqlens[b];
         n = (int64_t)p.cu_seqlens[b + 1] - a;
     }
-    kv = p.kv_lens[b];
-    q0 = (int)a;
-    qlen = (int)n;
-    if (a < 0 || n < 0 || n > p.T || a + n > p.N || kv < 0 || kv > (int64_t)p.max_pages * p.kv.page_size) {
+    Lane x{(int)a, (int)n, p.kv_lens[b]};
+    if (a < 0 || n < 0 || n > p.T || a + n > p.N || x.kv < 0 || x.kv > (int64_t)p.max_pages * p.kv.page_size) {
         bits |= GDN_ERRBIT_SEQLEN;
-        qlen = 0;
+        x.qlen = 0;
     }
+    return x;
 }
 
 template <typename C>
-__global__ void __launch_bounds__(kThreads) gdn_kv4_attention_kernel(Kv4AttentionParams p) {
-    constexpr int D = C::D, MT = C::MT, KT = C::KT, WT = C::WT;
-    constexpr int KS = D / 16;          // k steps of S
-    constexpr int NT = WT / 8;          // token groups of 8
-    constexpr int DT = D / 8;           // output tiles of 8 columns
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_scan[kThreads + 1];
+__device__ __forceinline__ int tiles_of(int kv) {
+    return kv > 0 ? (kv - 1) / C::TILE + 1 : 1;
+}
+
+template <typename C>
+__device__ __forceinline__ int64_t lane_tiles(const Kv4AttentionParams& p, const Lane& x) {
+    return ((int64_t)x.qlen * p.G + C::ROWS - 1) / C::ROWS * tiles_of<C>(x.kv) * p.kv.HK;
+}
+
+// The run of tiles of CTA c among `all`; the CTA that holds tile u
+__device__ __forceinline__ int64_t run_begin(int64_t all, int64_t ctas, int64_t c) { return all * c / ctas; }
+__device__ __forceinline__ int cta_of(int64_t all, int64_t ctas, int64_t u) {
+    int64_t z = u * ctas / all;
+    while (run_begin(all, ctas, z + 1) <= u) ++z;
+    while (run_begin(all, ctas, z) > u) --z;
+    return (int)z;
+}
+
+// One piece of a CTA's run: tiles kt0 .. kt1 - 1 of an item
+struct Piece {
+    int b, hk, r0, kt0, kt1, kts;
+    Lane x;
+};
+
+// Walks a CTA's run of tiles u .. u1 - 1; lane `b` holds tile `base` first
+template <typename C>
+struct Walk {
+    int64_t u, u1, base;
+    int b;
+    __device__ __forceinline__ bool next(const Kv4AttentionParams& p, Piece& y) {
+        if (u >= u1) return false;
+        uint32_t ignored = 0;
+        y.x = lane_extent(p, b, ignored);
+        int64_t n = lane_tiles<C>(p, y.x);
+        while (base + n <= u) {
+            base += n;
+            y.x = lane_extent(p, ++b, ignored);
+            n = lane_tiles<C>(p, y.x);
+        }
+        y.b = b;
+        y.kts = tiles_of<C>(y.x.kv);
+        const int64_t in = u - base;
+        const int item = (int)(in / y.kts);
+        y.kt0 = (int)(in - (int64_t)item * y.kts);
+        y.hk = item % p.kv.HK;
+        y.r0 = item / p.kv.HK * C::ROWS;
+        y.kt1 = (int)min((int64_t)y.kts, y.kt0 + (u1 - u));
+        u += y.kt1 - y.kt0;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// The copying warp: tiles of the run, page by page; lane i takes page i of a tile
+template <typename C>
+__device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUtensorMap* map, Walk<C> walk, uint32_t pool,
+                                        uint8_t* pool_p, uint32_t full, uint32_t empty, uint32_t& bits) {
+    const int lane = threadIdx.x & 31, P = p.kv.page_size, HK = p.kv.HK;
+    const int PR = P < C::TILE ? P : C::TILE;  // rows of a copy
+    uint32_t it = 0;
+    bool late = false;
+    Piece y;
+    while (!late && walk.next(p, y)) {
+        const int32_t* table = p.block_tables + (int64_t)y.b * p.max_pages;
+        auto entry = [&](int kt) {  // this lane's page of tile kt
+            const int tok = kt * C::TILE + lane * PR;
+            return kt < y.kt1 && lane * PR < C::TILE && tok < y.x.kv ? table[tok / P] : -2;
+        };
+        int pg = entry(y.kt0);
+        for (int kt = y.kt0; kt < y.kt1; ++kt, ++it) {
+            const int ahead = entry(kt + 1);
+            const uint32_t s = it % C::STAGES, round = it / C::STAGES;
+            if (round > 0 && !mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, GDN_WAIT_POLLS)) {
+                bits |= GDN_ERRBIT_TIMEOUT;
+                late = true;
+                break;
+            }
+            const uint32_t st = pool + s * C::STAGE, bar = full + 8 * s;
+            const bool here = pg != -2, ok = here && (uint32_t)pg < (uint32_t)p.kv.num_pages;
+            if (here && !ok) {  // a page outside the cache: zeros
+                bits |= GDN_ERRBIT_INDEX;
+                uint8_t* z = pool_p + s * C::STAGE;
+                for (int i = 0; i < 2; ++i) {
+                    for (int j = 0; j < PR * C::CB; j += 16)
+                        *reinterpret_cast<uint4*>(z + (i * C::TILE + lane * PR) * C::CB + j) = make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < PR * C::SB; j += 16)
+                        *reinterpret_cast<uint4*>(z + 2 * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB + j) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            const uint32_t n = __popc(__ballot_sync(~0u, ok));
+            if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)(2 * PR * (C::CB + C::SB)));
+            __syncwarp();
+            if (ok) {
+                const int off = (kt * C::TILE) & (P - 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    tma_load_4d(st + (i * C::TILE + lane * PR) * C::CB, map, 0, off, i * HK + y.hk, pg, bar);
+                    const int64_t row = (((int64_t)pg * 2 + i) * HK + y.hk) * P + off;
+                    bulk_g2s(st + 2 * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB, p.kv.scales + row * C::SB,
+                             (uint32_t)(PR * C::SB), bar);
+                }
+            }
+            pg = ahead;
+        }
+    }
+    // no copy outlives the CTA
+    for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
+        mbar_wait_bounded(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, GDN_WAIT_POLLS);
+}
+
+template <typename C>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(const __grid_constant__ Kv4AttentionParams p,
+                                                                     const __grid_constant__ CUtensorMap map) {
+    constexpr int D = C::D, NR = C::NR, WT = C::WT;
+    constexpr int KS = D / 16;   // k steps of S
+    constexpr int NT = WT / 8;   // groups of 8 tokens of a step
+    constexpr int DT = D / 16;   // output tiles of 16 dimensions
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t s_scan[C::THREADS + 1];
+    __shared__ int64_t s_warp[C::W + 4];
+    __shared__ uint64_t s_bar[2 * C::STAGES];
+    __shared__ int s_dead;
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* pool = smem;
-    uint4* s_q = reinterpret_cast<uint4*>(smem + C::POOL);
-    float2* s_ml = reinterpret_cast<float2*>(smem + C::POOL + C::QFRAG);             // [WK][ROWS]
-    float* s_sc = reinterpret_cast<float*>(smem + C::POOL + C::QFRAG + C::WK * C::ROWS * 8);  // [ROWS]
+    uint4* s_q = reinterpret_cast<uint4*>(smem + C::STAGES * C::STAGE);
+    float* s_o = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::QBYTES);  // [C::W][8][OROW]
+    float2* s_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(s_o) + C::MERGE);  // [C::W][8]
+    float* s_sc = reinterpret_cast<float*>(s_ml + C::W * 8);                             // [ROWS]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int wr = warp % C::WR, wk = warp / C::WR;
-    const uint32_t pool_u = smem_u32(pool);
+    const uint32_t full = smem_u32(s_bar), empty = full + 8 * C::STAGES;
     uint32_t bits = 0;
-    float* parts = reinterpret_cast<float*>(reinterpret_cast<PartDesc*>(p.workspace) + gridDim.x);
-    const int HK = p.kv.HK, P = p.kv.page_size, pshift = 31 - __clz(P);
 
     // ---- this CTA's run of tiles --------------------------------------------------------------------------
-    const int per = (p.B + kThreads - 1) / kThreads;
-    auto lane_tiles = [&](int b) -> int64_t {
-        int q0, qlen, kv;
-        lane_extent(p, b, q0, qlen, kv, bits);
-        const int64_t rts = ((int64_t)qlen * p.G + C::ROWS - 1) / C::ROWS;
-        const int64_t kts = kv > 0 ? (kv + KT - 1) / KT : 1;
-        return rts * kts * HK;
-    };
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, C::W);
+        }
+        fence_mbar_init();
+        s_dead = 0;
+    }
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
     {
-        int64_t mine = 0;
-        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) mine += lane_tiles(b);
-        int64_t x = mine;
+        int64_t x = 0;
+        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) x += lane_tiles<C>(p, lane_extent(p, b, bits));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(~0u, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) s_scan[kThreads - 3 + warp] = x;  // the last places are free until the sums are in
+        if (lane == 31) s_warp[warp] = x;
         __syncthreads();
-        int64_t before = 0;
-        for (int w = 0; w < warp; ++w) before += s_scan[kThreads - 3 + w];
-        __syncthreads();
-        s_scan[tid + 1] = before + x;
+        for (int w = 0; w < warp; ++w) x += s_warp[w];
+        s_scan[tid + 1] = x;
         if (tid == 0) s_scan[0] = 0;
         __syncthreads();
     }
-    const int64_t all = s_scan[kThreads];
-    const int64_t ctas = all < gridDim.x ? all : gridDim.x;
-    const int64_t u0 = blockIdx.x < ctas ? all * blockIdx.x / ctas : all, u1 = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : all;
+    const int64_t all = s_scan[C::THREADS], ctas = all < gridDim.x ? all : gridDim.x;
     PartDesc* desc = reinterpret_cast<PartDesc*>(p.workspace) + blockIdx.x;
+    float* parts = reinterpret_cast<float*>(reinterpret_cast<PartDesc*>(p.workspace) + gridDim.x);
     if (tid == 0) desc->last = -1;
     if (bits && p.err && blockIdx.x == 0) atomicOr(p.err, (int32_t)bits);
     bits = 0;
-
-    int b = 0;
-    int64_t base = 0;  // first tile of lane b
-    if (u0 < u1) {
-        int lo = 0, hi = kThreads;
+    if (blockIdx.x >= ctas) return;
+    Walk<C> walk;
+    walk.u = run_begin(all, ctas, blockIdx.x);
+    walk.u1 = run_begin(all, ctas, (int64_t)blockIdx.x + 1);
+    {
+        int lo = 0, hi = C::THREADS;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (s_scan[mid] <= u0) lo = mid;
+            if (s_scan[mid] <= walk.u) lo = mid;
             else hi = mid;
         }
-        b = lo * per;
-        base = s_scan[lo];
+        walk.b = lo * per;
+        walk.base = s_scan[lo];
     }
-    for (int64_t u = u0; u < u1;) {
-        // the item that holds tile u
-        int64_t n = lane_tiles(b);
-        while (base + n <= u) {
-            base += n;
-            n = lane_tiles(++b);
-        }
-        int q0, qlen, kv;
-        lane_extent(p, b, q0, qlen, kv, bits);
-        const int kts = kv > 0 ? (kv + KT - 1) / KT : 1;
-        const int64_t in = u - base;
-        const int item = (int)(in / kts), kt0 = (int)(in - (int64_t)item * kts);
-        const int hk = item % HK, rt = item / HK, r0 = rt * C::ROWS;
-        const int nrows = min(C::ROWS, qlen * p.G - r0);
-        const int kt1 = (int)min((int64_t)kts, kt0 + (u1 - u));
-        const int64_t u_item = u - kt0;  // the item's first tile
-        const int32_t* table = p.block_tables + (int64_t)b * p.max_pages;
+    if (warp >= C::W) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::PREG));
+        if (warp > C::W) return;
+        produce<C>(p, &map, walk, smem_u32(pool), pool, full, empty, bits);
+        if (bits && p.err) atomicOr(p.err, (int32_t)bits);
+        return;
+    }
 
-        // ---- the pipeline of tiles: thread i copies chunks of the token rows i / (CB / 16) + k * ROWSTEP -------
-        constexpr int CPR = C::CB / 16, RSTEP = kThreads / CPR, NR = KT / RSTEP;  // chunks of a row; rows a pass; passes
-        constexpr int SCH = KT * C::SB / 16;                                      // chunks of a tile's K (or V) scales
-        const int crow = tid / CPR, cch = tid % CPR;
-        auto page_of = [&](int tok) -> int {
-            if (tok >= kv) return -1;
-            const int pg = table[tok >> pshift];
-            if ((uint32_t)pg >= (uint32_t)p.kv.num_pages) {
-                bits |= GDN_ERRBIT_INDEX;
-                return -1;
-            }
-            return pg;
-        };
-        int pg[NR], spg[2];
-        auto fetch_pages = [&](int kt) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i) pg[i] = kt < kt1 ? page_of(kt * KT + crow + i * RSTEP) : -1;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int ch = tid + i * kThreads;
-                const int tok = kt * KT + (ch % SCH) * (16 / C::SB);
-                spg[i] = ch < 2 * SCH && kt < kt1 ? page_of(tok) : -1;
-            }
-        };
-        auto issue = [&](int kt) {  // from the pages that fetch_pages(kt) found
-            if (kt < kt1) {
-                const uint32_t st = pool_u + (uint32_t)((kt - kt0) % C::STAGES) * C::STAGE;
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    const int r = crow + i * RSTEP, off = (kt * KT + r) & (P - 1);
-                    const int64_t row = ((int64_t)max(pg[i], 0) * 2 * HK + hk) * P + off;
-                    const uint8_t* src = p.kv.codes + row * C::CB + cch * 16;
-                    const uint32_t n16 = pg[i] >= 0 ? 16u : 0u;
-                    cp_async16(st + code_off<D>(r, cch), src, n16);
-                    cp_async16(st + KT * C::CB + code_off<D>(r, cch), src + (int64_t)HK * P * C::CB, n16);
-                }
-#pragma unroll
-                for (int i = 0; i < (2 * SCH + kThreads - 1) / kThreads; ++i) {
-                    const int ch = tid + i * kThreads;
-                    if (ch < 2 * SCH) {
-                        const int which = ch / SCH, r = (ch % SCH) * (16 / C::SB), off = (kt * KT + r) & (P - 1);
-                        const int64_t row = (((int64_t)max(spg[i], 0) * 2 + which) * HK + hk) * P + off;
-                        // tokens that end inside the chunk leave zero scales behind them, whatever the page holds
-                        const int n = spg[i] >= 0 ? min(16, (kv - kt * KT - r) * C::SB) : 0;
-                        cp_async16(st + 2 * KT * C::CB + ch * 16, p.kv.scales + row * C::SB, (uint32_t)n);
-                    }
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int s = 0; s < C::STAGES - 1; ++s) {
-            fetch_pages(kt0 + s);
-            issue(kt0 + s);
-        }
-        fetch_pages(kt0 + C::STAGES - 1);
-
-        // ---- Q as f16 fragments in shared memory, each row scaled by a power of two -----------------------------
-        for (int r = warp; r < C::ROWS; r += kWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::CREG));
+    uint32_t it = 0;
+    bool dead = false;
+    Piece y;
+    while (walk.next(p, y)) {
+        const int nrows = min(C::ROWS, y.x.qlen * p.G - y.r0);
+        // ---- Q as f16 fragments in shared memory, each row scaled by a power of two ---------------------------
+        for (int r = warp; r < C::ROWS; r += C::W) {
             float x[D / 32];
             float top = 0.f;
+            const int t = (y.r0 + r) / p.G, h = y.hk * p.G + (y.r0 + r) - t * p.G;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 uint32_t w = 0;
-                if (r < nrows) {
-                    const int t = (r0 + r) / p.G, h = hk * p.G + (r0 + r) - t * p.G;
-                    w = *reinterpret_cast<const uint32_t*>((const __nv_bfloat16*)p.q + ((int64_t)(q0 + t) * p.HQ + h) * D + i * 64 + lane * 2);
-                }
+                if (r < nrows)
+                    w = *reinterpret_cast<const uint32_t*>((const __nv_bfloat16*)p.q + ((int64_t)(y.x.q0 + t) * p.HQ + h) * D +
+                                                           i * 64 + lane * 2);
                 x[2 * i] = __uint_as_float(w << 16);
                 x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
                 top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
@@ -268,194 +336,221 @@ __global__ void __launch_bounds__(kThreads) gdn_kv4_attention_kernel(Kv4Attentio
             if (lane == 0) s_sc[r] = up * p.scale * p.kv.k_scale * kLog2e;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
-                // dimension d is part of lane c's run: for D 128 c = d / 32 and k step (d % 32) / 4; for 64 runs of 16;
+                // dimension d belongs to lane c's run: for D 128 c = d / 32 and k step (d % 32) / 4; for 64 runs of 16;
                 // for 256 two halves of 128
                 const int d = i * 64 + lane * 2;
                 constexpr int RUN = D == 64 ? 16 : 32;
                 const int half = D == 256 ? d >> 7 : 0, dd = D == 256 ? d & 127 : d;
                 const int cc = dd / RUN, ks = half * (RUN / 4) + (dd % RUN) / 4, pair = (dd % 4) / 2;
-                const int mt = r / 16, rr = r % 16;
-                // fragment words: a0 (row g, pair 0), a1 (row g + 8, pair 0), a2 (row g, pair 1), a3 (row g + 8, pair 1)
-                uint32_t* f = reinterpret_cast<uint32_t*>(s_q + (mt * KS + ks) * 32 + (rr % 8) * 4 + cc);
-                f[pair * 2 + rr / 8] = f16x2_bits(x[2 * i] * down, x[2 * i + 1] * down);
+                uint32_t* f = reinterpret_cast<uint32_t*>(s_q + (r / 8 * (KS / 2) + ks / 2) * 32 + (r % 8) * 4 + cc);
+                f[(ks & 1) * 2 + pair] = f16x2_bits(x[2 * i] * down, x[2 * i + 1] * down);
             }
         }
-        __syncthreads();
-
-        float o[MT][DT][4], m[MT][2], l[MT][2], sc[MT][2];
-        int limit[MT][2];
+        named_sync(1, C::W * 32);
+        uint32_t qf[C::QREG ? NR : 1][C::QREG ? KS : 1][2];
+        if constexpr (C::QREG) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int i = 0; i < KS / 2; ++i) {
+                    const uint4 v = s_q[(n * (KS / 2) + i) * 32 + lane];
+                    qf[n][2 * i][0] = v.x, qf[n][2 * i][1] = v.y, qf[n][2 * i + 1][0] = v.z, qf[n][2 * i + 1][1] = v.w;
+                }
+        }
+        // rows 2c and 2c + 1 of each group of 8
+        float o[DT][NR][4], m[NR][2], l[NR][2], sc[NR][2];
+        int limit[NR][2];  // keys that the row sees
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = (wr * MT + mt) * 16 + h * 8 + g;
-                m[mt][h] = -INFINITY;
-                l[mt][h] = 0.f;
-                sc[mt][h] = s_sc[r];
-                limit[mt][h] = kv - qlen + (r0 + r) / p.G + 1;  // keys that the row sees
-#pragma unroll
-                for (int i = 0; i < DT; ++i) o[mt][i][2 * h] = o[mt][i][2 * h + 1] = 0.f;
+                const int r = n * 8 + 2 * c + h;
+                m[n][h] = -INFINITY;
+                l[n][h] = 0.f;
+                sc[n][h] = s_sc[r];
+                limit[n][h] = y.x.kv - y.x.qlen + (y.r0 + r) / p.G + 1;
             }
-        const int all_see = kv - qlen + r0 / p.G + 1;  // keys that every row sees
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+        }
+        const int all_see = y.x.kv - y.x.qlen + y.r0 / p.G + 1;  // keys that every row sees
 
-        for (int kt = kt0; kt < kt1; ++kt) {
-            cp_async_wait<C::STAGES - 2>();
-            __syncthreads();
-            issue(kt + C::STAGES - 1);
-            fetch_pages(kt + C::STAGES);
-            const uint8_t* st = pool + (size_t)((kt - kt0) % C::STAGES) * C::STAGE;
-            const uint8_t *kc = st, *vc = st + KT * C::CB, *ksc = st + 2 * KT * C::CB, *vsc = ksc + KT * C::SB;
+        for (int kt = y.kt0; kt < y.kt1; ++kt, ++it) {
+            const uint32_t stage = it % C::STAGES;
+            if (!dead && !mbar_wait_bounded(full + 8 * stage, (it / C::STAGES) & 1, GDN_WAIT_POLLS)) {
+                dead = true;
+                bits |= GDN_ERRBIT_TIMEOUT;
+                s_dead = 1;
+            }
+            const uint8_t* st = pool + stage * C::STAGE;
+            const uint8_t *kc = st, *vc = st + C::TILE * C::CB, *ksc = st + 2 * C::TILE * C::CB, *vsc = ksc + C::TILE * C::SB;
 #pragma unroll 1
             for (int step = 0; step < C::STEPS; ++step) {
-                const int w0 = (step * C::WK + wk) * WT;  // the warp's first token in the tile
-                // S: token group j's column n is token j * 8 + (n ^ ((n >> 1) & 1))
-                float s[MT][NT][4];
+                const int w0 = (step * C::W + warp) * WT;  // the warp's first token in the tile
+                const int tok0 = kt * C::TILE + w0;
+                if (tok0 >= y.x.kv || dead) break;
+                // S^T: row g of token group j is token j * 8 + (g ^ ((g >> 1) & 1))
+                float s[NT / 2][NR][4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int j = 0; j < NT / 2; ++j)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[mt][j][i] = 0.f;
+                    for (int n = 0; n < NR; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.f;
+                constexpr int WN = D == 64 ? 2 : 4;
 #pragma unroll
                 for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-                    uint32_t w[NT][D == 64 ? 2 : 4], scl[NT][2];
+                    uint32_t w[NT][WN], scl[NT][2];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         const int r = w0 + j * 8 + (g ^ ((g >> 1) & 1));
                         if constexpr (D == 64) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(kc + r * 32 + c * 8);
-                            w[j][0] = v.x;
-                            w[j][1] = v.y;
-                            const uint32_t f = e4m3x2_to_f16(ksc[r * 4 + c] * 0x101u);
-                            scl[j][0] = scl[j][1] = f;
+                            const uint2 v = *reinterpret_cast<const uint2*>(kc + code_off<D>(r, c >> 1) + (c & 1) * 8);
+                            w[j][0] = v.x, w[j][1] = v.y;
+                            scl[j][0] = scl[j][1] = e4m3x2_to_f16(ksc[r * 4 + c] * 0x101u);
                         } else {
                             const uint4 v = *reinterpret_cast<const uint4*>(kc + code_off<D>(r, half * 4 + c));
-                            w[j][0] = v.x;
-                            w[j][1] = v.y;
-                            w[j][2] = v.z;
-                            w[j][3] = v.w;
-                            const uint32_t f = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(ksc + r * C::SB + half * 8 + c * 2));
+                            w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+                            const uint32_t f =
+                                e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(ksc + r * C::SB + half * 8 + c * 2));
                             scl[j][0] = __byte_perm(f, f, 0x1010);
                             scl[j][1] = __byte_perm(f, f, 0x3232);
                         }
                     }
-                    constexpr int WN = D == 64 ? 2 : 4;
 #pragma unroll
                     for (int i = 0; i < WN; ++i) {
-                        uint32_t a0[MT][4], a1[MT][4];
+                        uint32_t q[NR][4];  // two k steps
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const uint4* q = s_q + ((wr * MT + mt) * KS + half * 8 + 2 * i) * 32 + lane;
-                            const uint4 x = q[0], y = q[32];
-                            a0[mt][0] = x.x, a0[mt][1] = x.y, a0[mt][2] = x.z, a0[mt][3] = x.w;
-                            a1[mt][0] = y.x, a1[mt][1] = y.y, a1[mt][2] = y.z, a1[mt][3] = y.w;
+                        for (int n = 0; n < NR; ++n) {
+                            if constexpr (C::QREG) {
+                                const int ks = half * 8 + 2 * i;
+                                q[n][0] = qf[n][ks][0], q[n][1] = qf[n][ks][1], q[n][2] = qf[n][ks + 1][0], q[n][3] = qf[n][ks + 1][1];
+                            } else {
+                                const uint4 v = s_q[(n * (KS / 2) + half * 4 + i) * 32 + lane];
+                                q[n][0] = v.x, q[n][1] = v.y, q[n][2] = v.z, q[n][3] = v.w;
+                            }
                         }
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            uint32_t f[4];
-                            e2m1x8_to_f16(w[j][i], f);
-                            const uint32_t sf = scl[j][i / 2];
+                        for (int j = 0; j < NT / 2; ++j) {
+                            uint32_t fa[4], fb[4];
+                            e2m1x8_to_f16(w[2 * j][i], fa);
+                            e2m1x8_to_f16(w[2 * j + 1][i], fb);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], sf);
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                mma_f16(s[mt][j], a0[mt], f[0], f[1]);
-                                mma_f16(s[mt][j], a1[mt], f[2], f[3]);
+                            for (int x = 0; x < 4; ++x) {
+                                fa[x] = hmul2(fa[x], scl[2 * j][i / 2]);
+                                fb[x] = hmul2(fb[x], scl[2 * j + 1][i / 2]);
                             }
+                            const uint32_t a0[4] = {fa[0], fb[0], fa[1], fb[1]}, a1[4] = {fa[2], fb[2], fa[3], fb[3]};
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) mma_f16(s[j][n], a0, q[n][0], q[n][1]);
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) mma_f16(s[j][n], a1, q[n][2], q[n][3]);
                         }
                     }
                 }
-                // softmax in units of log 2
-                const int tok0 = kt * KT + w0;
-                uint32_t pf[MT][NT][2];
+                // softmax in units of log 2; s[j][n]: groups 2j (first two) and 2j + 1, rows 2c and 2c + 1
+                bool above = false;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float top[2] = {-INFINITY, -INFINITY};
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int j = 0; j < NT / 2; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int h = i >> 1, n = 2 * c + (i & 1);
-                            float x = s[mt][j][i] * sc[mt][h];
-                            if (tok0 + WT > all_see && tok0 + j * 8 + (n ^ (c & 1)) >= limit[mt][h]) x = -INFINITY;
-                            s[mt][j][i] = x;
-                            top[h] = fmaxf(top[h], x);
-                        }
+                        for (int i = 0; i < 4; ++i) s[j][n][i] *= sc[n][i & 1];
+                if (tok0 + WT > all_see) {
+                    const int tk = tok0 + (g ^ ((g >> 1) & 1));
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (tk + (2 * j + (i >> 1)) * 8 >= limit[n][i & 1]) s[j][n][i] = -INFINITY;
+                }
+                float top[NR][2];
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
-                        top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
+                        float x = fmaxf(s[0][n][h], s[0][n][2 + h]);
+#pragma unroll
+                        for (int j = 1; j < NT / 2; ++j) x = fmaxf(x, fmaxf(s[j][n][h], s[j][n][2 + h]));
+                        top[n][h] = x;
+                        above |= x > m[n][h] + kSlack;
                     }
-                    if (__any_sync(~0u, top[0] > m[mt][0] || top[1] > m[mt][1])) {
+                if (__any_sync(~0u, above)) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float mn = fmaxf(m[mt][h], top[h]);
-                            const float f = mn == -INFINITY ? 1.f : exp2_fast(m[mt][h] - mn);
-                            m[mt][h] = mn;
-                            l[mt][h] *= f;
+                            float x = top[n][h];
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                            const float mn = fmaxf(m[n][h], x);
+                            const float f = mn == -INFINITY ? 1.f : exp2_fast(m[n][h] - mn);
+                            m[n][h] = mn;
+                            l[n][h] *= f;
 #pragma unroll
                             for (int i = 0; i < DT; ++i) {
-                                o[mt][i][2 * h] *= f;
-                                o[mt][i][2 * h + 1] *= f;
+                                o[i][n][h] *= f;
+                                o[i][n][2 + h] *= f;
                             }
                         }
-                    }
+                }
+                uint32_t pf[NT][NR];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float mm = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
+                for (int n = 0; n < NR; ++n) {
+                    const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const float e0 = exp2_fast(s[mt][j][2 * h] - mm), e1 = exp2_fast(s[mt][j][2 * h + 1] - mm);
-                            l[mt][h] += e0 + e1;
-                            pf[mt][j][h] = f16x2_bits(e0, e1);
-                        }
+                    for (int j = 0; j < NT; ++j) {
+                        const float e0 = exp2_fast(s[j >> 1][n][(j & 1) * 2] - m0), e1 = exp2_fast(s[j >> 1][n][(j & 1) * 2 + 1] - m1);
+                        l[n][0] += e0;
+                        l[n][1] += e1;
+                        pf[j][n] = movmatrix(f16x2_bits(e0, e1));
                     }
                 }
-                // O += P V: 16 tokens at a time; this lane's tokens are 2c, 2c + 1 of two groups, swapped for odd c
+                // O^T += V^T P^T: 16 tokens at a time; this lane's tokens are 2c, 2c + 1 of two groups, swapped for odd c
+                const bool tail = tok0 + WT > y.x.kv;  // what lies behind the last token may be anything, NaN scales too
 #pragma unroll
                 for (int j = 0; j < NT; j += 2) {
-                    constexpr int WN = D / 64;  // words of a run of D / 8 dimensions
-                    uint32_t w[4][WN], sv[2][WN > 2 ? 2 : 1];
+                    constexpr int VN = D / 64;  // words of a run of D / 8 dimensions
+                    uint32_t w[4][VN], sv[2][VN > 2 ? 2 : 1];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = 2 * c + (i & 1), r = w0 + (j + (i >> 1)) * 8 + (n ^ (c & 1));
                         if constexpr (D == 64) {
-                            w[i][0] = *reinterpret_cast<const uint32_t*>(vc + r * 32 + g * 4);
+                            w[i][0] = *reinterpret_cast<const uint32_t*>(vc + code_off<D>(r, g >> 2) + (g & 3) * 4);
                         } else if constexpr (D == 128) {
                             const uint2 v = *reinterpret_cast<const uint2*>(vc + code_off<D>(r, g >> 1) + (g & 1) * 8);
-                            w[i][0] = v.x;
-                            w[i][1] = v.y;
+                            w[i][0] = v.x, w[i][1] = v.y;
                         } else {
                             const uint4 v = *reinterpret_cast<const uint4*>(vc + code_off<D>(r, g));
-                            w[i][0] = v.x;
-                            w[i][1] = v.y;
-                            w[i][2] = v.z;
-                            w[i][3] = v.w;
+                            w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int ra = w0 + (j + i) * 8 + ((2 * c) ^ (c & 1)), rb = w0 + (j + i) * 8 + ((2 * c + 1) ^ (c & 1));
+                        uint32_t x, z;
                         if constexpr (D == 256) {
-                            const uint32_t x = *reinterpret_cast<const uint16_t*>(vsc + ra * 16 + g * 2);
-                            const uint32_t y = *reinterpret_cast<const uint16_t*>(vsc + rb * 16 + g * 2);
-                            sv[i][0] = e4m3x2_to_f16(__byte_perm(x, y, 0x0040));
-                            sv[i][1] = e4m3x2_to_f16(__byte_perm(x, y, 0x0051));
+                            x = *reinterpret_cast<const uint16_t*>(vsc + ra * 16 + g * 2);
+                            z = *reinterpret_cast<const uint16_t*>(vsc + rb * 16 + g * 2);
                         } else {
                             const int gr = D == 64 ? g >> 1 : g;
-                            sv[i][0] = e4m3x2_to_f16((uint32_t)vsc[ra * C::SB + gr] | ((uint32_t)vsc[rb * C::SB + gr] << 8));
+                            x = vsc[ra * C::SB + gr];
+                            z = vsc[rb * C::SB + gr];
+                        }
+                        if (tail) {
+                            if (kt * C::TILE + ra >= y.x.kv) x = 0;
+                            if (kt * C::TILE + rb >= y.x.kv) z = 0;
+                        }
+                        if constexpr (D == 256) {
+                            sv[i][0] = e4m3x2_to_f16(__byte_perm(x, z, 0x0040));
+                            sv[i][1] = e4m3x2_to_f16(__byte_perm(x, z, 0x0051));
+                        } else {
+                            sv[i][0] = e4m3x2_to_f16(x | (z << 8));
                         }
                     }
-                    uint32_t pa[MT][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        pa[mt][0] = pf[mt][j][0];
-                        pa[mt][1] = pf[mt][j][1];
-                        pa[mt][2] = pf[mt][j + 1][0];
-                        pa[mt][3] = pf[mt][j + 1][1];
-                    }
-#pragma unroll
-                    for (int x = 0; x < WN; ++x) {
+                    for (int x = 0; x < VN; ++x) {
                         // bytes (token a, token b) of one dimension: even dimensions, then odd ones
                         uint32_t f[2][2][4];
 #pragma unroll
@@ -465,135 +560,157 @@ __global__ void __launch_bounds__(kThreads) gdn_kv4_attention_kernel(Kv4Attentio
                             e2m1x8_to_f16(((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u), f[i][1]);
                             const uint32_t sf = sv[i][D == 256 ? x / 2 : 0];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                f[i][0][y] = hmul2(f[i][0][y], sf);
-                                f[i][1][y] = hmul2(f[i][1][y], sf);
+                            for (int z = 0; z < 4; ++z) {
+                                f[i][0][z] = hmul2(f[i][0][z], sf);
+                                f[i][1][z] = hmul2(f[i][1][z], sf);
                             }
                         }
 #pragma unroll
-                        for (int y = 0; y < 8; ++y)
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t a[4] = {f[0][0][z], f[0][1][z], f[1][0][z], f[1][1][z]};
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-                                mma_f16(o[mt][x * 8 + y], pa[mt], f[0][y & 1][y >> 1], f[1][y & 1][y >> 1]);
+                            for (int n = 0; n < NR; ++n) mma_f16(o[x * 4 + z][n], a, pf[j][n], pf[j + 1][n]);
+                        }
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * stage);
         }
-        cp_async_wait<0>();
-        __syncthreads();
 
-        // ---- the warps' parts of the item joined, then stored ----------------------------------------------------
-        float* s_o = reinterpret_cast<float*>(pool);  // [WK][ROWS][D]
+        // ---- the warps' parts of the item joined, 8 rows at a time, and stored -----------------------------------
+        const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
+        float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
+        constexpr int RC = D / 32, CH = D / 4;  // 16-byte chunks of a run and of a row
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < NR; ++n) {
+            named_sync(1, C::W * 32);  // the rows before are read (and s_sc, the fragments of Q)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float x = l[mt][h];
-                x += __shfl_xor_sync(~0u, x, 1);
-                x += __shfl_xor_sync(~0u, x, 2);
-                const int r = (wr * MT + mt) * 16 + h * 8 + g;
-                if (c == 0) s_ml[wk * C::ROWS + r] = make_float2(m[mt][h], x);
-                float* dst = s_o + ((size_t)wk * C::ROWS + r) * D;
+                float x = l[n][h];
+                x += __shfl_xor_sync(~0u, x, 4);
+                x += __shfl_xor_sync(~0u, x, 8);
+                x += __shfl_xor_sync(~0u, x, 16);
+                if (g == 0) s_ml[warp * 8 + 2 * c + h] = make_float2(m[n][h], x);
+                // runs' chunks XORed with their lane so that the stores of different lanes meet few banks twice
+                float* dst = s_o + (warp * 8 + 2 * c + h) * C::OROW + g * (D / 8);
 #pragma unroll
-                for (int i = 0; i < DT; ++i) {
-                    dst[(2 * c) * (D / 8) + i] = o[mt][i][2 * h];
-                    dst[(2 * c + 1) * (D / 8) + i] = o[mt][i][2 * h + 1];
-                }
+                for (int i = 0; i < RC; ++i)
+                    *reinterpret_cast<float4*>(dst + ((i ^ (g & (RC < 4 ? RC - 1 : 3))) << 2)) =
+                        make_float4(o[2 * i][n][h], o[2 * i][n][2 + h], o[2 * i + 1][n][h], o[2 * i + 1][n][2 + h]);
             }
-        __syncthreads();
-        const bool whole = kt0 == 0 && kt1 == kts;
-        float* part = parts + ((int64_t)blockIdx.x * 2 + (kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
-        for (int r = warp; r < nrows; r += kWarps) {
-            float mm = -INFINITY, ll = 0.f, f[C::WK];
+            named_sync(1, C::W * 32);
+            if (s_dead) continue;
 #pragma unroll
-            for (int w = 0; w < C::WK; ++w) mm = fmaxf(mm, s_ml[w * C::ROWS + r].x);
+            for (int k = 0; k < (8 * CH + C::W * 32 - 1) / (C::W * 32); ++k) {
+                const int idx = tid + k * C::W * 32, rr = idx / CH, ch = idx % CH, r = n * 8 + rr;
+                if (rr >= 8 || r >= nrows) continue;
+                float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-            for (int w = 0; w < C::WK; ++w) {
-                const float2 x = s_ml[w * C::ROWS + r];
-                f[w] = mm == -INFINITY ? 1.f : exp2_fast(x.x - mm);
-                ll += x.y * f[w];
-            }
-            const int t = (r0 + r) / p.G, h = hk * p.G + (r0 + r) - t * p.G;
-            const int64_t out = (int64_t)(q0 + t) * p.HQ + h;
-            const float inv = ll > 0.f ? p.kv.v_scale / ll : ll != ll ? ll : 0.f;
+                for (int w = 0; w < C::W; ++w) mm = fmaxf(mm, s_ml[w * 8 + rr].x);
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int gg = ch / RC, j = ch % RC, at = gg * (D / 8) + ((j ^ (gg & (RC < 4 ? RC - 1 : 3))) << 2);
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const int d = i * 64 + lane * 2;
-                float a = 0.f, bb = 0.f;
-#pragma unroll
-                for (int w = 0; w < C::WK; ++w) {
-                    const float2 x = *reinterpret_cast<const float2*>(s_o + ((size_t)w * C::ROWS + r) * D + d);
-                    a = fmaf(x.x, f[w], a);
-                    bb = fmaf(x.y, f[w], bb);
+                for (int w = 0; w < C::W; ++w) {
+                    const float2 x = s_ml[w * 8 + rr];
+                    const float f = mm == -INFINITY ? 1.f : exp2_fast(x.x - mm);
+                    ll += x.y * f;
+                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * C::OROW + at);
+                    a.x = fmaf(v.x, f, a.x);
+                    a.y = fmaf(v.y, f, a.y);
+                    a.z = fmaf(v.z, f, a.z);
+                    a.w = fmaf(v.w, f, a.w);
                 }
                 if (whole) {
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(a * inv, bb * inv);
-                    *reinterpret_cast<__nv_bfloat162*>((__nv_bfloat16*)p.o + out * D + d) = y;
+                    const int t = (y.r0 + r) / p.G, h = y.hk * p.G + (y.r0 + r) - t * p.G;
+                    const int64_t out = (int64_t)(y.x.q0 + t) * p.HQ + h;
+                    const float inv = ll > 0.f ? p.kv.v_scale / ll : ll != ll ? ll : 0.f;
+                    *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + out * D + ch * 4) =
+                        make_uint2(bf16x2_bits(a.x * inv, a.y * inv), bf16x2_bits(a.z * inv, a.w * inv));
+                    if (p.lse && ch == 0) p.lse[out] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
                 } else {
-                    *reinterpret_cast<float2*>(part + (int64_t)r * D + d) = make_float2(a, bb);
-                }
-            }
-            if (lane == 0) {
-                if (whole) {
-                    if (p.lse) p.lse[out] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
-                } else {
-                    part[(int64_t)C::ROWS * D + 2 * r] = mm;
-                    part[(int64_t)C::ROWS * D + 2 * r + 1] = ll;
+                    *reinterpret_cast<float4*>(part + (int64_t)r * D + ch * 4) = a;
+                    if (ch == 0) *reinterpret_cast<float2*>(part + (int64_t)C::ROWS * D + 2 * r) = make_float2(mm, ll);
                 }
             }
         }
-        if (!whole && kt0 == 0 && tid == 0) {
-            // the CTA whose run holds the item's last tile
-            const int64_t end = u_item + kts - 1;
-            int64_t z = (end * ctas) / all;
-            while (all * (z + 1) / ctas <= end) ++z;
-            while (all * z / ctas > end) --z;
-            desc->last = (int32_t)z;
+        if (!whole && y.kt0 == 0 && tid == 0 && !s_dead) {
+            desc->last = cta_of(all, ctas, walk.u - (y.kt1 - y.kt0) + y.kts - 1);
             desc->rows = nrows;
-            desc->q0 = q0;
-            desc->r0 = r0;
-            desc->hk = hk;
+            desc->q0 = y.x.q0;
+            desc->r0 = y.r0;
+            desc->hk = y.hk;
         }
-        __syncthreads();
-        u += kt1 - kt0;
     }
     if (bits && p.err) atomicOr(p.err, (int32_t)bits);
 }
 
-// Joins the parts of the items that CTA x of the first kernel began and did not end: block (x, y) takes rows y, y + gridDim.y, ..
-template <typename C>
-__global__ void __launch_bounds__(kThreads) gdn_kv4_attention_join_kernel(Kv4AttentionParams p, int ctas) {
-    constexpr int D = C::D;
+// Joins the parts of items that more than one CTA worked on: block (x, y) takes rows y, y + gridDim.y, .. of the item that
+// CTA x began and did not end.  The four warps take every fourth part each; D / 4 threads (two rows' worth for D 64) cover
+// a row.
+constexpr int kJoinThreads = 128;
+constexpr int kMaxParts = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) gdn_kv4_attention_join_kernel(Kv4AttentionParams p, int rows_max, int ctas) {
+    __shared__ float s_f[kMaxParts];
+    __shared__ float s_red[2 * kJoinThreads / 32];
+    __shared__ float4 s_acc[kJoinThreads];
     grid_dependency_wait();
     const PartDesc d = reinterpret_cast<const PartDesc*>(p.workspace)[blockIdx.x];
     if (d.last < 0) return;
     const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const PartDesc*>(p.workspace) + ctas);
-    const int first = blockIdx.x, n = d.last - first + 1;
-    const int64_t step = part_floats(C::ROWS, D);
+    const int first = blockIdx.x, n = d.last - first + 1, tid = threadIdx.x;
+    const int64_t step = part_floats(rows_max, D);
+    auto part = [&](int i) { return parts + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * step; };
     for (int r = blockIdx.y; r < d.rows; r += gridDim.y) {
-        auto part = [&](int i) { return parts + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * step; };
         float mm = -INFINITY;
-        for (int i = 0; i < n; ++i) mm = fmaxf(mm, part(i)[(int64_t)C::ROWS * D + 2 * r]);
-        float ll = 0.f, a[(D + kThreads - 1) / kThreads] = {};
-        for (int i = 0; i < n; ++i) {
-            const float* q = part(i);
-            const float f = mm == -INFINITY ? 1.f : exp2_fast(q[(int64_t)C::ROWS * D + 2 * r] - mm);
-            ll = fmaf(q[(int64_t)C::ROWS * D + 2 * r + 1], f, ll);
+        for (int i = tid; i < n; i += kJoinThreads) mm = fmaxf(mm, part(i)[(int64_t)rows_max * D + 2 * r]);
 #pragma unroll
-            for (int k = 0; k < (D + kThreads - 1) / kThreads; ++k) {
-                const int x = threadIdx.x + k * kThreads;
-                if (x < D) a[k] = fmaf(q[(int64_t)r * D + x], f, a[k]);
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+        if ((tid & 31) == 0) s_red[tid >> 5] = mm;
+        __syncthreads();
+        mm = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+        float ll = 0.f;
+        for (int i = tid; i < n; i += kJoinThreads) {
+            const float2 x = *reinterpret_cast<const float2*>(part(i) + (int64_t)rows_max * D + 2 * r);
+            const float f = mm == -INFINITY ? 1.f : exp2_fast(x.x - mm);
+            s_f[i] = f;
+            ll = fmaf(x.y, f, ll);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(~0u, ll, o);
+        if ((tid & 31) == 0) s_red[4 + (tid >> 5)] = ll;
+        __syncthreads();
+        ll = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+        constexpr int TR = D / 4, GR = kJoinThreads / TR;  // threads of a row; parts side by side
+        const int ch = tid % TR, gr = tid / TR;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = gr; i < n; i += GR) {
+            const float4 v = *reinterpret_cast<const float4*>(part(i) + (int64_t)r * D + ch * 4);
+            const float f = s_f[i];
+            a.x = fmaf(v.x, f, a.x);
+            a.y = fmaf(v.y, f, a.y);
+            a.z = fmaf(v.z, f, a.z);
+            a.w = fmaf(v.w, f, a.w);
+        }
+        s_acc[tid] = a;
+        __syncthreads();
+        if (gr == 0) {
+#pragma unroll
+            for (int k = 1; k < GR; ++k) {
+                const float4 v = s_acc[k * TR + ch];
+                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
             }
+            const int t = (d.r0 + r) / p.G, h = d.hk * p.G + (d.r0 + r) - t * p.G;
+            const int64_t out = (int64_t)(d.q0 + t) * p.HQ + h;
+            const float inv = ll > 0.f ? p.kv.v_scale / ll : ll != ll ? ll : 0.f;
+            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + out * D + ch * 4) =
+                make_uint2(bf16x2_bits(a.x * inv, a.y * inv), bf16x2_bits(a.z * inv, a.w * inv));
+            if (ch == 0 && p.lse) p.lse[out] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
         }
-        const int t = (d.r0 + r) / p.G, h = d.hk * p.G + (d.r0 + r) - t * p.G;
-        const int64_t out = (int64_t)(d.q0 + t) * p.HQ + h;
-        const float inv = ll > 0.f ? p.kv.v_scale / ll : ll != ll ? ll : 0.f;
-#pragma unroll
-        for (int k = 0; k < (D + kThreads - 1) / kThreads; ++k) {
-            const int x = threadIdx.x + k * kThreads;
-            if (x < D) ((__nv_bfloat16*)p.o)[out * D + x] = __float2bfloat16_rn(a[k] * inv);
-        }
-        if (threadIdx.x == 0 && p.lse) p.lse[out] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+        __syncthreads();
     }
 }
 
@@ -604,54 +721,96 @@ int sm_count() {
     return sms;
 }
 
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 3;  // at most; as many as fit
+static_assert(kCtasPerSm * 200 <= kMaxParts, "parts of an item");
+
+// The codes as TMA sees them: [num_pages][2 HK][page_size][D / 2 bytes], copied by page (a tile at most)
+cudaError_t codes_map(const Kv4& kv, int tile, CUtensorMap* map) {
+    const EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t CB = (cuuint64_t)kv.D / 2, P = (cuuint64_t)kv.page_size;
+    const cuuint64_t dims[4] = {CB, P, (cuuint64_t)2 * kv.HK, (cuuint64_t)kv.num_pages};
+    const cuuint64_t strides[3] = {CB, CB * P, CB * P * 2 * kv.HK};
+    const cuuint32_t box[4] = {(cuuint32_t)CB, (cuuint32_t)(P < (cuuint64_t)tile ? P : (cuuint64_t)tile), 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle sw = kv.D == 64    ? CU_TENSOR_MAP_SWIZZLE_32B
+                                  : kv.D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                : CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kv.codes, dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// CTAs of an SM, found once for each kernel and device
+template <typename C>
+cudaError_t resident(int* n) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(gdn_kv4_attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, gdn_kv4_attention_kernel<C>, C::THREADS, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // the warps' registers are split anew in the kernel: the block has to hold what that sums up to
+    cudaFuncAttributes at{};
+    e = cudaFuncGetAttributes(&at, gdn_kv4_attention_kernel<C>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != C::LREG) return cudaErrorLaunchOutOfResources;
+    *n = *n < 1 ? 1 : *n > kCtasPerSm ? kCtasPerSm : *n;
+    if (dev < 64) known[dev].store(*n, std::memory_order_relaxed);
+    return cudaSuccess;
+}
 
 template <typename C>
 cudaError_t run(const Kv4AttentionParams& p, cudaStream_t s) {
     const int sms = sm_count();
     if (sms == 0) return cudaErrorNoDevice;
-    const int ctas = sms * kCtasPerSm;
-    cudaError_t e = cudaFuncSetAttribute(gdn_kv4_attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    int per = 0;
+    CUtensorMap map;
+    cudaError_t e = resident<C>(&per);
+    if (e == cudaSuccess) e = codes_map(p.kv, C::TILE, &map);
     if (e != cudaSuccess) return e;
-    gdn_kv4_attention_kernel<C><<<ctas, kThreads, C::SMEM, s>>>(p);
+    const int ctas = sms * per;
+    gdn_kv4_attention_kernel<C><<<ctas, C::THREADS, C::SMEM, s>>>(p, map);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas, C::ROWS < 8 ? C::ROWS : 8);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gdn_kv4_attention_join_kernel<C>, p, ctas);
+    return cudaLaunchKernelEx(&cfg, gdn_kv4_attention_join_kernel<C::D>, p, C::ROWS, ctas);
 }
 
-// Rows of an item: one m16 tile a warp while the lane's rows fit it, two up to 32 (a warp's unpacked fragments then serve
-// both); more rows go to other warps.  D = 256 keeps one (its O takes 128 registers a thread).
+// Rows of an item: the lane's rows, by 8, 16, 32 or 64, as far as O^T (D * rows / 32 registers a thread) leaves room; the
+// unpacked fragments of a tile then serve all of them
 int item_rows(int64_t rows, int D) {
-    if (rows <= 16) return 16;
-    if (rows <= 32) return 32;
-    return 64;
-}
-
-template <int D>
-cudaError_t run_d(const Kv4AttentionParams& p, int rows, cudaStream_t s) {
-    if constexpr (D == 256) {
-        return rows == 16 ? run<Cfg<256, 1, 1>>(p, s) : rows == 32 ? run<Cfg<256, 1, 2>>(p, s) : run<Cfg<256, 1, 4>>(p, s);
-    } else {
-        return rows == 16 ? run<Cfg<D, 1, 1>>(p, s) : rows == 32 ? run<Cfg<D, 2, 1>>(p, s) : run<Cfg<D, 2, 2>>(p, s);
-    }
+    const int most = D == 64 ? 64 : D == 128 ? 32 : 16;
+    int n = 8;
+    while (n < rows && n < most) n *= 2;
+    return n;
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_attention(const Kv4AttentionParams& p, cudaStream_t s) {
     const int rows = item_rows((int64_t)p.T * p.G, p.kv.D);
-    return p.kv.D == 64    ? run_d<64>(p, rows, s)
-           : p.kv.D == 128 ? run_d<128>(p, rows, s)
-                           : run_d<256>(p, rows, s);
+    switch (p.kv.D * 100 + rows) {
+    case 6408: return run<Cfg<64, 1, 8, 32, 256, 3, 2>>(p, s);
+    case 6416: return run<Cfg<64, 2, 8, 32, 256, 3, 2>>(p, s);
+    case 6432: return run<Cfg<64, 4, 8, 16, 128, 4, 1>>(p, s);
+    case 6464: return run<Cfg<64, 8, 8, 16, 128, 4, 1>>(p, s);
+    case 12808: return run<Cfg<128, 1, 8, 32, 256, 2, 2>>(p, s);
+    case 12816: return run<Cfg<128, 2, 8, 32, 256, 4, 1>>(p, s);
+    case 12832: return run<Cfg<128, 4, 8, 16, 128, 4, 1>>(p, s);
+    case 25608: return run<Cfg<256, 1, 8, 16, 128, 3, 1>>(p, s);
+    default: return run<Cfg<256, 2, 8, 16, 128, 3, 1>>(p, s);
+    }
 }
 
 int64_t kv4_attention_workspace(int B, int T, int HQ, int HK, int D) {
