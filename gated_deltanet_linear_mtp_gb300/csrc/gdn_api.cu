@@ -555,6 +555,7 @@ gdn_status gdn_qk_norm_rope(const gdn_qk_dims* dims, const void* q, const void* 
     if (dims->N == 0) return GDN_OK;
     if (!q || !k || !q_weight || !k_weight || !positions || !q_out || (!k_out && !store) || (dims->R > 0 && !inv_freq))
         return GDN_ERR_NULL;
+    if (store && k_out == k) return GDN_ERR_VALUE;  // a key row may be read once more after its k_out is written
     if (dims->q_stride * sz % 16 || dims->k_stride * sz % 16 || (store && dims->v_stride * sz % 16)) return GDN_ERR_ALIGN;
     for (const void* x : {q, k, (const void*)q_weight, (const void*)k_weight, (const void*)q_out, (const void*)k_out, v})
         if (!aligned(x, 16)) return GDN_ERR_ALIGN;

@@ -408,8 +408,8 @@ typedef struct gdn_qk_dims {
  *     y = x / sqrt(mean(x^2) + eps) * weight
  *     (y_a, y_b) = (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = positions[n] * inv_freq[i]
  * q [N, HQ, D], k [N, HK, D] with their strides; q_weight, k_weight [D] fp32; positions [N] int32; inv_freq [R / 2] fp32
- * (read only if R > 0); q_out [N, HQ, D], k_out [N, HK, D] without gaps, which may be q and k themselves where those have
- * none.  With a cache, k (after norm and rotation, not rounded in between) and v [N, HK, D] are stored at slot_map[n]
+ * (read only if R > 0); q_out [N, HQ, D], k_out [N, HK, D] without gaps, which may be q and (without a cache) k themselves
+ * where those have none.  With a cache, k (after norm and rotation, not rounded in between) and v [N, HK, D] are stored at slot_map[n]
  * ([N] int32; -1 stores nothing): for each 16 dimensions the scale e4m3(max|x| / 6 / k_scale), to nearest even and at
  * most 448, and the codes e2m1(x / (scale * k_scale)), to nearest even and at most 6.  The keys' codes are those of the
  * exact value whatever the rounding of the sums.  k_out may then be NULL.  NaN is stored as 0 and an infinity as the largest number,

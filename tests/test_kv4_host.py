@@ -60,7 +60,7 @@ def norm_rope(L, d=None, c=None, store=True, **ptr):
     base = dict(N=4, HQ=8, HK=2, D=128, R=64, interleaved=0, dtype=1, q_stride=1024, k_stride=256, v_stride=256, eps=1e-6)
     base.update(d or {})
     dims = gdn._QkDimsC(**base)
-    a = dict(q=P, k=P, qw=P, kw=P, pos=P, freq=P, qo=P, ko=P, v=P if store else None, slots=P if store else None, err=None)
+    a = dict(q=P, k=P, qw=P, kw=P, pos=P, freq=P, qo=P, ko=ctypes.c_void_p(0x20000), v=P if store else None, slots=P if store else None, err=None)
     a.update(ptr)
     cc = cache(**(c or {})) if store else None
     return L.gdn_qk_norm_rope(ctypes.byref(dims), a["q"], a["k"], a["qw"], a["kw"], a["pos"], a["freq"], a["qo"], a["ko"],
@@ -90,6 +90,11 @@ def test_norm_rope_without_a_cache(L):
     assert norm_rope(L, store=False, ko=None) == NULL
     assert norm_rope(L, store=False, v=P) == NULL
     assert norm_rope(L, dict(N=0), store=False) == OK
+
+
+def test_keys_are_not_stored_from_where_they_are_overwritten(L):
+    other = ctypes.c_void_p(0x30000)
+    assert norm_rope(L, k=other, ko=other) == VALUE
 
 
 @pytest.mark.parametrize("kw,status", BAD_CACHES)
