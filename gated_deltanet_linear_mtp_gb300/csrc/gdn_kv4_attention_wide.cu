@@ -1,0 +1,568 @@
+// gdn_kv4_attention_wide.cu -- attention over the 4-bit cache for lanes of many rows (prompts): the same operation as
+// gdn_kv4_attention.cu, on the tensor cores of tcgen05.
+//
+// Bound: the products, 4 D flops a row and key.  An item is a tile of MT * 128 rows (whole tokens times the G heads of a key
+// head) of one lane and key head; a CTA takes its tiles of TILE keys in turn, as four kinds of warps:
+//   * one warp copies the packed tiles into shared memory by TMA (shared with the decode kernel);
+//   * a warpgroup unpacks them into f16 operand tiles (128-byte swizzle, a ring of three: K, V, K, ..), once for all rows: a
+//     number costs the unpacking 1/256 of its products;
+//   * one thread issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory;
+//   * a warpgroup for each 128 rows takes a row of S a thread, forms P in place of S as f16 and keeps the row's statistics.
+// With two tiles of rows the softmax of one runs while the tensor cores work on the other.  The running maximum moves only
+// where a score passes it by more than 2^8 (then that thread scales its row of O in tensor memory, which waits for
+// nothing: the S it holds was committed after the product that last wrote O), so O stays in tensor memory throughout.
+// Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16, fp32.
+//
+// Work split: all tiles of all items are numbered and each CTA (one an SM) takes an equal run of them, since the rows of a
+// prompt see anything from few to all keys and items of whole rows leave SMs idle at the end; parts are joined by the decode
+// kernel's second launch.
+#include <atomic>
+
+#include "gdn_kv4_attention.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 512;  // 4 warpgroups: softmax, softmax or unpacking, unpacking, MMA and copies
+constexpr int kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kLaunchRegs = 128, kSoftRegs = 176, kUnpackRegs = 104, kRestRegs = 56;
+static_assert(2 * kSoftRegs + kUnpackRegs + kRestRegs <= 4 * kLaunchRegs, "the block's registers");
+constexpr int kRing = 3;
+
+template <int D_>
+struct Wide {
+    static constexpr int D = D_;
+    static constexpr int MT = D == 256 ? 1 : 2;        // tiles of 128 rows
+    static constexpr int TILE = D == 256 ? 64 : 128;   // keys of a tile
+    static constexpr int ROWS = MT * 128;
+    static constexpr int STAGES = 2;                   // of packed tiles
+    static constexpr int CB = D / 2, SB = D / 16, STAGE = 2 * TILE * (CB + SB);
+    static constexpr int UNPACK = 128 * (3 - MT);      // threads that unpack
+    static constexpr int QBYTES = 128 * D * 2, KVBYTES = TILE * D * 2;
+    static constexpr int Q_AT = 0, RING_AT = MT * QBYTES, POOL_AT = RING_AT + kRing * KVBYTES;
+    static constexpr int SMEM = 1024 + POOL_AT + STAGES * STAGE;
+    static constexpr int O_COL = 0, S_COL = MT * D, COLS = 512;
+    static_assert(S_COL + MT * TILE <= COLS, "tensor memory");
+};
+
+// instruction descriptor of tcgen05.mma kind::f16 with f16 operands, D fp32
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* f) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* w) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]),
+        "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]),
+        "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
+        : "memory");
+}
+
+// ---- the run of tiles: pairs (lane, row tile), each with a tile of keys for every key head ------------------------
+template <typename C>
+__device__ __forceinline__ int row_tiles(const Kv4AttentionParams& p, const Lane& x) {
+    const int tt = C::ROWS / p.G;  // tokens of a row tile
+    return (x.qlen + tt - 1) / tt;
+}
+
+// Tiles of keys that row tile rt of a lane sees
+template <typename C>
+__device__ __forceinline__ int key_tiles(const Kv4AttentionParams& p, const Lane& x, int rt) {
+    const int64_t end = min((int64_t)(rt + 1) * (C::ROWS / p.G), (int64_t)x.qlen);
+    const int64_t keys = x.kv - x.qlen + end;
+    return keys > 0 ? (int)((keys - 1) / C::TILE + 1) : 1;
+}
+
+template <typename C>
+struct WideWalk {
+    int64_t u, u1, base;  // base: first tile of pair (b, rt)
+    int b, rt;
+    __device__ __forceinline__ bool next(const Kv4AttentionParams& p, Piece& y) {
+        if (u >= u1) return false;
+        uint32_t ignored = 0;
+        y.x = lane_extent(p, b, ignored);
+        for (;;) {
+            const int rts = row_tiles<C>(p, y.x);
+            if (rt >= rts) {
+                rt = 0;
+                y.x = lane_extent(p, ++b, ignored);
+                continue;
+            }
+            y.kts = key_tiles<C>(p, y.x, rt);
+            if (base + (int64_t)y.kts * p.kv.HK > u) break;
+            base += (int64_t)y.kts * p.kv.HK;
+            ++rt;
+        }
+        y.b = b;
+        const int64_t in = u - base;
+        y.hk = (int)(in / y.kts);
+        y.kt0 = (int)(in - (int64_t)y.hk * y.kts);
+        y.r0 = rt * (C::ROWS / p.G) * p.G;
+        y.kt1 = (int)min((int64_t)y.kts, y.kt0 + (u1 - u));
+        u += y.kt1 - y.kt0;
+        return true;
+    }
+};
+
+// Sum over the threads before this one, and over all, of a number each
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_warp, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t z = __shfl_up_sync(~0u, y, o);
+        if (lane >= o) y += z;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = y;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    return before + y - x;
+}
+
+// The lane and row tile of pair i; s_pairs[t]: pairs before the lanes of thread t (`per` lanes each)
+template <typename C>
+__device__ void locate(const Kv4AttentionParams& p, const int64_t* s_pairs, int per, int64_t i, int& b, int& rt) {
+    int lo = 0, hi = kThreads;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_pairs[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    uint32_t ignored = 0;
+    int64_t at = s_pairs[lo];
+    b = lo * per;
+    for (;;) {
+        const int n = row_tiles<C>(p, lane_extent(p, b, ignored));
+        if (at + n > i) break;
+        at += n;
+        ++b;
+    }
+    rt = (int)(i - at);
+}
+
+template <typename C>
+__global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(const __grid_constant__ Kv4AttentionParams p,
+                                                                             const __grid_constant__ CUtensorMap map) {
+    constexpr int D = C::D, MT = C::MT, TILE = C::TILE;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t s_pairs[kThreads + 1], s_tiles[kThreads + 1], s_warp[kThreads / 32];
+    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kRing + 4 * MT];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_dead;
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t base_u = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8 * C::STAGES, kv_full = raw_empty + 8 * C::STAGES,
+                   kv_empty = kv_full + 8 * kRing, q_full = kv_empty + 8 * kRing, s_full = q_full + 8 * MT,
+                   p_full = s_full + 8 * MT, o_full = p_full + 8 * MT;
+    uint32_t bits = 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(raw_full + 8 * i, 1), mbar_init(raw_empty + 8 * i, C::UNPACK / 32);
+        for (int i = 0; i < kRing; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, 1);
+        for (int i = 0; i < MT; ++i) {
+            mbar_init(q_full + 8 * i, 4);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        fence_mbar_init();
+        s_dead = 0;
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), C::COLS);
+
+    // ---- this CTA's run of tiles --------------------------------------------------------------------------
+    WideWalk<C> walk;
+    int64_t all;
+    {
+        const int per = (p.B + kThreads - 1) / kThreads;
+        int64_t n = 0, pairs;
+        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) n += row_tiles<C>(p, lane_extent(p, b, bits));
+        s_pairs[tid] = block_scan(n, s_warp, pairs);
+        if (tid == 0) s_pairs[kThreads] = pairs;
+        __syncthreads();
+        const int64_t i0 = pairs * tid / kThreads, i1 = pairs * (tid + 1) / kThreads;
+        n = 0;
+        if (i0 < i1) {
+            int b, rt;
+            uint32_t ignored = 0;
+            locate<C>(p, s_pairs, per, i0, b, rt);
+            Lane x = lane_extent(p, b, ignored);
+            for (int64_t i = i0; i < i1; ++i, ++rt) {
+                while (rt >= row_tiles<C>(p, x)) {
+                    rt = 0;
+                    x = lane_extent(p, ++b, ignored);
+                }
+                n += key_tiles<C>(p, x, rt);
+            }
+        }
+        s_tiles[tid] = block_scan(n * p.kv.HK, s_warp, all);
+        if (tid == 0) s_tiles[kThreads] = all;
+        __syncthreads();
+        const int64_t ctas = all < gridDim.x ? all : gridDim.x;
+        walk.u = walk.u1 = 0;
+        if (blockIdx.x < ctas) {
+            walk.u = run_begin(all, ctas, blockIdx.x);
+            walk.u1 = run_begin(all, ctas, (int64_t)blockIdx.x + 1);
+            int lo = 0, hi = kThreads;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_tiles[mid] <= walk.u) lo = mid;
+                else hi = mid;
+            }
+            walk.base = s_tiles[lo];
+            locate<C>(p, s_pairs, per, pairs * lo / kThreads, walk.b, walk.rt);
+        }
+    }
+    const int64_t ctas = all < gridDim.x ? all : gridDim.x;
+    PartDesc* desc = reinterpret_cast<PartDesc*>(p.workspace) + blockIdx.x;
+    float* parts = reinterpret_cast<float*>(reinterpret_cast<PartDesc*>(p.workspace) + gridDim.x);
+    if (tid == 0) desc->last = -1;
+    if (bits && p.err && blockIdx.x == 0) atomicOr(p.err, (int32_t)bits);
+    bits = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* dead = &s_dead;
+    auto wait = [&](uint32_t bar, uint32_t parity) {  // false: it ran out, and the CTA's work with it
+        if (*dead) return false;
+        if (mbar_wait_bounded(bar, parity, GDN_WAIT_POLLS)) return true;
+        *dead = 1;
+        bits |= GDN_ERRBIT_TIMEOUT;
+        return false;
+    };
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, wait(bar, parity)) != 0; };
+
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+        if (warp == kLoadWarp) {
+            produce<C>(p, &map, walk, base_u + C::POOL_AT, smem + C::POOL_AT, raw_full, raw_empty, bits);
+        } else if (warp == kMmaWarp && lane == 0) {
+            // tiles go through the ring as K0, V0, K1, V1, ..; slot n of a piece sequence is ring place n % kRing
+            constexpr uint32_t id_s = idesc_f16(128, TILE), id_o = idesc_f16(128, D) | (1u << 16);
+            uint32_t slot = 0, piece[2] = {0, 0}, tile[2] = {0, 0};  // ring slots; pieces and tiles of each tile of rows
+            Piece y;
+            bool go = true;
+            auto ring_wait = [&](uint32_t n) { return wait(kv_full + 8 * (n % kRing), (n / kRing) & 1); };
+            // descriptors differ in their start address alone: 16 bytes count 1
+            const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT), k_desc = umma_desc_sw128(base_u + C::RING_AT),
+                           v_desc = umma_desc_sw128_mn(base_u + C::RING_AT, TILE * 128);
+            auto product_s = [&](uint32_t n, int m) {
+                const uint64_t q = q_desc + m * (C::QBYTES / 16), k = k_desc + (n % kRing) * (C::KVBYTES / 16);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    umma_bf16(tmem + C::S_COL + m * TILE, q + ((ks / 4) * 128 * 128 + (ks % 4) * 32) / 16,
+                              k + ((ks / 4) * TILE * 128 + (ks % 4) * 32) / 16, id_s, ks > 0);
+                umma_commit(s_full + 8 * m);
+            };
+            while (go && walk.next(p, y)) {
+                const int n = y.kt1 - y.kt0, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), mts = nrows > 128 ? MT : 1;
+                for (int m = 0; m < mts && go; ++m) go = wait(q_full + 8 * m, piece[m] & 1);
+                go = go && ring_wait(slot);
+                if (!go) break;
+                tc_fence_after();
+                for (int m = 0; m < mts; ++m) product_s(slot, m);
+                umma_commit(kv_empty + 8 * (slot % kRing));
+                ++slot;
+                for (int i = 0; i < n && go; ++i) {  // `slot` holds V of tile i, the next one K of tile i + 1
+                    const bool more = i + 1 < n;
+                    go = ring_wait(slot) && (!more || ring_wait(slot + 1));
+                    for (int m = 0; m < mts && go; ++m) {
+                        go = wait(p_full + 8 * m, (tile[m] + i) & 1);
+                        if (!go) break;
+                        tc_fence_after();
+                        const uint64_t v = v_desc + (slot % kRing) * (C::KVBYTES / 16);
+#pragma unroll
+                        for (int ks = 0; ks < TILE / 16; ++ks)
+                            umma_bf16_ta(tmem + C::O_COL + m * D, tmem + C::S_COL + m * TILE + ks * 8,
+                                         v + ks * (2048 / 16), id_o, i > 0 || ks > 0);
+                        if (more) product_s(slot + 1, m);
+                        else umma_commit(o_full + 8 * m);
+                    }
+                    if (!go) break;
+                    umma_commit(kv_empty + 8 * (slot % kRing));
+                    if (more) umma_commit(kv_empty + 8 * ((slot + 1) % kRing));
+                    slot += more ? 2 : 1;
+                }
+                for (int m = 0; m < mts; ++m) ++piece[m], tile[m] += n;
+            }
+        }
+    } else if (warp >= 4 * MT) {
+        // ---- unpacking: thread (row, part of its dimensions) -------------------------------------------------
+        if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kUnpackRegs));
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        constexpr int PARTS = C::UNPACK / TILE, RUN = D / PARTS;  // dimensions of a thread
+        const int idx = tid - 128 * MT, r = idx % TILE, part = idx / TILE;
+        uint32_t it = 0, slot = 0;
+        Piece y;
+        bool go = true;
+        while (go && walk.next(p, y)) {
+            for (int kt = y.kt0; kt < y.kt1 && go; ++kt, ++it) {
+                const uint32_t st = it % C::STAGES;
+                go = warp_wait(raw_full + 8 * st, (it / C::STAGES) & 1);
+                if (!go) break;
+                const uint8_t* raw = smem + C::POOL_AT + st * C::STAGE;
+                const bool real = kt * TILE + r < y.x.kv;  // what lies behind the last token may be anything
+#pragma unroll
+                for (int which = 0; which < 2; ++which, ++slot) {
+                    const uint32_t at = slot % kRing;
+                    if (slot >= kRing) go = go && warp_wait(kv_empty + 8 * at, (slot / kRing - 1) & 1);
+                    if (!go) break;
+                    uint8_t* dst = smem + C::RING_AT + at * C::KVBYTES;
+                    const uint8_t* codes = raw + which * TILE * C::CB;
+                    const uint8_t* sc = raw + 2 * TILE * C::CB + which * TILE * C::SB + r * C::SB + part * (RUN / 16);
+#pragma unroll
+                    for (int c = 0; c < RUN / 32; ++c) {
+                        const int c16 = part * (RUN / 32) + c;  // 16 bytes of codes: 32 dimensions, two scales
+                        const uint4 w = *reinterpret_cast<const uint4*>(codes + code_off<D>(r, c16));
+                        const uint32_t two = real ? *reinterpret_cast<const uint16_t*>(sc + 2 * c) : 0u;
+                        const uint32_t f2 = e4m3x2_to_f16(two);
+                        const uint32_t sf[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t f[4];
+                            e2m1x8_to_f16(ws[j], f);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], sf[j >> 1]);
+                            *reinterpret_cast<uint4*>(dst + sw128(TILE, r, c16 * 4 + j)) = make_uint4(f[0], f[1], f[2], f[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv_full + 8 * at);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_empty + 8 * st);
+            }
+        }
+    } else {
+        // ---- softmax: one row a thread ---------------------------------------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int mt = warp >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // lane 32 (warp mod 4) in the upper half
+        const uint32_t s_col = lanes + C::S_COL + mt * TILE, o_col = lanes + C::O_COL + mt * D;
+        uint32_t tile = 0, piece = 0;  // of this tile of rows
+        Piece y;
+        bool go = true;
+        while (go && walk.next(p, y)) {
+            const int n = y.kt1 - y.kt0, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = mt * 128 + row;
+            if (mt > 0 && nrows <= 128) continue;
+            const bool mine = r < nrows;
+            const int t = (y.r0 + r) / p.G, h = y.hk * p.G + (y.r0 + r) - t * p.G;
+            const int64_t out = mine ? (int64_t)(y.x.q0 + t) * p.HQ + h : 0;
+            // Q: this thread's row as f16, scaled by a power of two (and by the sign of p.scale)
+            float sc;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + out * D);
+                float top = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = mine ? src[c] : make_uint4(0, 0, 0, 0);
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = bf16x2_to_float2(ws[j]);
+                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                }
+                uint32_t e = __float_as_uint(top) >> 23;
+                e = e < 30 ? 30 : e > 224 ? 224 : e;
+                const float down = __uint_as_float((254u - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
+                // (at least 2^-120: a masked score of -inf must stay one)
+                sc = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
+                uint8_t* dst = smem + C::Q_AT + mt * C::QBYTES;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = mine ? src[c] : make_uint4(0, 0, 0, 0);
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t f[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = bf16x2_to_float2(ws[j]);
+                        f[j] = f16x2_bits(v.x * down, v.y * down);
+                    }
+                    *reinterpret_cast<uint4*>(dst + sw128(128, row, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full + 8 * mt);
+            }
+            const int limit = y.x.kv - y.x.qlen + t + 1;                   // keys that the row sees
+            const int all_see = y.x.kv - y.x.qlen + y.r0 / p.G + 1;        // that every row of the item sees
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < n && go; ++i) {
+                go = warp_wait(s_full + 8 * mt, (tile + i) & 1);
+                if (!go) break;
+                tc_fence_after();
+                float x[TILE];
+#pragma unroll
+                for (int c = 0; c < TILE / 32; ++c) tmem_ld32(s_col + 32 * c, x + 32 * c);
+                tmem_wait_ld();
+                const int first = (y.kt0 + i) * TILE;
+                if (first + TILE > all_see) {
+                    const int lim = limit - first;
+#pragma unroll
+                    for (int j = 0; j < TILE; ++j)
+                        if (j >= lim) x[j] = -INFINITY;
+                }
+                float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int j = 4; j < TILE; j += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) t4[k] = j + 4 + k < TILE ? fmaxf(fmaxf(t4[k], x[j + k]), x[j + 4 + k]) : fmaxf(t4[k], x[j + k]);
+                const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+                const bool move = top > m + kSlack;
+                if (__any_sync(~0u, move)) {
+                    const float mn = move ? top : m;
+                    const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (i > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            float v[16];
+                            tmem_ld16(o_col + 16 * c, v);
+                            tmem_wait_ld();
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j] * f);
+                            tmem_st8(o_col + 16 * c, w);
+                            tmem_st8(o_col + 16 * c + 8, w + 8);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float mm = m == -INFINITY ? 0.f : m;
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < TILE / 64; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float a = exp2_fast(fmaf(x[64 * c + 2 * j], sc, -mm)), b = exp2_fast(fmaf(x[64 * c + 2 * j + 1], sc, -mm));
+                        l4[j & 3] += a + b;
+                        w[j] = f16x2_bits(a, b);
+                    }
+                    tmem_st32(s_col + 32 * c, w);
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * mt);
+            }
+            go = go && warp_wait(o_full + 8 * mt, piece & 1);
+            if (!go) break;
+            tile += n;
+            ++piece;
+            tc_fence_after();
+            const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
+            float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
+            const float inv = l > 0.f ? p.kv.v_scale / l : l != l ? l : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                tmem_ld32(o_col + 32 * c, v);
+                tmem_wait_ld();
+                if (!mine) continue;
+                if (whole) {
+                    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + out * D + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j] = make_uint4(bf16x2_bits(v[8 * j] * inv, v[8 * j + 1] * inv), bf16x2_bits(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
+                                            bf16x2_bits(v[8 * j + 4] * inv, v[8 * j + 5] * inv), bf16x2_bits(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(part + (int64_t)r * D + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
+            }
+            if (mine) {
+                if (!whole) *reinterpret_cast<float2*>(part + (int64_t)C::ROWS * D + 2 * r) = make_float2(m, l);
+                else if (p.lse) p.lse[out] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+            }
+            if (!whole && y.kt0 == 0 && tid == 0) {
+                desc->last = cta_of(all, ctas, walk.u - n + y.kts - 1);
+                desc->rows = nrows;
+                desc->q0 = y.x.q0;
+                desc->r0 = y.r0;
+                desc->hk = y.hk;
+            }
+            tc_fence_before();  // O is read before the next piece's first product writes it
+        }
+    }
+    if (bits && p.err) atomicOr(p.err, (int32_t)bits);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::COLS);
+    }
+}
+
+template <int D>
+cudaError_t run(const Kv4AttentionParams& p, cudaStream_t s) {
+    using C = Wide<D>;
+    static std::atomic<uint64_t> ready{0};  // a bit for each device whose kernel attributes are set and checked
+    const int sms = sm_count();
+    if (sms == 0) return cudaErrorNoDevice;
+    int dev = 0;
+    CUtensorMap map;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = codes_map(p.kv, C::TILE, &map);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        // the warps' registers are split anew in the kernel: the block has to hold what that sums up to
+        cudaFuncAttributes at{};
+        e = cudaFuncGetAttributes(&at, gdn_kv4_attention_wide_kernel<C>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
+        e = cudaFuncSetAttribute(gdn_kv4_attention_wide_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    gdn_kv4_attention_wide_kernel<C><<<sms, kThreads, C::SMEM, s>>>(p, map);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_kv4_join(p, C::ROWS, sms, s) : e;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_attention_wide(const Kv4AttentionParams& p, cudaStream_t s) {
+    return p.kv.D == 64 ? run<64>(p, s) : p.kv.D == 128 ? run<128>(p, s) : run<256>(p, s);
+}
+
+int64_t kv4_attention_wide_workspace(int D) {
+    const int sms = sm_count();
+    const int rows = D == 256 ? Wide<256>::ROWS : Wide<128>::ROWS;
+    return (int64_t)(sms > 0 ? sms : 152) * ((int64_t)sizeof(PartDesc) + 2 * part_floats(rows, D) * 4);
+}
+
+}  // namespace gdn
