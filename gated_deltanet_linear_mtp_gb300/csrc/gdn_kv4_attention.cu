@@ -42,6 +42,7 @@ namespace {
 template <int D_, int NR_, int W_, int WT_, int TILE_, int STAGES_, int CTAS_>
 struct Cfg {
     static constexpr int D = D_, NR = NR_, W = W_, WT = WT_, TILE = TILE_, STAGES = STAGES_, CTAS = CTAS_;
+    static constexpr bool SPLIT = false;  // a stage holds keys and values
     static constexpr int ROWS = 8 * NR, THREADS = 32 * (W + 4), STEPS = TILE / W / WT;
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a token's codes and scales
     static constexpr int STAGE = 2 * TILE * (CB + SB);
@@ -514,13 +515,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
 }
 
 // Joins the parts of items that more than one CTA worked on: block (x, y) takes rows y, y + gridDim.y, .. of the item that
-// CTA x began and did not end.  The four warps take every fourth part each; D / 4 threads (two rows' worth for D 64) cover
-// a row.
+// CTA x began and did not end.  Few parts: a warp takes a row.  Many: the block takes a row, D / 4 threads a part of it, and
+// as many parts side by side as that leaves room for.
 constexpr int kJoinThreads = 128;
+constexpr int kFewParts = 4;
 constexpr int kMaxParts = 1024;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) gdn_kv4_attention_join_kernel(Kv4AttentionParams p, int rows_max, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 8) gdn_kv4_attention_join_kernel(Kv4AttentionParams p, int rows_max, int ctas) {
     __shared__ float s_f[kMaxParts];
     __shared__ float s_red[2 * kJoinThreads / 32];
     __shared__ float4 s_acc[kJoinThreads];
@@ -531,6 +533,54 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_kv4_attention_join_kernel(Kv
     const int first = blockIdx.x, n = d.last - first + 1, tid = threadIdx.x;
     const int64_t step = part_floats(rows_max, D);
     auto part = [&](int i) { return parts + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * step; };
+    auto store = [&](int r, int ch, float4 a, float mm, float ll) {
+        const int t = (d.r0 + r) / p.G, h = d.hk * p.G + (d.r0 + r) - t * p.G;
+        const int64_t out = (int64_t)(d.q0 + t) * p.HQ + h;
+        const float inv = ll > 0.f ? p.kv.v_scale / ll : ll != ll ? ll : 0.f;
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + out * D + ch * 4) =
+            make_uint2(bf16x2_bits(a.x * inv, a.y * inv), bf16x2_bits(a.z * inv, a.w * inv));
+        if (ch == 0 && p.lse) p.lse[out] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+    };
+    if (n <= kFewParts) {  // a row a warp: nothing to exchange, all loads at once
+        const int lane = tid & 31;
+        constexpr int V = (D / 4 + 31) / 32;
+        for (int r = blockIdx.y * (kJoinThreads / 32) + (tid >> 5); r < d.rows; r += gridDim.y * (kJoinThreads / 32)) {
+            float2 ml[kFewParts];
+            float4 v[kFewParts][V];
+#pragma unroll
+            for (int i = 0; i < kFewParts; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                if (i >= n) continue;
+                ml[i] = *reinterpret_cast<const float2*>(part(i) + (int64_t)rows_max * D + 2 * r);
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (lane + 32 * k < D / 4) v[i][k] = *reinterpret_cast<const float4*>(part(i) + (int64_t)r * D + (lane + 32 * k) * 4);
+            }
+            float mm = ml[0].x, ll = 0.f;
+#pragma unroll
+            for (int i = 1; i < kFewParts; ++i) mm = fmaxf(mm, ml[i].x);
+            float4 a[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kFewParts; ++i) {
+                if (i >= n) continue;
+                const float f = mm == -INFINITY ? 1.f : exp2_fast(ml[i].x - mm);
+                ll = fmaf(ml[i].y, f, ll);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    a[k].x = fmaf(v[i][k].x, f, a[k].x);
+                    a[k].y = fmaf(v[i][k].y, f, a[k].y);
+                    a[k].z = fmaf(v[i][k].z, f, a[k].z);
+                    a[k].w = fmaf(v[i][k].w, f, a[k].w);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (lane + 32 * k < D / 4) store(r, lane + 32 * k, a[k], mm, ll);
+        }
+        return;
+    }
     for (int r = blockIdx.y; r < d.rows; r += gridDim.y) {
         float mm = -INFINITY;
         for (int i = tid; i < n; i += kJoinThreads) mm = fmaxf(mm, part(i)[(int64_t)rows_max * D + 2 * r]);
@@ -571,12 +621,7 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_kv4_attention_join_kernel(Kv
                 const float4 v = s_acc[k * TR + ch];
                 a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
             }
-            const int t = (d.r0 + r) / p.G, h = d.hk * p.G + (d.r0 + r) - t * p.G;
-            const int64_t out = (int64_t)(d.q0 + t) * p.HQ + h;
-            const float inv = ll > 0.f ? p.kv.v_scale / ll : ll != ll ? ll : 0.f;
-            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + out * D + ch * 4) =
-                make_uint2(bf16x2_bits(a.x * inv, a.y * inv), bf16x2_bits(a.z * inv, a.w * inv));
-            if (ch == 0 && p.lse) p.lse[out] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+            store(r, ch, a, mm, ll);
         }
         __syncthreads();
     }
@@ -640,7 +685,7 @@ int item_rows(int64_t rows, int D) {
 template <int D>
 cudaError_t run_join(const Kv4AttentionParams& p, int rows, int ctas, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, rows < 8 ? rows : rows <= 64 ? 8 : 64);
+    cfg.gridDim = dim3(ctas, rows <= 64 ? 8 : rows / 16);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -80,10 +80,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// The copying warp: tiles of the run, page by page; lane i takes page i of a tile
+// The copying warp: tiles of the run, page by page; lane i takes page i of a tile.  A stage holds a tile's keys and values
+// (codes of both, then scales of both), or with C::SPLIT its keys or its values.
 template <typename C, typename W>
 __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUtensorMap* map, W walk, uint32_t pool,
                                         uint8_t* pool_p, uint32_t full, uint32_t empty, uint32_t& bits) {
+    constexpr int KINDS = C::SPLIT ? 1 : 2;  // of rows in a stage
     const int lane = threadIdx.x & 31, P = p.kv.page_size, HK = p.kv.HK;
     const int PR = P < C::TILE ? P : C::TILE;  // rows of a copy
     uint32_t it = 0;
@@ -96,39 +98,42 @@ __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUten
             return kt < y.kt1 && lane * PR < C::TILE && tok < y.x.kv ? table[tok / P] : -2;
         };
         int pg = entry(y.kt0);
-        for (int kt = y.kt0; kt < y.kt1; ++kt, ++it) {
+        for (int kt = y.kt0; kt < y.kt1 && !late; ++kt) {
             const int ahead = entry(kt + 1);
-            const uint32_t s = it % C::STAGES, round = it / C::STAGES;
-            if (round > 0 && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, GDN_WAIT_POLLS))) {
-                bits |= GDN_ERRBIT_TIMEOUT;
-                late = true;
-                break;
-            }
-            const uint32_t st = pool + s * C::STAGE, bar = full + 8 * s;
-            const bool here = pg != -2, ok = here && (uint32_t)pg < (uint32_t)p.kv.num_pages;
-            if (here && !ok) {  // a page outside the cache: zeros
-                bits |= GDN_ERRBIT_INDEX;
-                uint8_t* z = pool_p + s * C::STAGE;
-                for (int i = 0; i < 2; ++i) {
-                    for (int j = 0; j < PR * C::CB; j += 16)
-                        *reinterpret_cast<uint4*>(z + (i * C::TILE + lane * PR) * C::CB + j) = make_uint4(0, 0, 0, 0);
-                    for (int j = 0; j < PR * C::SB; j += 16)
-                        *reinterpret_cast<uint4*>(z + 2 * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB + j) =
-                            make_uint4(0, 0, 0, 0);
+            for (int part = 0; part < 2 / KINDS; ++part, ++it) {
+                const uint32_t s = it % C::STAGES, round = it / C::STAGES;
+                if (round > 0 && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, GDN_WAIT_POLLS))) {
+                    bits |= GDN_ERRBIT_TIMEOUT;
+                    late = true;
+                    break;
                 }
-                fence_proxy_async_smem();
-            }
-            const uint32_t n = __popc(__ballot_sync(~0u, ok));
-            if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)(2 * PR * (C::CB + C::SB)));
-            __syncwarp();
-            if (ok) {
-                const int off = (kt * C::TILE) & (P - 1);
+                const uint32_t st = pool + s * C::STAGE, bar = full + 8 * s;
+                const bool here = pg != -2, ok = here && (uint32_t)pg < (uint32_t)p.kv.num_pages;
+                if (here && !ok) {  // a page outside the cache: zeros
+                    bits |= GDN_ERRBIT_INDEX;
+                    uint8_t* z = pool_p + s * C::STAGE;
+                    for (int i = 0; i < KINDS; ++i) {
+                        for (int j = 0; j < PR * C::CB; j += 16)
+                            *reinterpret_cast<uint4*>(z + (i * C::TILE + lane * PR) * C::CB + j) = make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < PR * C::SB; j += 16)
+                            *reinterpret_cast<uint4*>(z + KINDS * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB + j) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                const uint32_t n = __popc(__ballot_sync(~0u, ok));
+                if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)(KINDS * PR * (C::CB + C::SB)));
+                __syncwarp();
+                if (ok) {
+                    const int off = (kt * C::TILE) & (P - 1);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    tma_load_4d(st + (i * C::TILE + lane * PR) * C::CB, map, 0, off, i * HK + y.hk, pg, bar);
-                    const int64_t row = (((int64_t)pg * 2 + i) * HK + y.hk) * P + off;
-                    bulk_g2s(st + 2 * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB, p.kv.scales + row * C::SB,
-                             (uint32_t)(PR * C::SB), bar);
+                    for (int i = 0; i < KINDS; ++i) {
+                        const int which = part + i;
+                        tma_load_4d(st + (i * C::TILE + lane * PR) * C::CB, map, 0, off, which * HK + y.hk, pg, bar);
+                        const int64_t row = (((int64_t)pg * 2 + which) * HK + y.hk) * P + off;
+                        bulk_g2s(st + KINDS * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB, p.kv.scales + row * C::SB,
+                                 (uint32_t)(PR * C::SB), bar);
+                    }
                 }
             }
             pg = ahead;

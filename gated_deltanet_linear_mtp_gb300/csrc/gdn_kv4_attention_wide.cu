@@ -4,13 +4,14 @@
 // Bound: the products, 4 D flops a row and key.  An item is a tile of MT * 128 rows (whole tokens times the G heads of a key
 // head) of one lane and key head; a CTA takes its tiles of TILE keys in turn, as four kinds of warps:
 //   * one warp copies the packed tiles into shared memory by TMA (shared with the decode kernel);
-//   * a warpgroup unpacks them into f16 operand tiles (128-byte swizzle, a ring of three: K, V, K, ..), once for all rows: a
+//   * a warpgroup unpacks them into f16 operand tiles (128-byte swizzle, a ring of four: K, V, K, ..), once for all rows: a
 //     number costs the unpacking 1/256 of its products;
-//   * one thread issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory;
+//   * a thread for each 128 rows issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory;
 //   * a warpgroup for each 128 rows takes a row of S a thread, forms P in place of S as f16 and keeps the row's statistics.
-// With two tiles of rows the softmax of one runs while the tensor cores work on the other.  The running maximum moves only
-// where a score passes it by more than 2^8 (then that thread scales its row of O in tensor memory, which waits for
-// nothing: the S it holds was committed after the product that last wrote O), so O stays in tensor memory throughout.
+// S goes by units of 64 keys in two buffers: the way from a product to its softmax and back takes longer than either
+// (600 cycles each way measured), and with one buffer of 128 keys the tensor cores waited for it (831 us for two chunks of
+// 2048 tokens behind 8192 keys, HQ 32, HK 4, D 128).  The running maximum moves only where a score passes it by more than
+// 2^8 (then that thread scales its row of O in tensor memory), so O stays in tensor memory throughout.
 // Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16, fp32.
 //
 // Work split: all tiles of all items are numbered and each CTA (one an SM) takes an equal run of them, since the rows of a
@@ -25,10 +26,10 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 512;  // 4 warpgroups: softmax, softmax or unpacking, unpacking, MMA and copies
-constexpr int kMmaWarp = 12, kLoadWarp = 13;
-constexpr int kLaunchRegs = 128, kSoftRegs = 176, kUnpackRegs = 104, kRestRegs = 56;
+constexpr int kMmaWarp = 12, kLoadWarp = 14;  // kMmaWarp + m issues the products of rows 128 m ..
+constexpr int kLaunchRegs = 128, kSoftRegs = 160, kUnpackRegs = 112, kRestRegs = 80;
 static_assert(2 * kSoftRegs + kUnpackRegs + kRestRegs <= 4 * kLaunchRegs, "the block's registers");
-constexpr int kRing = 3;
+constexpr int kRing = 4;
 
 template <int D_>
 struct Wide {
@@ -36,14 +37,16 @@ struct Wide {
     static constexpr int MT = D == 256 ? 1 : 2;        // tiles of 128 rows
     static constexpr int TILE = D == 256 ? 64 : 128;   // keys of a tile
     static constexpr int ROWS = MT * 128;
-    static constexpr int STAGES = 2;                   // of packed tiles
-    static constexpr int CB = D / 2, SB = D / 16, STAGE = 2 * TILE * (CB + SB);
+    static constexpr bool SPLIT = true;                // a stage of the copies holds keys or values
+    static constexpr int STAGES = 3;
+    static constexpr int CB = D / 2, SB = D / 16, STAGE = TILE * (CB + SB);
     static constexpr int UNPACK = 128 * (3 - MT);      // threads that unpack
     static constexpr int QBYTES = 128 * D * 2, KVBYTES = TILE * D * 2;
     static constexpr int Q_AT = 0, RING_AT = MT * QBYTES, POOL_AT = RING_AT + kRing * KVBYTES;
     static constexpr int SMEM = 1024 + POOL_AT + STAGES * STAGE;
+    static constexpr int UNIT = 64, UPT = TILE / UNIT;  // keys of a product S; of them in a tile
     static constexpr int O_COL = 0, S_COL = MT * D, COLS = 512;
-    static_assert(S_COL + MT * TILE <= COLS, "tensor memory");
+    static_assert(S_COL + MT * 2 * UNIT <= COLS, "tensor memory");
 };
 
 // instruction descriptor of tcgen05.mma kind::f16 with f16 operands, D fp32
@@ -65,15 +68,47 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* f) {
     for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* w) {
+// The wait for this thread's loads, and that what they loaded is not used before it
+__device__ __forceinline__ void tmem_wait_ld32(float (&f)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]), "+f"(f[8]),
+                   "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]), "+f"(f[16]),
+                   "+f"(f[17]), "+f"(f[18]), "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]), "+f"(f[24]),
+                   "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30]), "+f"(f[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]),
-        "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]),
-        "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
         : "memory");
+}
+
+// The thread's row of `cols` columns (a multiple of 16) times f: fp32, or two f16 a column
+template <bool HALF>
+__device__ __noinline__ void scale_columns(uint32_t col, int cols, float f) {
+    tmem_wait_st();
+    for (int c = 0; c < cols; c += 16) {
+        float v[16];
+        uint32_t w[16];
+        tmem_ld16(col + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (HALF) {
+                const uint32_t b = __float_as_uint(v[j]);
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                w[j] = f16x2_bits(x.x * f, x.y * f);
+            } else {
+                w[j] = __float_as_uint(v[j] * f);
+            }
+        }
+        tmem_st16(col + c, w);
+    }
+    tmem_wait_st();
 }
 
 // ---- the run of tiles: pairs (lane, row tile), each with a tile of keys for every key head ------------------------
@@ -169,27 +204,25 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                                                                              const __grid_constant__ CUtensorMap map) {
     constexpr int D = C::D, MT = C::MT, TILE = C::TILE;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t s_pairs[kThreads + 1], s_tiles[kThreads + 1], s_warp[kThreads / 32];
-    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kRing + 4 * MT];
+    __shared__ int64_t s_warp[kThreads / 32];
+    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kRing + 6 * MT];
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t base_u = smem_u32(smem);
+    int64_t* s_pairs = reinterpret_cast<int64_t*>(smem + C::RING_AT);  // [kThreads + 1], before the ring is filled
+    int64_t* s_tiles = s_pairs + kThreads + 1;                         // [kThreads + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8 * C::STAGES, kv_full = raw_empty + 8 * C::STAGES,
                    kv_empty = kv_full + 8 * kRing, q_full = kv_empty + 8 * kRing, s_full = q_full + 8 * MT,
-                   p_full = s_full + 8 * MT, o_full = p_full + 8 * MT;
+                   p_full = s_full + 16 * MT, pv_done = p_full + 16 * MT;  // s_full, p_full: two for each 128 rows
     uint32_t bits = 0;
 
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) mbar_init(raw_full + 8 * i, 1), mbar_init(raw_empty + 8 * i, C::UNPACK / 32);
-        for (int i = 0; i < kRing; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, 1);
-        for (int i = 0; i < MT; ++i) {
-            mbar_init(q_full + 8 * i, 4);
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 4);
-            mbar_init(o_full + 8 * i, 1);
-        }
+        for (int i = 0; i < kRing; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, MT);
+        for (int i = 0; i < MT; ++i) mbar_init(q_full + 8 * i, 4), mbar_init(pv_done + 8 * i, 1);
+        for (int i = 0; i < 2 * MT; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4);
         fence_mbar_init();
         s_dead = 0;
     }
@@ -250,8 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
     auto wait = [&](uint32_t bar, uint32_t parity) {  // false: it ran out, and the CTA's work with it
-        if (*dead) return false;
-        if (mbar_wait_bounded(bar, parity, GDN_WAIT_POLLS)) return true;
+        for (uint32_t i = 0; i < GDN_WAIT_POLLS; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((i & 63) == 63 && *dead) return false;
+        }
         *dead = 1;
         bits |= GDN_ERRBIT_TIMEOUT;
         return false;
@@ -262,54 +297,61 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
         if (warp == kLoadWarp) {
             produce<C>(p, &map, walk, base_u + C::POOL_AT, smem + C::POOL_AT, raw_full, raw_empty, bits);
-        } else if (warp == kMmaWarp && lane == 0) {
-            // tiles go through the ring as K0, V0, K1, V1, ..; slot n of a piece sequence is ring place n % kRing
-            constexpr uint32_t id_s = idesc_f16(128, TILE), id_o = idesc_f16(128, D) | (1u << 16);
-            uint32_t slot = 0, piece[2] = {0, 0}, tile[2] = {0, 0};  // ring slots; pieces and tiles of each tile of rows
+        } else if (warp < kMmaWarp + MT && lane == 0) {
+            // Tiles go through the ring as K0, V0, K1, V1, ..; slot n of all is ring place n % kRing.  A thread for each 128
+            // rows: what one waits for passes while the other's products run.  Units of 64 keys alternate between two
+            // buffers of S, so that a softmax finds its next scores ready whatever the way there and back takes.
+            constexpr uint32_t id_s = idesc_f16(128, C::UNIT), id_o = idesc_f16(128, D) | (1u << 16);
+            const int m = warp - kMmaWarp;
+            uint32_t slot = 0, piece = 0, unit = 0;  // ring slots; pieces and units of these rows
             Piece y;
             bool go = true;
             auto ring_wait = [&](uint32_t n) { return wait(kv_full + 8 * (n % kRing), (n / kRing) & 1); };
+            auto release = [&](uint32_t n) { umma_commit(kv_empty + 8 * (n % kRing)); };
             // descriptors differ in their start address alone: 16 bytes count 1
-            const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT), k_desc = umma_desc_sw128(base_u + C::RING_AT),
+            const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT + m * C::QBYTES), k_desc = umma_desc_sw128(base_u + C::RING_AT),
                            v_desc = umma_desc_sw128_mn(base_u + C::RING_AT, TILE * 128);
-            auto product_s = [&](uint32_t n, int m) {
-                const uint64_t q = q_desc + m * (C::QBYTES / 16), k = k_desc + (n % kRing) * (C::KVBYTES / 16);
+            // scores of unit u of the piece: K of its tile is ring slot slot + 2 (u / UPT), V the one behind
+            auto product_s = [&](int u) {
+                const uint32_t n = slot + 2 * (u / C::UPT), at = unit + u;
+                if (u % C::UPT == 0 && !ring_wait(n)) return false;
+                tc_fence_after();
+                const uint64_t k = k_desc + (n % kRing) * (C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    umma_bf16(tmem + C::S_COL + m * TILE, q + ((ks / 4) * 128 * 128 + (ks % 4) * 32) / 16,
+                    umma_bf16(tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT, q_desc + ((ks / 4) * 128 * 128 + (ks % 4) * 32) / 16,
                               k + ((ks / 4) * TILE * 128 + (ks % 4) * 32) / 16, id_s, ks > 0);
-                umma_commit(s_full + 8 * m);
+                umma_commit(s_full + 8 * (2 * m + (at & 1)));
+                if (u % C::UPT == C::UPT - 1) release(n);
+                return true;
             };
             while (go && walk.next(p, y)) {
-                const int n = y.kt1 - y.kt0, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), mts = nrows > 128 ? MT : 1;
-                for (int m = 0; m < mts && go; ++m) go = wait(q_full + 8 * m, piece[m] & 1);
-                go = go && ring_wait(slot);
-                if (!go) break;
-                tc_fence_after();
-                for (int m = 0; m < mts; ++m) product_s(slot, m);
-                umma_commit(kv_empty + 8 * (slot % kRing));
-                ++slot;
-                for (int i = 0; i < n && go; ++i) {  // `slot` holds V of tile i, the next one K of tile i + 1
-                    const bool more = i + 1 < n;
-                    go = ring_wait(slot) && (!more || ring_wait(slot + 1));
-                    for (int m = 0; m < mts && go; ++m) {
-                        go = wait(p_full + 8 * m, (tile[m] + i) & 1);
-                        if (!go) break;
-                        tc_fence_after();
-                        const uint64_t v = v_desc + (slot % kRing) * (C::KVBYTES / 16);
-#pragma unroll
-                        for (int ks = 0; ks < TILE / 16; ++ks)
-                            umma_bf16_ta(tmem + C::O_COL + m * D, tmem + C::S_COL + m * TILE + ks * 8,
-                                         v + ks * (2048 / 16), id_o, i > 0 || ks > 0);
-                        if (more) product_s(slot + 1, m);
-                        else umma_commit(o_full + 8 * m);
+                const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0);
+                if (m * 128 >= nrows) {  // no rows here: the tiles pass by
+                    for (int i = 0; i < 2 * n && go; ++i, ++slot) {
+                        go = ring_wait(slot);
+                        if (go) mbar_arrive(kv_empty + 8 * (slot % kRing));
                     }
-                    if (!go) break;
-                    umma_commit(kv_empty + 8 * (slot % kRing));
-                    if (more) umma_commit(kv_empty + 8 * ((slot + 1) % kRing));
-                    slot += more ? 2 : 1;
+                    continue;
                 }
-                for (int m = 0; m < mts; ++m) ++piece[m], tile[m] += n;
+                go = wait(q_full + 8 * m, piece & 1) && product_s(0) && (units < 2 || product_s(1));
+                for (int u = 0; u < units && go; ++u) {
+                    const uint32_t at = unit + u, nv = slot + 2 * (u / C::UPT) + 1;
+                    go = (u % C::UPT != 0 || ring_wait(nv)) && wait(p_full + 8 * (2 * m + (at & 1)), (at >> 1) & 1);
+                    if (!go) break;
+                    tc_fence_after();
+                    const uint64_t v = v_desc + (nv % kRing) * (C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
+#pragma unroll
+                    for (int ks = 0; ks < C::UNIT / 16; ++ks)
+                        umma_bf16_ta(tmem + C::O_COL + m * D, tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT + ks * 8,
+                                     v + ks * (2048 / 16), id_o, u > 0 || ks > 0);
+                    umma_commit(pv_done + 8 * m);
+                    if (u % C::UPT == C::UPT - 1) release(nv);
+                    if (u + 2 < units) go = product_s(u + 2);
+                }
+                ++piece;
+                unit += units;
+                slot += 2 * n;
             }
         }
     } else if (warp >= 4 * MT) {
@@ -318,47 +360,50 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         constexpr int PARTS = C::UNPACK / TILE, RUN = D / PARTS;  // dimensions of a thread
         const int idx = tid - 128 * MT, r = idx % TILE, part = idx / TILE;
-        uint32_t it = 0, slot = 0;
+        uint32_t slot = 0;
         Piece y;
         bool go = true;
         while (go && walk.next(p, y)) {
-            for (int kt = y.kt0; kt < y.kt1 && go; ++kt, ++it) {
-                const uint32_t st = it % C::STAGES;
-                go = warp_wait(raw_full + 8 * st, (it / C::STAGES) & 1);
-                if (!go) break;
-                const uint8_t* raw = smem + C::POOL_AT + st * C::STAGE;
+            for (int kt = y.kt0; kt < y.kt1 && go; ++kt) {
                 const bool real = kt * TILE + r < y.x.kv;  // what lies behind the last token may be anything
-#pragma unroll
+#pragma unroll 1
                 for (int which = 0; which < 2; ++which, ++slot) {
-                    const uint32_t at = slot % kRing;
+                    const uint32_t at = slot % kRing, st = slot % C::STAGES;
+                    go = warp_wait(raw_full + 8 * st, (slot / C::STAGES) & 1);
                     if (slot >= kRing) go = go && warp_wait(kv_empty + 8 * at, (slot / kRing - 1) & 1);
                     if (!go) break;
                     uint8_t* dst = smem + C::RING_AT + at * C::KVBYTES;
-                    const uint8_t* codes = raw + which * TILE * C::CB;
-                    const uint8_t* sc = raw + 2 * TILE * C::CB + which * TILE * C::SB + r * C::SB + part * (RUN / 16);
+                    const uint8_t* codes = smem + C::POOL_AT + st * C::STAGE;
+                    const uint8_t* sc = codes + TILE * C::CB + r * C::SB + part * (RUN / 16);
+                    uint4 w[RUN / 32];
+                    uint32_t two[RUN / 32];
+#pragma unroll
+                    for (int c = 0; c < RUN / 32; ++c) {  // 16 bytes of codes: 32 dimensions, two scales
+                        w[c] = *reinterpret_cast<const uint4*>(codes + code_off<D>(r, part * (RUN / 32) + c));
+                        two[c] = real ? *reinterpret_cast<const uint16_t*>(sc + 2 * c) : 0u;
+                    }
 #pragma unroll
                     for (int c = 0; c < RUN / 32; ++c) {
-                        const int c16 = part * (RUN / 32) + c;  // 16 bytes of codes: 32 dimensions, two scales
-                        const uint4 w = *reinterpret_cast<const uint4*>(codes + code_off<D>(r, c16));
-                        const uint32_t two = real ? *reinterpret_cast<const uint16_t*>(sc + 2 * c) : 0u;
-                        const uint32_t f2 = e4m3x2_to_f16(two);
+                        const uint32_t f2 = e4m3x2_to_f16(two[c]);
                         const uint32_t sf[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t f[4];
                             e2m1x8_to_f16(ws[j], f);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], sf[j >> 1]);
-                            *reinterpret_cast<uint4*>(dst + sw128(TILE, r, c16 * 4 + j)) = make_uint4(f[0], f[1], f[2], f[3]);
+                            *reinterpret_cast<uint4*>(dst + sw128(TILE, r, (part * (RUN / 32) + c) * 4 + j)) =
+                                make_uint4(f[0], f[1], f[2], f[3]);
                         }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(kv_full + 8 * at);
+                    if (lane == 0) {
+                        mbar_arrive(kv_full + 8 * at);
+                        mbar_arrive(raw_empty + 8 * st);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(raw_empty + 8 * st);
             }
         }
     } else {
@@ -366,12 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int mt = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // lane 32 (warp mod 4) in the upper half
-        const uint32_t s_col = lanes + C::S_COL + mt * TILE, o_col = lanes + C::O_COL + mt * D;
-        uint32_t tile = 0, piece = 0;  // of this tile of rows
+        const uint32_t s_col0 = lanes + C::S_COL + mt * 2 * C::UNIT, o_col = lanes + C::O_COL + mt * D;
+        uint32_t unit = 0;  // of this tile of rows
         Piece y;
         bool go = true;
         while (go && walk.next(p, y)) {
-            const int n = y.kt1 - y.kt0, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = mt * 128 + row;
+            const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = mt * 128 + row;
             if (mt > 0 && nrows <= 128) continue;
             const bool mine = r < nrows;
             const int t = (y.r0 + r) / p.G, h = y.hk * p.G + (y.r0 + r) - t * p.G;
@@ -416,71 +461,72 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             const int limit = y.x.kv - y.x.qlen + t + 1;                   // keys that the row sees
             const int all_see = y.x.kv - y.x.qlen + y.r0 / p.G + 1;        // that every row of the item sees
             float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < n && go; ++i) {
-                go = warp_wait(s_full + 8 * mt, (tile + i) & 1);
+            for (int u = 0; u < units && go; ++u, ++unit) {
+                go = warp_wait(s_full + 8 * (2 * mt + (unit & 1)), (unit >> 1) & 1);
                 if (!go) break;
                 tc_fence_after();
-                float x[TILE];
+                const uint32_t s_col = s_col0 + (unit & 1) * C::UNIT;
+                const int first = y.kt0 * TILE + u * C::UNIT;
+                const bool mask = first + C::UNIT > all_see;
+                F2 l2 = f2(0.f, 0.f);
+                // 32 columns at a time: P's 16 columns go where S has been read
+                auto chunk = [&](float (&x)[32], int c) {
+                    if (mask) {
+                        const int lim = limit - first - 32 * c;
 #pragma unroll
-                for (int c = 0; c < TILE / 32; ++c) tmem_ld32(s_col + 32 * c, x + 32 * c);
-                tmem_wait_ld();
-                const int first = (y.kt0 + i) * TILE;
-                if (first + TILE > all_see) {
-                    const int lim = limit - first;
-#pragma unroll
-                    for (int j = 0; j < TILE; ++j)
-                        if (j >= lim) x[j] = -INFINITY;
-                }
-                float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int j = 4; j < TILE; j += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) t4[k] = j + 4 + k < TILE ? fmaxf(fmaxf(t4[k], x[j + k]), x[j + 4 + k]) : fmaxf(t4[k], x[j + k]);
-                const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
-                const bool move = top > m + kSlack;
-                if (__any_sync(~0u, move)) {
-                    const float mn = move ? top : m;
-                    const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (i > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            float v[16];
-                            tmem_ld16(o_col + 16 * c, v);
-                            tmem_wait_ld();
-                            uint32_t w[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j] * f);
-                            tmem_st8(o_col + 16 * c, w);
-                            tmem_st8(o_col + 16 * c + 8, w + 8);
-                        }
-                        tmem_wait_st();
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= lim) x[j] = -INFINITY;
                     }
-                }
-                const float mm = m == -INFINITY ? 0.f : m;
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 0; c < TILE / 64; ++c) {
-                    uint32_t w[32];
+                    for (int j = 4; j < 28; j += 8)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float a = exp2_fast(fmaf(x[64 * c + 2 * j], sc, -mm)), b = exp2_fast(fmaf(x[64 * c + 2 * j + 1], sc, -mm));
-                        l4[j & 3] += a + b;
+                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[j + k]), x[j + 4 + k]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], x[28 + k]);
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+                    const bool move = top > m + kSlack;
+                    if (__any_sync(~0u, move)) {
+                        const float mn = move ? top : m;
+                        const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+                        m = mn;
+                        l *= f;
+                        l2 = mul(l2, f2(f, f));
+                        if (u > 0) {  // the product that last wrote O: the one before it is done, as these scores came after it
+                            go = warp_wait(pv_done + 8 * mt, (unit - 1) & 1);
+                            tc_fence_after();
+                            scale_columns<false>(o_col, D, f);
+                        }
+                        scale_columns<true>(s_col, 16 * c, f);
+                    }
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 z = split(fma(f2(x[2 * j], x[2 * j + 1]), f2(sc, sc), f2(mm, mm)));
+                        const float a = exp2_fast(z.x), b = exp2_fast(z.y);
+                        l2 = add(l2, f2(a, b));
                         w[j] = f16x2_bits(a, b);
                     }
-                    tmem_st32(s_col + 32 * c, w);
-                }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    tmem_st16(s_col + 16 * c, w);
+                };
+                float xa[32], xb[32];
+                tmem_ld32(s_col, xa);
+                tmem_ld32(s_col + 32, xb);
+                tmem_wait_ld32(xa);
+                tmem_wait_ld32(xb);
+                chunk(xa, 0);
+                chunk(xb, 1);
+                const float2 ls = split(l2);
+                l += ls.x + ls.y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * mt);
+                if (lane == 0) mbar_arrive(p_full + 8 * (2 * mt + (unit & 1)));
             }
-            go = go && warp_wait(o_full + 8 * mt, piece & 1);
+            if (units > 1) go = go && warp_wait(pv_done + 8 * mt, unit & 1);  // the last product but one, and the last
+            go = go && warp_wait(pv_done + 8 * mt, (unit - 1) & 1);
             if (!go) break;
-            tile += n;
-            ++piece;
             tc_fence_after();
             const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
             float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);

@@ -39,31 +39,6 @@ constexpr float kMaxF32 = 3.4028235e38f;
 constexpr int kRows = 2;  // of a token that a group of lanes loads together
 constexpr int kCtas = 4;  // of an SM: 2 rows and 32 warps an SM beat 4 rows and 16 (8192 tokens 49.5 us against 55.6)
 
-// ---- two fp32 numbers an instruction -----------------------------------------------------------------------
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 split(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // Four consecutive numbers as two pairs
 template <typename T>
 struct Quad;
