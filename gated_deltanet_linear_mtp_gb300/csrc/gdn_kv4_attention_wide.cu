@@ -112,45 +112,41 @@ __device__ __noinline__ void scale_columns(uint32_t col, int cols, float f) {
 }
 
 // ---- the run of tiles: pairs (lane, row tile), each with a tile of keys for every key head ------------------------
-template <typename C>
-__device__ __forceinline__ int row_tiles(const Kv4AttentionParams& p, const Lane& x) {
-    const int tt = C::ROWS / p.G;  // tokens of a row tile
-    return (x.qlen + tt - 1) / tt;
-}
+// tt: tokens of a row tile
+__device__ __forceinline__ int row_tiles(const Lane& x, int tt) { return (x.qlen + tt - 1) / tt; }
 
 // Tiles of keys that row tile rt of a lane sees
 template <typename C>
-__device__ __forceinline__ int key_tiles(const Kv4AttentionParams& p, const Lane& x, int rt) {
-    const int64_t end = min((int64_t)(rt + 1) * (C::ROWS / p.G), (int64_t)x.qlen);
-    const int64_t keys = x.kv - x.qlen + end;
-    return keys > 0 ? (int)((keys - 1) / C::TILE + 1) : 1;
+__device__ __forceinline__ int key_tiles(const Lane& x, int tt, int rt) {
+    const int keys = x.kv - x.qlen + min((rt + 1) * tt, x.qlen);  // qlen <= N, kv: both below 2^31
+    return keys > 0 ? (keys - 1) / C::TILE + 1 : 1;
 }
 
 template <typename C>
 struct WideWalk {
     int64_t u, u1, base;  // base: first tile of pair (b, rt)
-    int b, rt;
+    int b, rt, tt;
+    Lane x;  // of lane b
     __device__ __forceinline__ bool next(const Kv4AttentionParams& p, Piece& y) {
         if (u >= u1) return false;
         uint32_t ignored = 0;
-        y.x = lane_extent(p, b, ignored);
         for (;;) {
-            const int rts = row_tiles<C>(p, y.x);
-            if (rt >= rts) {
+            if (rt * tt >= x.qlen) {
                 rt = 0;
-                y.x = lane_extent(p, ++b, ignored);
+                x = lane_extent(p, ++b, ignored);
                 continue;
             }
-            y.kts = key_tiles<C>(p, y.x, rt);
+            y.kts = key_tiles<C>(x, tt, rt);
             if (base + (int64_t)y.kts * p.kv.HK > u) break;
             base += (int64_t)y.kts * p.kv.HK;
             ++rt;
         }
+        y.x = x;
         y.b = b;
-        const int64_t in = u - base;
-        y.hk = (int)(in / y.kts);
-        y.kt0 = (int)(in - (int64_t)y.hk * y.kts);
-        y.r0 = rt * (C::ROWS / p.G) * p.G;
+        const uint32_t in = (uint32_t)(u - base);  // below kts * HK
+        y.hk = (int)(in / (uint32_t)y.kts);
+        y.kt0 = (int)(in - (uint32_t)y.hk * y.kts);
+        y.r0 = rt * tt * p.G;
         y.kt1 = (int)min((int64_t)y.kts, y.kt0 + (u1 - u));
         u += y.kt1 - y.kt0;
         return true;
@@ -179,8 +175,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_warp, int64_
 }
 
 // The lane and row tile of pair i; s_pairs[t]: pairs before the lanes of thread t (`per` lanes each)
-template <typename C>
-__device__ void locate(const Kv4AttentionParams& p, const int64_t* s_pairs, int per, int64_t i, int& b, int& rt) {
+__device__ __forceinline__ void locate(const Kv4AttentionParams& p, const int64_t* s_pairs, int per, int tt, int64_t i, int& b, int& rt) {
     int lo = 0, hi = kThreads;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -191,7 +186,7 @@ __device__ void locate(const Kv4AttentionParams& p, const int64_t* s_pairs, int 
     int64_t at = s_pairs[lo];
     b = lo * per;
     for (;;) {
-        const int n = row_tiles<C>(p, lane_extent(p, b, ignored));
+        const int n = row_tiles(lane_extent(p, b, ignored), tt);
         if (at + n > i) break;
         at += n;
         ++b;
@@ -232,9 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     WideWalk<C> walk;
     int64_t all;
     {
-        const int per = (p.B + kThreads - 1) / kThreads;
+        const int per = (p.B + kThreads - 1) / kThreads, tt = C::ROWS / p.G;
         int64_t n = 0, pairs;
-        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) n += row_tiles<C>(p, lane_extent(p, b, bits));
+        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) n += row_tiles(lane_extent(p, b, bits), tt);
         s_pairs[tid] = block_scan(n, s_warp, pairs);
         if (tid == 0) s_pairs[kThreads] = pairs;
         __syncthreads();
@@ -243,14 +238,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         if (i0 < i1) {
             int b, rt;
             uint32_t ignored = 0;
-            locate<C>(p, s_pairs, per, i0, b, rt);
+            locate(p, s_pairs, per, tt, i0, b, rt);
             Lane x = lane_extent(p, b, ignored);
             for (int64_t i = i0; i < i1; ++i, ++rt) {
-                while (rt >= row_tiles<C>(p, x)) {
+                while (rt * tt >= x.qlen) {
                     rt = 0;
                     x = lane_extent(p, ++b, ignored);
                 }
-                n += key_tiles<C>(p, x, rt);
+                n += key_tiles<C>(x, tt, rt);
             }
         }
         s_tiles[tid] = block_scan(n * p.kv.HK, s_warp, all);
@@ -268,7 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 else hi = mid;
             }
             walk.base = s_tiles[lo];
-            locate<C>(p, s_pairs, per, pairs * lo / kThreads, walk.b, walk.rt);
+            uint32_t ignored = 0;
+            locate(p, s_pairs, per, tt, pairs * lo / kThreads, walk.b, walk.rt);
+            walk.x = lane_extent(p, walk.b, ignored);
+            walk.tt = tt;
         }
     }
     const int64_t ctas = all < gridDim.x ? all : gridDim.x;
@@ -312,10 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT + m * C::QBYTES), k_desc = umma_desc_sw128(base_u + C::RING_AT),
                            v_desc = umma_desc_sw128_mn(base_u + C::RING_AT, TILE * 128);
             // scores of unit u of the piece: K of its tile is ring slot slot + 2 (u / UPT), V the one behind
+            auto keys_wait = [&](int u) { return u % C::UPT != 0 || ring_wait(slot + 2 * (u / C::UPT)); };
             auto product_s = [&](int u) {
                 const uint32_t n = slot + 2 * (u / C::UPT), at = unit + u;
-                if (u % C::UPT == 0 && !ring_wait(n)) return false;
-                tc_fence_after();
                 const uint64_t k = k_desc + (n % kRing) * (C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
@@ -323,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                               k + ((ks / 4) * TILE * 128 + (ks % 4) * 32) / 16, id_s, ks > 0);
                 umma_commit(s_full + 8 * (2 * m + (at & 1)));
                 if (u % C::UPT == C::UPT - 1) release(n);
-                return true;
             };
             while (go && walk.next(p, y)) {
                 const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0);
@@ -334,10 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                     }
                     continue;
                 }
-                go = wait(q_full + 8 * m, piece & 1) && product_s(0) && (units < 2 || product_s(1));
+                for (int u = 0; u < 2 && u < units && go; ++u) {
+                    go = keys_wait(u) && (u > 0 || wait(q_full + 8 * m, piece & 1));
+                    if (!go) break;
+                    tc_fence_after();
+                    product_s(u);
+                }
                 for (int u = 0; u < units && go; ++u) {
                     const uint32_t at = unit + u, nv = slot + 2 * (u / C::UPT) + 1;
-                    go = (u % C::UPT != 0 || ring_wait(nv)) && wait(p_full + 8 * (2 * m + (at & 1)), (at >> 1) & 1);
+                    // what comes early is waited for first: between P and the products stands one wait
+                    go = (u % C::UPT != 0 || ring_wait(nv)) && (u + 2 >= units || keys_wait(u + 2)) &&
+                         wait(p_full + 8 * (2 * m + (at & 1)), (at >> 1) & 1);
                     if (!go) break;
                     tc_fence_after();
                     const uint64_t v = v_desc + (nv % kRing) * (C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                                      v + ks * (2048 / 16), id_o, u > 0 || ks > 0);
                     umma_commit(pv_done + 8 * m);
                     if (u % C::UPT == C::UPT - 1) release(nv);
-                    if (u + 2 < units) go = product_s(u + 2);
+                    if (u + 2 < units) product_s(u + 2);
                 }
                 ++piece;
                 unit += units;
@@ -425,15 +428,21 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             float sc;
             {
                 const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + out * D);
+                constexpr int HELD = D / 8 < 16 ? D / 8 : 16;  // 16-byte pieces in registers; a longer row is read twice
+                uint4 w[HELD];
                 float top = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 w = mine ? src[c] : make_uint4(0, 0, 0, 0);
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = bf16x2_to_float2(ws[j]);
-                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                for (int c0 = D / 8 - HELD; c0 >= 0; c0 -= HELD) {
+#pragma unroll
+                    for (int c = 0; c < HELD; ++c) w[c] = mine ? src[c0 + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < HELD; ++c) {
+                        const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 v = bf16x2_to_float2(ws[j]);
+                            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        }
                     }
                 }
                 uint32_t e = __float_as_uint(top) >> 23;
@@ -442,17 +451,23 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 // (at least 2^-120: a masked score of -inf must stay one)
                 sc = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
                 uint8_t* dst = smem + C::Q_AT + mt * C::QBYTES;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 w = mine ? src[c] : make_uint4(0, 0, 0, 0);
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t f[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = bf16x2_to_float2(ws[j]);
-                        f[j] = f16x2_bits(v.x * down, v.y * down);
+                for (int c0 = 0; c0 < D / 8; c0 += HELD) {
+                    if (c0 > 0) {
+#pragma unroll
+                        for (int c = 0; c < HELD; ++c) w[c] = mine ? src[c0 + c] : make_uint4(0, 0, 0, 0);
                     }
-                    *reinterpret_cast<uint4*>(dst + sw128(128, row, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+                    for (int c = 0; c < HELD; ++c) {
+                        const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                        uint32_t f[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 v = bf16x2_to_float2(ws[j]);
+                            f[j] = f16x2_bits(v.x * down, v.y * down);
+                        }
+                        *reinterpret_cast<uint4*>(dst + sw128(128, row, c0 + c)) = make_uint4(f[0], f[1], f[2], f[3]);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
