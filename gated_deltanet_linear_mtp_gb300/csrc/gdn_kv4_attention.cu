@@ -7,9 +7,9 @@
 // r % G, so the cached keys and values are read once for all of them.  An item is (lane, row tile, key head).
 //
 // Bound: the cache's 9/16 byte a number from HBM, and close behind it the issue slots of the unpacking (two conversions'
-// worth of instructions a pair of numbers); with 32 rows and more the tensor cores' rate for mma.sync (600 TFLOP/s
-// measured).  Nothing is dequantised into memory: one warp brings packed tiles of 128 tokens into shared memory by TMA
-// (swizzled, a pipeline of kStages), and each lane of the others unpacks the codes of its own MMA fragments (cvt
+// worth of instructions a pair of numbers); with 32 rows the tensor cores' rate for mma.sync (600 TFLOP/s measured).  More
+// rows go to gdn_kv4_attention_wide.cu.  Nothing is dequantised into memory: one warp brings packed tiles of 128 tokens into shared memory by TMA
+// (swizzled, a pipeline of several), and each lane of the others unpacks the codes of its own MMA fragments (cvt
 // e2m1x2 -> f16x2, one multiply by the group's scale; both exact).  Keys and values are the M operand and the rows are N:
 // N goes by 8, so a decode's 8 rows waste nothing.  The products' summation index may be permuted freely, which makes the
 // fragments contiguous in storage:
@@ -27,7 +27,8 @@
 // Work split: all tiles of all items are numbered item by item and each CTA takes an equal run of them, so one long lane
 // fills the GPU as well as many short ones.  A run ends in an item's middle on most CTAs: such parts (m, l, O in fp32) go
 // to the workspace, two at most a CTA, and a second kernel, launched programmatically behind the first, joins them in
-// order.  The four warps of a CTA take 32 tokens each of a tile and join their parts in shared memory.
+// order.  The eight warps of a CTA take 16 or 32 tokens each of a tile and join their parts in shared memory.
+#include <algorithm>
 #include <atomic>
 
 #include "gdn_kv4_attention.cuh"
@@ -37,11 +38,11 @@ namespace gdn {
 namespace {
 
 // NR: groups of 8 rows of an item; W: warps that compute (one of four more copies, and those four give their registers to
-// the others: LREG a thread at launch, then CREG and PREG); WT: tokens of a warp's step; TILE: tokens of a
-// tile; STAGES: tiles in the pipeline; CTAS: of an SM, at least
-template <int D_, int NR_, int W_, int WT_, int TILE_, int STAGES_, int CTAS_>
+// the others: LREG a thread at launch, then CREG and PREG); WT: tokens of a warp's step; TILE: tokens of a tile; STAGES: tiles
+// in the pipeline; CTAS: of an SM
+template <int D_, int NR_, int WT_, int TILE_, int STAGES_, int CTAS_>
 struct Cfg {
-    static constexpr int D = D_, NR = NR_, W = W_, WT = WT_, TILE = TILE_, STAGES = STAGES_, CTAS = CTAS_;
+    static constexpr int D = D_, NR = NR_, W = 8, WT = WT_, TILE = TILE_, STAGES = STAGES_, CTAS = CTAS_;
     static constexpr bool SPLIT = false;  // a stage holds keys and values
     static constexpr int ROWS = 8 * NR, THREADS = 32 * (W + 4), STEPS = TILE / W / WT;
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a token's codes and scales
@@ -52,46 +53,8 @@ struct Cfg {
     static constexpr int MERGE = W * 8 * OROW * 4;
     static constexpr int SMEM = 1024 + STAGES * STAGE + QBYTES + MERGE + W * 64 + ROWS * 4;
     static constexpr int LREG = CTAS == 1 ? 168 : 80, CREG = CTAS == 1 ? 232 : 104, PREG = CTAS == 1 ? 40 : 32;
-    static_assert(W == 8 && 2 * CREG + PREG <= 3 * LREG, "the block's registers");
+    static_assert(2 * CREG + PREG <= 3 * LREG, "the block's registers");
     static_assert(STEPS * W * WT == TILE && TILE % 128 == 0 && WT % 16 == 0, "tile split");
-};
-
-template <typename C>
-__device__ __forceinline__ int tiles_of(int kv) {
-    return kv > 0 ? (kv - 1) / C::TILE + 1 : 1;
-}
-
-template <typename C>
-__device__ __forceinline__ int64_t lane_tiles(const Kv4AttentionParams& p, const Lane& x) {
-    return ((int64_t)x.qlen * p.G + C::ROWS - 1) / C::ROWS * tiles_of<C>(x.kv) * p.kv.HK;
-}
-
-// Walks a CTA's run of tiles u .. u1 - 1; lane `b` holds tile `base` first
-template <typename C>
-struct Walk {
-    int64_t u, u1, base;
-    int b;
-    __device__ __forceinline__ bool next(const Kv4AttentionParams& p, Piece& y) {
-        if (u >= u1) return false;
-        uint32_t ignored = 0;
-        y.x = lane_extent(p, b, ignored);
-        int64_t n = lane_tiles<C>(p, y.x);
-        while (base + n <= u) {
-            base += n;
-            y.x = lane_extent(p, ++b, ignored);
-            n = lane_tiles<C>(p, y.x);
-        }
-        y.b = b;
-        y.kts = tiles_of<C>(y.x.kv);
-        const int64_t in = u - base;
-        const int item = (int)(in / y.kts);
-        y.kt0 = (int)(in - (int64_t)item * y.kts);
-        y.hk = item % p.kv.HK;
-        y.r0 = item / p.kv.HK * C::ROWS;
-        y.kt1 = (int)min((int64_t)y.kts, y.kt0 + (u1 - u));
-        u += y.kt1 - y.kt0;
-        return true;
-    }
 };
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -115,8 +78,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* pool = smem;
     uint4* s_q = reinterpret_cast<uint4*>(smem + C::STAGES * C::STAGE);
-    float* s_o = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::QBYTES);  // [C::W][8][OROW]
-    float2* s_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(s_o) + C::MERGE);  // [C::W][8]
+    float* s_o = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::QBYTES);  // [W][8][OROW]
+    float2* s_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(s_o) + C::MERGE);  // [W][8]
     float* s_sc = reinterpret_cast<float*>(s_ml + C::W * 8);                             // [ROWS]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const uint32_t full = smem_u32(s_bar), empty = full + 8 * C::STAGES;
@@ -132,21 +95,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
         s_dead = 0;
     }
     const int per = (p.B + C::THREADS - 1) / C::THREADS;
-    {
-        int64_t x = 0;
-        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) x += lane_tiles<C>(p, lane_extent(p, b, bits));
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(~0u, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) s_warp[warp] = x;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) x += s_warp[w];
-        s_scan[tid + 1] = x;
-        if (tid == 0) s_scan[0] = 0;
-        __syncthreads();
-    }
+    scan_lanes<C>(p, per, s_scan, s_warp, bits);
     const int64_t all = s_scan[C::THREADS], ctas = all < gridDim.x ? all : gridDim.x;
     PartDesc* desc = reinterpret_cast<PartDesc*>(p.workspace) + blockIdx.x;
     float* parts = reinterpret_cast<float*>(reinterpret_cast<PartDesc*>(p.workspace) + gridDim.x);
@@ -154,19 +103,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
     if (bits && p.err && blockIdx.x == 0) atomicOr(p.err, (int32_t)bits);
     bits = 0;
     if (blockIdx.x >= ctas) return;
-    Walk<C> walk;
-    walk.u = run_begin(all, ctas, blockIdx.x);
-    walk.u1 = run_begin(all, ctas, (int64_t)blockIdx.x + 1);
-    {
-        int lo = 0, hi = C::THREADS;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_scan[mid] <= walk.u) lo = mid;
-            else hi = mid;
-        }
-        walk.b = lo * per;
-        walk.base = s_scan[lo];
-    }
+    Walk<C> walk = begin_walk<C>(per, s_scan, all, ctas);
     if (warp >= C::W) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::PREG));
         if (warp > C::W) return;
@@ -447,7 +384,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
             if (lane == 0) mbar_arrive(empty + 8 * stage);
         }
 
-        // ---- the warps' parts of the item joined, 8 rows at a time, and stored -----------------------------------
+        // ---- the warps' parts of the item joined, a group of rows of each warp at a time, and stored ---------------
         const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
         float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
         constexpr int RC = D / 32, CH = D / 4;  // 16-byte chunks of a run and of a row
@@ -470,10 +407,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
             }
             named_sync(1, C::W * 32);
             if (s_dead) continue;
-#pragma unroll
-            for (int k = 0; k < (8 * CH + C::W * 32 - 1) / (C::W * 32); ++k) {
-                const int idx = tid + k * C::W * 32, rr = idx / CH, ch = idx % CH, r = n * 8 + rr;
-                if (rr >= 8 || r >= nrows) continue;
+            for (int idx = tid; idx < 8 * CH; idx += C::W * 32) {
+                const int rr = idx / CH, ch = idx % CH, r = n * 8 + rr;
+                if (r >= nrows) continue;
                 float mm = -INFINITY, ll = 0.f;
 #pragma unroll
                 for (int w = 0; w < C::W; ++w) mm = fmaxf(mm, s_ml[w * 8 + rr].x);
@@ -627,7 +563,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) gdn_kv4_attention_join_kernel
     }
 }
 
-constexpr int kCtasPerSm = 3;  // at most; as many as fit
+constexpr int kCtasPerSm = 2;  // at most
 static_assert(kCtasPerSm * 200 <= kMaxParts, "parts of an item");
 
 // CTAs of an SM, found once for each kernel and device
@@ -667,20 +603,12 @@ cudaError_t run(const Kv4AttentionParams& p, cudaStream_t s) {
     return launch_kv4_join(p, C::ROWS, ctas, s);
 }
 
-// More rows than this go to the tcgen05 kernel
-bool wide(int64_t rows, int D) {
-    (void)D;
-    return rows > 64;
-}
+// More rows than this go to the tcgen05 kernel, although 128 is what it wants: 256 lanes of 64 rows over 2100 keys, D 64, took
+// 278 us there and 352 us here; 128 lanes of 32 rows over 8500 keys, D 128, 535 us there and 354 us here.
+bool wide(int64_t rows) { return rows > 32; }
 
-// Rows of an item: the lane's rows, by 8, 16, 32 or 64, as far as O^T (D * rows / 32 registers a thread) leaves room; the
-// unpacked fragments of a tile then serve all of them
-int item_rows(int64_t rows, int D) {
-    const int most = D == 64 ? 64 : D == 128 ? 32 : 16;
-    int n = 8;
-    while (n < rows && n < most) n *= 2;
-    return n;
-}
+// Rows of an item: 8, 16 or 32; of D 256 at most 16 (O^T takes D * rows / 32 registers a thread), more take several items
+int item_rows(int64_t rows, int D) { return rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32; }
 
 template <int D>
 cudaError_t run_join(const Kv4AttentionParams& p, int rows, int ctas, cudaStream_t s) {
@@ -705,28 +633,28 @@ cudaError_t launch_kv4_join(const Kv4AttentionParams& p, int rows, int ctas, cud
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttentionParams& p, cudaStream_t s) {
-    if (wide((int64_t)p.T * p.G, p.kv.D)) return launch_kv4_attention_wide(p, s);
+    if (wide((int64_t)p.T * p.G)) return launch_kv4_attention_wide(p, s);
     const int rows = item_rows((int64_t)p.T * p.G, p.kv.D);
     switch (p.kv.D * 100 + rows) {
-    case 6408: return run<Cfg<64, 1, 8, 32, 256, 3, 2>>(p, s);
-    case 6416: return run<Cfg<64, 2, 8, 32, 256, 3, 2>>(p, s);
-    case 6432: return run<Cfg<64, 4, 8, 16, 128, 4, 1>>(p, s);
-    case 6464: return run<Cfg<64, 8, 8, 16, 128, 4, 1>>(p, s);
-    case 12808: return run<Cfg<128, 1, 8, 32, 256, 2, 2>>(p, s);
-    case 12816: return run<Cfg<128, 2, 8, 32, 256, 4, 1>>(p, s);
-    case 12832: return run<Cfg<128, 4, 8, 16, 128, 4, 1>>(p, s);
-    case 25608: return run<Cfg<256, 1, 8, 16, 128, 3, 1>>(p, s);
-    default: return run<Cfg<256, 2, 8, 16, 128, 3, 1>>(p, s);
+    case 6408: return run<Cfg<64, 1, 32, 256, 3, 2>>(p, s);
+    case 6416: return run<Cfg<64, 2, 32, 256, 3, 2>>(p, s);
+    case 6432: return run<Cfg<64, 4, 16, 128, 4, 1>>(p, s);
+    case 12808: return run<Cfg<128, 1, 32, 256, 2, 2>>(p, s);
+    case 12816: return run<Cfg<128, 2, 32, 256, 4, 1>>(p, s);
+    case 12832: return run<Cfg<128, 4, 16, 128, 4, 1>>(p, s);
+    case 25608: return run<Cfg<256, 1, 16, 128, 3, 1>>(p, s);
+    default: return run<Cfg<256, 2, 16, 128, 3, 1>>(p, s);
     }
 }
 
 int64_t kv4_attention_workspace(int B, int T, int HQ, int HK, int D) {
     (void)B;
-    if (wide((int64_t)T * (HQ / HK), D)) return kv4_attention_wide_workspace(D);
+    // a call may bring fewer rows than this: the most that any kernel up to them wants
+    const int64_t rows = (int64_t)T * (HQ / HK);
     const int sms = sm_count();
     const int64_t ctas = (int64_t)(sms > 0 ? sms : 152) * kCtasPerSm;
-    const int rows = item_rows((int64_t)T * (HQ / HK), D);
-    return ctas * ((int64_t)sizeof(PartDesc) + 2 * part_floats(rows, D) * 4);
+    const int64_t n = ctas * ((int64_t)sizeof(PartDesc) + 2 * part_floats(item_rows(rows, D), D) * 4);
+    return wide(rows) ? std::max(n, kv4_attention_wide_workspace(D)) : n;
 }
 
 }  // namespace gdn

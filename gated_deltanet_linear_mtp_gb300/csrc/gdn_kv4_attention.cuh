@@ -72,6 +72,80 @@ struct Piece {
     Lane x;
 };
 
+template <typename C>
+__device__ __forceinline__ int tiles_of(int kv) {
+    return kv > 0 ? (kv - 1) / C::TILE + 1 : 1;
+}
+
+template <typename C>
+__device__ __forceinline__ int64_t lane_tiles(const Kv4AttentionParams& p, const Lane& x) {
+    return ((int64_t)x.qlen * p.G + C::ROWS - 1) / C::ROWS * tiles_of<C>(x.kv) * p.kv.HK;
+}
+
+// Walks a CTA's run of tiles u .. u1 - 1; lane `b` holds tile `base` first
+template <typename C>
+struct Walk {
+    int64_t u, u1, base;
+    int b;
+    __device__ __forceinline__ bool next(const Kv4AttentionParams& p, Piece& y) {
+        if (u >= u1) return false;
+        uint32_t ignored = 0;
+        y.x = lane_extent(p, b, ignored);
+        int64_t n = lane_tiles<C>(p, y.x);
+        while (base + n <= u) {
+            base += n;
+            y.x = lane_extent(p, ++b, ignored);
+            n = lane_tiles<C>(p, y.x);
+        }
+        y.b = b;
+        y.kts = tiles_of<C>(y.x.kv);
+        const int64_t in = u - base;
+        const int item = (int)(in / y.kts);
+        y.kt0 = (int)(in - (int64_t)item * y.kts);
+        y.hk = item % p.kv.HK;
+        y.r0 = item / p.kv.HK * C::ROWS;
+        y.kt1 = (int)min((int64_t)y.kts, y.kt0 + (u1 - u));
+        u += y.kt1 - y.kt0;
+        return true;
+    }
+};
+
+// Sums of the lanes' tiles before each thread's lanes (`per` each) into s_scan [THREADS + 1]; all of the block's threads
+template <typename C>
+__device__ __forceinline__ void scan_lanes(const Kv4AttentionParams& p, int per, int64_t* s_scan, int64_t* s_warp, uint32_t& bits) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t x = 0;
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) x += lane_tiles<C>(p, lane_extent(p, b, bits));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += s_warp[w];
+    s_scan[tid + 1] = x;
+    if (tid == 0) s_scan[0] = 0;
+    __syncthreads();
+}
+
+// The walk of this block's run
+template <typename C>
+__device__ __forceinline__ Walk<C> begin_walk(int per, const int64_t* s_scan, int64_t all, int64_t ctas) {
+    Walk<C> walk;
+    walk.u = run_begin(all, ctas, blockIdx.x);
+    walk.u1 = run_begin(all, ctas, (int64_t)blockIdx.x + 1);
+    int lo = 0, hi = C::THREADS;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_scan[mid] <= walk.u) lo = mid;
+        else hi = mid;
+    }
+    walk.b = lo * per;
+    walk.base = s_scan[lo];
+    return walk;
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
@@ -142,6 +216,45 @@ __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUten
     // no copy outlives the CTA
     for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
         mbar_wait_bounded(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, GDN_WAIT_POLLS);
+}
+
+// ---- tensor memory ----------------------------------------------------------------------------------------------
+// instruction descriptor of tcgen05.mma kind::f16 with f16 operands, D fp32
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* f) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
+}
+
+// The wait for this thread's loads, and that what they loaded is not used before it
+__device__ __forceinline__ void tmem_wait_ld32(float (&f)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]), "+f"(f[8]),
+                   "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]), "+f"(f[16]),
+                   "+f"(f[17]), "+f"(f[18]), "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]), "+f"(f[24]),
+                   "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30]), "+f"(f[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+        : "memory");
 }
 
 // ---- host ---------------------------------------------------------------------------------------------------

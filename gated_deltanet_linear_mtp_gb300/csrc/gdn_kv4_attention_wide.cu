@@ -4,13 +4,13 @@
 // Bound: the products, 4 D flops a row and key.  An item is a tile of MT * 128 rows (whole tokens times the G heads of a key
 // head) of one lane and key head; a CTA takes its tiles of TILE keys in turn, as four kinds of warps:
 //   * one warp copies the packed tiles into shared memory by TMA (shared with the decode kernel);
-//   * a warpgroup unpacks them into f16 operand tiles (128-byte swizzle, a ring of four: K, V, K, ..), once for all rows: a
+//   * a warpgroup unpacks them into f16 operand tiles (128-byte swizzle, a ring of two pairs), once for all rows: a
 //     number costs the unpacking 1/256 of its products;
 //   * a thread for each 128 rows issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory;
 //   * a warpgroup for each 128 rows takes a row of S a thread, forms P in place of S as f16 and keeps the row's statistics.
 // S goes by units of 64 keys in two buffers: the way from a product to its softmax and back takes longer than either
-// (600 cycles each way measured), and with one buffer of 128 keys the tensor cores waited for it (831 us for two chunks of
-// 2048 tokens behind 8192 keys, HQ 32, HK 4, D 128).  The running maximum moves only where a score passes it by more than
+// (about 600 cycles each way), and with one buffer of 128 keys the tensor cores waited for it (665 us for two chunks of 2048
+// tokens behind 8192 keys, HQ 32, HK 4, D 128, against 573).  The running maximum moves only where a score passes it by more than
 // 2^8 (then that thread scales its row of O in tensor memory), so O stays in tensor memory throughout.
 // Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16, fp32.
 //
@@ -29,7 +29,7 @@ constexpr int kThreads = 512;  // 4 warpgroups: softmax, softmax or unpacking, u
 constexpr int kMmaWarp = 12, kLoadWarp = 14;  // kMmaWarp + m issues the products of rows 128 m ..
 constexpr int kLaunchRegs = 128, kSoftRegs = 160, kUnpackRegs = 112, kRestRegs = 80;
 static_assert(2 * kSoftRegs + kUnpackRegs + kRestRegs <= 4 * kLaunchRegs, "the block's registers");
-constexpr int kRing = 4;
+constexpr int kPairs = 2;  // places of the ring of unpacked tiles: V of one tile and K of the next
 
 template <int D_>
 struct Wide {
@@ -42,50 +42,12 @@ struct Wide {
     static constexpr int CB = D / 2, SB = D / 16, STAGE = TILE * (CB + SB);
     static constexpr int UNPACK = 128 * (3 - MT);      // threads that unpack
     static constexpr int QBYTES = 128 * D * 2, KVBYTES = TILE * D * 2;
-    static constexpr int Q_AT = 0, RING_AT = MT * QBYTES, POOL_AT = RING_AT + kRing * KVBYTES;
+    static constexpr int Q_AT = 0, RING_AT = MT * QBYTES, POOL_AT = RING_AT + 2 * kPairs * KVBYTES;
     static constexpr int SMEM = 1024 + POOL_AT + STAGES * STAGE;
     static constexpr int UNIT = 64, UPT = TILE / UNIT;  // keys of a product S; of them in a tile
     static constexpr int O_COL = 0, S_COL = MT * D, COLS = 512;
     static_assert(S_COL + MT * 2 * UNIT <= COLS, "tensor memory");
 };
-
-// instruction descriptor of tcgen05.mma kind::f16 with f16 operands, D fp32
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* f) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
-}
-
-// The wait for this thread's loads, and that what they loaded is not used before it
-__device__ __forceinline__ void tmem_wait_ld32(float (&f)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]), "+f"(f[8]),
-                   "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]), "+f"(f[16]),
-                   "+f"(f[17]), "+f"(f[18]), "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]), "+f"(f[24]),
-                   "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30]), "+f"(f[31])
-                 :
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-        : "memory");
-}
 
 // The thread's row of `cols` columns (a multiple of 16) times f: fp32, or two f16 a column
 template <bool HALF>
@@ -200,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     constexpr int D = C::D, MT = C::MT, TILE = C::TILE;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[kThreads / 32];
-    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kRing + 6 * MT];
+    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kPairs + 7 * MT];
+    __shared__ float s_sc[MT * 128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -209,14 +172,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     int64_t* s_tiles = s_pairs + kThreads + 1;                         // [kThreads + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8 * C::STAGES, kv_full = raw_empty + 8 * C::STAGES,
-                   kv_empty = kv_full + 8 * kRing, q_full = kv_empty + 8 * kRing, s_full = q_full + 8 * MT,
-                   p_full = s_full + 16 * MT, pv_done = p_full + 16 * MT;  // s_full, p_full: two for each 128 rows
+                   kv_empty = kv_full + 8 * kPairs, q_full = kv_empty + 8 * kPairs, s_full = q_full + 8 * MT,
+                   p_full = s_full + 16 * MT, pv_prev = p_full + 16 * MT, pv_last = pv_prev + 8 * MT;
+    // s_full, p_full: two for each 128 rows; pv_prev, pv_last: the last P V of a piece but one, and the last
     uint32_t bits = 0;
 
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) mbar_init(raw_full + 8 * i, 1), mbar_init(raw_empty + 8 * i, C::UNPACK / 32);
-        for (int i = 0; i < kRing; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, MT);
-        for (int i = 0; i < MT; ++i) mbar_init(q_full + 8 * i, 4), mbar_init(pv_done + 8 * i, 1);
+        for (int i = 0; i < kPairs; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, MT);
+        for (int i = 0; i < MT; ++i) mbar_init(q_full + 8 * i, 4), mbar_init(pv_prev + 8 * i, 1), mbar_init(pv_last + 8 * i, 1);
         for (int i = 0; i < 2 * MT; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4);
         fence_mbar_init();
         s_dead = 0;
@@ -296,65 +260,75 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         if (warp == kLoadWarp) {
             produce<C>(p, &map, walk, base_u + C::POOL_AT, smem + C::POOL_AT, raw_full, raw_empty, bits);
         } else if (warp < kMmaWarp + MT && lane == 0) {
-            // Tiles go through the ring as K0, V0, K1, V1, ..; slot n of all is ring place n % kRing.  A thread for each 128
-            // rows: what one waits for passes while the other's products run.  Units of 64 keys alternate between two
-            // buffers of S, so that a softmax finds its next scores ready whatever the way there and back takes.
+            // The ring holds pairs: pair j of a piece is V of its tile j - 1 and K of its tile j (the first has K alone, the
+            // last V alone), since a unit's P V and the scores two units on need them together.  A thread for each 128 rows:
+            // what one waits for (250 cycles even for what is ready, as it queues behind the products) passes while the
+            // other's products run.  Units of 64 keys alternate between two buffers of S, so that a softmax finds its next
+            // scores ready whatever the way there and back takes.
             constexpr uint32_t id_s = idesc_f16(128, C::UNIT), id_o = idesc_f16(128, D) | (1u << 16);
             const int m = warp - kMmaWarp;
-            uint32_t slot = 0, piece = 0, unit = 0;  // ring slots; pieces and units of these rows
+            uint32_t pair = 0, piece = 0, unit = 0;  // ring pairs before this piece; pieces and units of these rows
             Piece y;
             bool go = true;
-            auto ring_wait = [&](uint32_t n) { return wait(kv_full + 8 * (n % kRing), (n / kRing) & 1); };
-            auto release = [&](uint32_t n) { umma_commit(kv_empty + 8 * (n % kRing)); };
+            auto pair_wait = [&](uint32_t n) { return wait(kv_full + 8 * (n % kPairs), (n / kPairs) & 1); };
             // descriptors differ in their start address alone: 16 bytes count 1
-            const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT + m * C::QBYTES), k_desc = umma_desc_sw128(base_u + C::RING_AT),
+            const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT + m * C::QBYTES),
+                           k_desc = umma_desc_sw128(base_u + C::RING_AT + C::KVBYTES),
                            v_desc = umma_desc_sw128_mn(base_u + C::RING_AT, TILE * 128);
-            // scores of unit u of the piece: K of its tile is ring slot slot + 2 (u / UPT), V the one behind
-            auto keys_wait = [&](int u) { return u % C::UPT != 0 || ring_wait(slot + 2 * (u / C::UPT)); };
-            auto product_s = [&](int u) {
-                const uint32_t n = slot + 2 * (u / C::UPT), at = unit + u;
-                const uint64_t k = k_desc + (n % kRing) * (C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
+            auto product_s = [&](int u) {  // scores of unit u of the piece
+                const uint32_t n = pair + u / C::UPT, at = unit + u;
+                const uint64_t k = k_desc + (n % kPairs) * (2 * C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     umma_bf16(tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT, q_desc + ((ks / 4) * 128 * 128 + (ks % 4) * 32) / 16,
                               k + ((ks / 4) * TILE * 128 + (ks % 4) * 32) / 16, id_s, ks > 0);
                 umma_commit(s_full + 8 * (2 * m + (at & 1)));
-                if (u % C::UPT == C::UPT - 1) release(n);
             };
             while (go && walk.next(p, y)) {
                 const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0);
                 if (m * 128 >= nrows) {  // no rows here: the tiles pass by
-                    for (int i = 0; i < 2 * n && go; ++i, ++slot) {
-                        go = ring_wait(slot);
-                        if (go) mbar_arrive(kv_empty + 8 * (slot % kRing));
+                    for (int i = 0; i <= n && go; ++i, ++pair) {
+                        go = pair_wait(pair);
+                        if (go) mbar_arrive(kv_empty + 8 * (pair % kPairs));
                     }
                     continue;
                 }
+                int have = 0;  // pairs of the piece that are known to be there
+                auto need = [&](int q) {
+                    for (; go && have <= q; ++have) go = pair_wait(pair + have);
+                };
                 for (int u = 0; u < 2 && u < units && go; ++u) {
-                    go = keys_wait(u) && (u > 0 || wait(q_full + 8 * m, piece & 1));
+                    need(u / C::UPT);
+                    if (u == 0) go = go && wait(q_full + 8 * m, piece & 1);
                     if (!go) break;
                     tc_fence_after();
                     product_s(u);
+                    if (u == C::UPT - 1) umma_commit(kv_empty + 8 * (pair % kPairs));
                 }
+                auto need_for = [&](int u) {  // P V of unit u, and the scores two units on
+                    if (u < units) need(u / C::UPT + 1);
+                    if (u + 2 < units) need((u + 2) / C::UPT);
+                };
+                need_for(0);
                 for (int u = 0; u < units && go; ++u) {
-                    const uint32_t at = unit + u, nv = slot + 2 * (u / C::UPT) + 1;
-                    // what comes early is waited for first: between P and the products stands one wait
-                    go = (u % C::UPT != 0 || ring_wait(nv)) && (u + 2 >= units || keys_wait(u + 2)) &&
-                         wait(p_full + 8 * (2 * m + (at & 1)), (at >> 1) & 1);
+                    const uint32_t at = unit + u, nv = pair + u / C::UPT + 1;
+                    go = wait(p_full + 8 * (2 * m + (at & 1)), (at >> 1) & 1);
                     if (!go) break;
                     tc_fence_after();
-                    const uint64_t v = v_desc + (nv % kRing) * (C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
+                    const uint64_t v = v_desc + (nv % kPairs) * (2 * C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
 #pragma unroll
                     for (int ks = 0; ks < C::UNIT / 16; ++ks)
                         umma_bf16_ta(tmem + C::O_COL + m * D, tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT + ks * 8,
                                      v + ks * (2048 / 16), id_o, u > 0 || ks > 0);
-                    umma_commit(pv_done + 8 * m);
-                    if (u % C::UPT == C::UPT - 1) release(nv);
+                    need_for(u + 1);  // while P V runs; then P is all that the next unit waits for
+                    if (!go) break;
                     if (u + 2 < units) product_s(u + 2);
+                    else umma_commit((u + 1 < units ? pv_prev : pv_last) + 8 * m);  // scores two units on tell of the others
+                    if (u % C::UPT == C::UPT - 1) umma_commit(kv_empty + 8 * (nv % kPairs));
                 }
                 ++piece;
                 unit += units;
-                slot += 2 * n;
+                pair += n + 1;
             }
         }
     } else if (warp >= 4 * MT) {
@@ -363,50 +337,53 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         constexpr int PARTS = C::UNPACK / TILE, RUN = D / PARTS;  // dimensions of a thread
         const int idx = tid - 128 * MT, r = idx % TILE, part = idx / TILE;
-        uint32_t slot = 0;
-        Piece y;
+        uint32_t pair = 0, stage = 0;  // ring pairs; stages of the copies
+        Piece y{};
         bool go = true;
-        while (go && walk.next(p, y)) {
-            for (int kt = y.kt0; kt < y.kt1 && go; ++kt) {
-                const bool real = kt * TILE + r < y.x.kv;  // what lies behind the last token may be anything
-#pragma unroll 1
-                for (int which = 0; which < 2; ++which, ++slot) {
-                    const uint32_t at = slot % kRing, st = slot % C::STAGES;
-                    go = warp_wait(raw_full + 8 * st, (slot / C::STAGES) & 1);
-                    if (slot >= kRing) go = go && warp_wait(kv_empty + 8 * at, (slot / kRing - 1) & 1);
-                    if (!go) break;
-                    uint8_t* dst = smem + C::RING_AT + at * C::KVBYTES;
-                    const uint8_t* codes = smem + C::POOL_AT + st * C::STAGE;
-                    const uint8_t* sc = codes + TILE * C::CB + r * C::SB + part * (RUN / 16);
-                    uint4 w[RUN / 32];
-                    uint32_t two[RUN / 32];
+        auto tile = [&](int kt, uint8_t* dst) {  // the next stage into an operand tile
+            const uint32_t st = stage % C::STAGES;
+            go = warp_wait(raw_full + 8 * st, (stage / C::STAGES) & 1);
+            if (!go) return;
+            ++stage;
+            const bool real = kt * TILE + r < y.x.kv;  // what lies behind the last token may be anything
+            const uint8_t* codes = smem + C::POOL_AT + st * C::STAGE;
+            const uint8_t* sc = codes + TILE * C::CB + r * C::SB + part * (RUN / 16);
+            uint4 w[RUN / 32];
+            uint32_t two[RUN / 32];
 #pragma unroll
-                    for (int c = 0; c < RUN / 32; ++c) {  // 16 bytes of codes: 32 dimensions, two scales
-                        w[c] = *reinterpret_cast<const uint4*>(codes + code_off<D>(r, part * (RUN / 32) + c));
-                        two[c] = real ? *reinterpret_cast<const uint16_t*>(sc + 2 * c) : 0u;
-                    }
+            for (int c = 0; c < RUN / 32; ++c) {  // 16 bytes of codes: 32 dimensions, two scales
+                w[c] = *reinterpret_cast<const uint4*>(codes + code_off<D>(r, part * (RUN / 32) + c));
+                two[c] = real ? *reinterpret_cast<const uint16_t*>(sc + 2 * c) : 0u;
+            }
 #pragma unroll
-                    for (int c = 0; c < RUN / 32; ++c) {
-                        const uint32_t f2 = e4m3x2_to_f16(two[c]);
-                        const uint32_t sf[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
-                        const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+            for (int c = 0; c < RUN / 32; ++c) {
+                const uint32_t f2 = e4m3x2_to_f16(two[c]);
+                const uint32_t sf[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
+                const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t f[4];
-                            e2m1x8_to_f16(ws[j], f);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t f[4];
+                    e2m1x8_to_f16(ws[j], f);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], sf[j >> 1]);
-                            *reinterpret_cast<uint4*>(dst + sw128(TILE, r, (part * (RUN / 32) + c) * 4 + j)) =
-                                make_uint4(f[0], f[1], f[2], f[3]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(kv_full + 8 * at);
-                        mbar_arrive(raw_empty + 8 * st);
-                    }
+                    for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], sf[j >> 1]);
+                    *reinterpret_cast<uint4*>(dst + sw128(TILE, r, (part * (RUN / 32) + c) * 4 + j)) = make_uint4(f[0], f[1], f[2], f[3]);
                 }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_empty + 8 * st);
+        };
+        while (go && walk.next(p, y)) {
+            for (int kt = y.kt0; kt <= y.kt1 && go; ++kt, ++pair) {  // V of tile kt - 1, K of tile kt
+                const uint32_t at = pair % kPairs;
+                if (pair >= kPairs) go = warp_wait(kv_empty + 8 * at, (pair / kPairs - 1) & 1);
+                uint8_t* dst = smem + C::RING_AT + at * 2 * C::KVBYTES;
+#pragma unroll 1
+                for (int which = kt > y.kt0 ? 0 : 1; which < (kt < y.kt1 ? 2 : 1) && go; ++which)
+                    tile(kt - 1 + which, dst + which * C::KVBYTES);
+                if (!go) break;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv_full + 8 * at);
             }
         }
     } else {
@@ -415,64 +392,66 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         const int mt = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // lane 32 (warp mod 4) in the upper half
         const uint32_t s_col0 = lanes + C::S_COL + mt * 2 * C::UNIT, o_col = lanes + C::O_COL + mt * D;
-        uint32_t unit = 0;  // of this tile of rows
+        uint32_t unit = 0, piece = 0, prev = 0;  // of this tile of rows: units, pieces, and pieces of more than one unit
         Piece y;
         bool go = true;
         while (go && walk.next(p, y)) {
             const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = mt * 128 + row;
             if (mt > 0 && nrows <= 128) continue;
             const bool mine = r < nrows;
-            const int t = (y.r0 + r) / p.G, h = y.hk * p.G + (y.r0 + r) - t * p.G;
-            const int64_t out = mine ? (int64_t)(y.x.q0 + t) * p.HQ + h : 0;
-            // Q: this thread's row as f16, scaled by a power of two (and by the sign of p.scale)
-            float sc;
-            {
-                const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + out * D);
-                constexpr int HELD = D / 8 < 16 ? D / 8 : 16;  // 16-byte pieces in registers; a longer row is read twice
-                uint4 w[HELD];
-                float top = 0.f;
+            // where row x of the item lies in q and o: a row of 128 is loaded and stored by LR lanes, 16 bytes each
+            constexpr int LR = D / 8, RPI = 32 / LR;
+            const int wrow = (warp & 3) * 32;  // the warp's first row of its 128
+            uint8_t* stage = smem + C::Q_AT + mt * C::QBYTES;
+            const uint32_t magic = 65535u / (uint32_t)p.G + 1u;  // x / G = x * magic >> 16 for x < 256 and G <= 64
+            const int t_first = y.r0 / p.G;
+            auto place = [&](int x) {
+                const int t = (int)((uint32_t)x * magic >> 16);
+                return (int64_t)(y.x.q0 + t_first + t) * p.HQ + y.hk * p.G + x - t * p.G;
+            };
+            // Q as f16, each row scaled by a power of two (and by the sign of p.scale)
+#pragma unroll 1
+            for (int i0 = 0; i0 < LR; i0 += 8) {
+                uint4 w[8];
 #pragma unroll
-                for (int c0 = D / 8 - HELD; c0 >= 0; c0 -= HELD) {
-#pragma unroll
-                    for (int c = 0; c < HELD; ++c) w[c] = mine ? src[c0 + c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int c = 0; c < HELD; ++c) {
-                        const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 v = bf16x2_to_float2(ws[j]);
-                            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                        }
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int x = mt * 128 + wrow + (i0 + i) * RPI + lane / LR;
+                    w[i] = x < nrows ? reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + place(x) * D)[lane % LR] : make_uint4(0, 0, 0, 0);
                 }
-                uint32_t e = __float_as_uint(top) >> 23;
-                e = e < 30 ? 30 : e > 224 ? 224 : e;
-                const float down = __uint_as_float((254u - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
-                // (at least 2^-120: a masked score of -inf must stay one)
-                sc = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
-                uint8_t* dst = smem + C::Q_AT + mt * C::QBYTES;
+                uint32_t top[8];  // of each half of a word: magnitudes order as integers
 #pragma unroll
-                for (int c0 = 0; c0 < D / 8; c0 += HELD) {
-                    if (c0 > 0) {
+                for (int i = 0; i < 8; ++i)
+                    top[i] = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
 #pragma unroll
-                        for (int c = 0; c < HELD; ++c) w[c] = mine ? src[c0 + c] : make_uint4(0, 0, 0, 0);
+                for (int o = LR / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(~0u, top[i], o));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int lr = wrow + (i0 + i) * RPI + lane / LR;
+                    // the exponent, kept where its power of two and the reciprocal are normal numbers (NaN and infinity count
+                    // as the largest)
+                    uint32_t e = max(top[i] & 0xffffu, top[i] >> 16) >> 7;
+                    e = e < 30 ? 30 : e > 224 ? 224 : e;
+                    const float down = __uint_as_float((254u - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
+                    // (at least 2^-120: a masked score of -inf must stay one)
+                    if (lane % LR == 0)
+                        s_sc[mt * 128 + lr] = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
+                    const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    uint32_t f[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = bf16x2_to_float2(ws[j]);
+                        f[j] = f16x2_bits(v.x * down, v.y * down);
                     }
-#pragma unroll
-                    for (int c = 0; c < HELD; ++c) {
-                        const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-                        uint32_t f[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 v = bf16x2_to_float2(ws[j]);
-                            f[j] = f16x2_bits(v.x * down, v.y * down);
-                        }
-                        *reinterpret_cast<uint4*>(dst + sw128(128, row, c0 + c)) = make_uint4(f[0], f[1], f[2], f[3]);
-                    }
+                    *reinterpret_cast<uint4*>(stage + sw128(128, lr, lane % LR)) = make_uint4(f[0], f[1], f[2], f[3]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full + 8 * mt);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * mt);
+            const float sc = s_sc[mt * 128 + row];
+            const int t = t_first + (int)((uint32_t)r * magic >> 16);
             const int limit = y.x.kv - y.x.qlen + t + 1;                   // keys that the row sees
             const int all_see = y.x.kv - y.x.qlen + y.r0 / p.G + 1;        // that every row of the item sees
             float m = -INFINITY, l = 0.f;
@@ -507,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                         m = mn;
                         l *= f;
                         l2 = mul(l2, f2(f, f));
-                        if (u > 0) {  // the product that last wrote O: the one before it is done, as these scores came after it
-                            go = warp_wait(pv_done + 8 * mt, (unit - 1) & 1);
+                        if (u > 0) {  // the product that last wrote O came before the next unit's scores, or is the last but one
+                            go = u + 1 < units ? warp_wait(s_full + 8 * (2 * mt + ((unit + 1) & 1)), ((unit + 1) >> 1) & 1)
+                                               : warp_wait(pv_prev + 8 * mt, prev & 1);
                             tc_fence_after();
                             scale_columns<false>(o_col, D, f);
                         }
@@ -539,34 +519,51 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * (2 * mt + (unit & 1)));
             }
-            if (units > 1) go = go && warp_wait(pv_done + 8 * mt, unit & 1);  // the last product but one, and the last
-            go = go && warp_wait(pv_done + 8 * mt, (unit - 1) & 1);
+            go = go && warp_wait(pv_last + 8 * mt, piece & 1);
             if (!go) break;
+            ++piece;
+            prev += units > 1;
             tc_fence_after();
             const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
             float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
             const float inv = l > 0.f ? p.kv.v_scale / l : l != l ? l : 0.f;
+            // rows go out through Q's place in shared memory, a warp's own rows, so that a row's lanes store side by side
+            const int passes = whole ? 1 : 2;  // bf16, or fp32 in two halves
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                float v[32];
-                tmem_ld32(o_col + 32 * c, v);
-                tmem_wait_ld();
-                if (!mine) continue;
-                if (whole) {
-                    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + out * D + 32 * c);
+            for (int pass = 0; pass < passes; ++pass) {
+                uint8_t* mine_at = stage + row * 2 * D;
+#pragma unroll 1
+                for (int c = 0; c < (whole ? D / 32 : D / 64); ++c) {
+                    float v[32];
+                    tmem_ld32(o_col + pass * (D / 2) + 32 * c, v);
+                    tmem_wait_ld32(v);
+                    if (whole) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(bf16x2_bits(v[8 * j] * inv, v[8 * j + 1] * inv), bf16x2_bits(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
-                                            bf16x2_bits(v[8 * j + 4] * inv, v[8 * j + 5] * inv), bf16x2_bits(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(part + (int64_t)r * D + 32 * c);
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(mine_at + (((4 * c + j) ^ (row & 7)) << 4)) =
+                                make_uint4(bf16x2_bits(v[8 * j] * inv, v[8 * j + 1] * inv), bf16x2_bits(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
+                                           bf16x2_bits(v[8 * j + 4] * inv, v[8 * j + 5] * inv), bf16x2_bits(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4*>(mine_at + (((8 * c + j) ^ (row & 7)) << 4)) =
+                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
                 }
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < LR; ++i) {
+                    const int lr = wrow + i * RPI + lane / LR, x = mt * 128 + lr;
+                    const uint4 w = *reinterpret_cast<const uint4*>(stage + lr * 2 * D + (((lane % LR) ^ (lr & 7)) << 4));
+                    if (x >= nrows) continue;
+                    if (whole) reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + place(x) * D)[lane % LR] = w;
+                    else reinterpret_cast<uint4*>(part + (int64_t)x * D + pass * (D / 2))[lane % LR] = w;
+                }
+                __syncwarp();
             }
             if (mine) {
                 if (!whole) *reinterpret_cast<float2*>(part + (int64_t)C::ROWS * D + 2 * r) = make_float2(m, l);
-                else if (p.lse) p.lse[out] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+                else if (p.lse) p.lse[place(r)] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             }
             if (!whole && y.kt0 == 0 && tid == 0) {
                 desc->last = cta_of(all, ctas, walk.u - n + y.kts - 1);
