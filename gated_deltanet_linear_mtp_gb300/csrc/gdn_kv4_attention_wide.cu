@@ -49,17 +49,17 @@ struct Wide {
     static_assert(S_COL + MT * 2 * UNIT <= COLS, "tensor memory");
 };
 
-// The thread's row of `cols` columns (a multiple of 16) times f: fp32, or two f16 a column
+// The thread's row of `cols` columns (a multiple of 8) times f: fp32, or two f16 a column
 template <bool HALF>
 __device__ __noinline__ void scale_columns(uint32_t col, int cols, float f) {
     tmem_wait_st();
-    for (int c = 0; c < cols; c += 16) {
+    for (int c = 0; c < cols; c += 8) {
         float v[16];
-        uint32_t w[16];
-        tmem_ld16(col + c, v);
-        tmem_wait_ld();
+        uint32_t w[8];
+        tmem_ld16(col + c, v);  // of which the first 8 are used
+        tmem_wait_ld16(v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
             if (HALF) {
                 const uint32_t b = __float_as_uint(v[j]);
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&b));
@@ -68,7 +68,7 @@ __device__ __noinline__ void scale_columns(uint32_t col, int cols, float f) {
                 w[j] = __float_as_uint(v[j] * f);
             }
         }
-        tmem_st16(col + c, w);
+        tmem_st8(col + c, w);
     }
     tmem_wait_st();
 }
@@ -463,21 +463,22 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 const int first = y.kt0 * TILE + u * C::UNIT;
                 const bool mask = first + C::UNIT > all_see;
                 F2 l2 = f2(0.f, 0.f);
-                // 32 columns at a time: P's 16 columns go where S has been read
-                auto chunk = [&](float (&x)[32], int c) {
+                // 16 columns at a time, P's 8 where S has been read, and not unrolled: the loop's instructions stay in the
+                // scheduler's cache, which four kinds of warps share (unrolled over all 64 columns 595 us against 540)
+#pragma unroll 1
+                for (int c = 0; c < C::UNIT; c += 16) {
+                    float x[16];
+                    tmem_ld16(s_col + c, x);
+                    tmem_wait_ld16(x);
                     if (mask) {
-                        const int lim = limit - first - 32 * c;
+                        const int lim = limit - first - c;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < 16; ++j)
                             if (j >= lim) x[j] = -INFINITY;
                     }
                     float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int j = 4; j < 28; j += 8)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[j + k]), x[j + 4 + k]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], x[28 + k]);
+                    for (int j = 4; j < 16; ++j) t4[j & 3] = fmaxf(t4[j & 3], x[j]);
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
                     const bool move = top > m + kSlack;
                     if (__any_sync(~0u, move)) {
@@ -492,26 +493,19 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                             tc_fence_after();
                             scale_columns<false>(o_col, D, f);
                         }
-                        scale_columns<true>(s_col, 16 * c, f);
+                        scale_columns<true>(s_col, c / 2, f);
                     }
                     const float mm = m == -INFINITY ? 0.f : -m;
-                    uint32_t w[16];
+                    uint32_t w[8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         const float2 z = split(fma(f2(x[2 * j], x[2 * j + 1]), f2(sc, sc), f2(mm, mm)));
                         const float a = exp2_fast(z.x), b = exp2_fast(z.y);
                         l2 = add(l2, f2(a, b));
                         w[j] = f16x2_bits(a, b);
                     }
-                    tmem_st16(s_col + 16 * c, w);
-                };
-                float xa[32], xb[32];
-                tmem_ld32(s_col, xa);
-                tmem_ld32(s_col + 32, xb);
-                tmem_wait_ld32(xa);
-                tmem_wait_ld32(xb);
-                chunk(xa, 0);
-                chunk(xb, 1);
+                    tmem_st8(s_col + c / 2, w);
+                }
                 const float2 ls = split(l2);
                 l += ls.x + ls.y;
                 tmem_wait_st();
@@ -533,20 +527,20 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             for (int pass = 0; pass < passes; ++pass) {
                 uint8_t* mine_at = stage + row * 2 * D;
 #pragma unroll 1
-                for (int c = 0; c < (whole ? D / 32 : D / 64); ++c) {
-                    float v[32];
-                    tmem_ld32(o_col + pass * (D / 2) + 32 * c, v);
-                    tmem_wait_ld32(v);
+                for (int c = 0; c < (whole ? D : D / 2); c += 16) {
+                    float v[16];
+                    tmem_ld16(o_col + pass * (D / 2) + c, v);
+                    tmem_wait_ld16(v);
                     if (whole) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4*>(mine_at + (((4 * c + j) ^ (row & 7)) << 4)) =
+                        for (int j = 0; j < 2; ++j)
+                            *reinterpret_cast<uint4*>(mine_at + (((c / 8 + j) ^ (row & 7)) << 4)) =
                                 make_uint4(bf16x2_bits(v[8 * j] * inv, v[8 * j + 1] * inv), bf16x2_bits(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
                                            bf16x2_bits(v[8 * j + 4] * inv, v[8 * j + 5] * inv), bf16x2_bits(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4*>(mine_at + (((8 * c + j) ^ (row & 7)) << 4)) =
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4*>(mine_at + (((c / 4 + j) ^ (row & 7)) << 4)) =
                                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     }
                 }
