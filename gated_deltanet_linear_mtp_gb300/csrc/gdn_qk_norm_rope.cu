@@ -138,6 +138,14 @@ __device__ __forceinline__ float div_odd(float a, float b) {
     return fmaf(q, b, -a) != 0.f ? __uint_as_float(__float_as_uint(q) | 1u) : q;
 }
 
+// The largest magnitude of eight numbers, by their bits: NaN where one is among them, else infinity
+__device__ __forceinline__ float largest(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    return __uint_as_float(m);
+}
+
 // Where a token's row of the cache lies
 struct Slot {
     int64_t page;
@@ -289,25 +297,31 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int step = NG / side, sub = grp / step, mine = grp - sub * step;
     const Chunks<INTER> ch(l, p.R);
 
-    // where a row's two chunks are read: values lie in neighbouring chunks
+    // where a row's two chunks are read (values lie in neighbouring chunks) and written, and the way to the group's next token
     const T* src[U];
-    int64_t hop[U];
+    T* dst[U];
+    int64_t hop[U], out_hop[U];
     int gap[U];
+    bool mine_here[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = mine + u * step + r0;
         const bool q = r < p.HQ, k = r < p.HQ + p.HK;
-        const int64_t stride = q ? p.q_stride : k ? p.k_stride : p.v_stride;
+        const int64_t stride = q ? p.q_stride : k ? p.k_stride : p.v_stride, out_stride = (int64_t)(q ? p.HQ : p.HK) * D;
+        T* out = k ? (T*)(q ? p.q_out : p.k_out) : nullptr;
+        mine_here[u] = mine + u * step < nr;
         src[u] = (q ? (const T*)p.q + (int64_t)r * D : k ? (const T*)p.k + (int64_t)(r - p.HQ) * D : (const T*)p.v + (int64_t)(r - p.HQ - p.HK) * D) +
                  (t0 + sub) * stride + (k ? ch.a * 4 : l * 8);
+        dst[u] = out ? out + (t0 + sub) * out_stride + (int64_t)(q ? r : r - p.HQ) * D + ch.a * 4 : nullptr;
         hop[u] = stride * side;
+        out_hop[u] = out ? out_stride * side : 0;
         gap[u] = k ? (ch.b - ch.a) * 4 : 4;
     }
     typename Quad<T>::Raw raw[U][2];
     auto fetch = [&](int i) {  // the group's rows of the CTA's token i
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i < nt && mine + u * step < nr) {
+            if (i < nt && mine_here[u]) {
                 raw[u][0] = Quad<T>::load(src[u]);
                 raw[u][1] = Quad<T>::load(src[u] + gap[u]);
             }
@@ -334,6 +348,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             co = *reinterpret_cast<const float4*>(cs + i * H + 4 * l);
             si = *reinterpret_cast<const float4*>(sn + i * H + 4 * l);
         }
+        const F2 c2[2] = {f2(co.x, co.y), f2(co.z, co.w)}, s2[2] = {f2(si.x, si.y), f2(si.z, si.w)};
+        const F2 n2[2] = {f2(-si.x, -si.y), f2(-si.z, -si.w)};
         Slot slot{0, 0, false};
         if (STORE && mine + r0 + (U - 1) * step >= p.HQ) {
             const int32_t s = p.slot_map[t];
@@ -343,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = mine + u * step + r0;
-            if (mine + u * step >= nr) continue;  // the same for all lanes of a row
+            if (!mine_here[u]) continue;  // the same for all lanes of a row
             F2 x[2][2];
             Quad<T>::unpack(raw[u][0], x[0]);
             Quad<T>::unpack(raw[u][1], x[1]);
@@ -351,20 +367,19 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             if (is_v) {
                 if constexpr (STORE) {
                     if (!slot.ok) continue;
-                    float v[8], top = 0.f;
-                    bool odd = false;
+                    float v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 a = split(x[j >> 1][j & 1]);
                         v[2 * j] = a.x, v[2 * j + 1] = a.y;
                     }
+                    float top = largest(v);
+                    if (!(top <= kMaxF32)) {
+                        bits |= GDN_ERRBIT_NONFINITE;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        odd |= !(fabsf(v[j]) <= kMaxF32);
-                        v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -kMaxF32), kMaxF32);
-                        top = fmaxf(top, fabsf(v[j]));
+                        for (int j = 0; j < 8; ++j) v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -kMaxF32), kMaxF32);
+                        top = largest(v);
                     }
-                    if (odd) bits |= GDN_ERRBIT_NONFINITE;
                     top = fmaxf(top, __shfl_xor_sync(gmask, top, 1));
                     const uint32_t sb = f32_to_e4m3(div_odd(fminf(top / p.kv.v_scale, kMaxF32), 6.f));
                     const float s = e4m3_to_f32(sb) * p.kv.v_scale, inv = 1.f / s;
@@ -419,8 +434,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                         z[j >> 1][j & 1] = f2(fmaf(a.x, c4[j], -a.y * s4[j]), fmaf(a.y, c4[j], a.x * s4[j]));
                     }
                 } else {
-                    const F2 c2[2] = {f2(co.x, co.y), f2(co.z, co.w)}, s2[2] = {f2(si.x, si.y), f2(si.z, si.w)};
-                    const F2 n2[2] = {f2(-si.x, -si.y), f2(-si.z, -si.w)};
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         z[0][j] = fma(y[0][j], c2[j], mul(y[1][j], n2[j]));
@@ -428,11 +441,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                     }
                 }
             }
-            T* out = is_k ? (T*)p.k_out : (T*)p.q_out;
-            if (out) {
-                out += ((int64_t)t * (is_k ? p.HK : p.HQ) + (is_k ? r - p.HQ : r)) * D;
-                Quad<T>::store(out + ch.a * 4, z[0]);
-                Quad<T>::store(out + ch.b * 4, z[1]);
+            if (dst[u]) {
+                Quad<T>::store(dst[u], z[0]);
+                Quad<T>::store(dst[u] + gap[u], z[1]);
+                dst[u] += out_hop[u];
             }
             if constexpr (STORE) {
                 if (!is_k || !slot.ok) continue;
@@ -442,12 +454,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                 float v[8], e[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 a = split(z[j >> 1][j & 1]);
+                    const float2 a = split(z[j >> 1][j & 1]), b = split(y[j >> 1][j & 1]);
                     v[2 * j] = a.x, v[2 * j + 1] = a.y;
-                    if (INTER) {
-                        const float2 b = split(y[j >> 1][j & 1]);
-                        e[j] = fabsf(b.x) + fabsf(b.y);
-                    }
+                    if (INTER) e[j] = fabsf(b.x) + fabsf(b.y);
                 }
                 if (!INTER) {
 #pragma unroll
@@ -457,19 +466,24 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                         e[2 * j + 1] = fabsf(a.y) + fabsf(b.y);
                     }
                 }
-                bool odd = false;
-                float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
+                const bool odd = !(largest(v) <= kMaxF32);
+                if (odd) {
+                    bits |= GDN_ERRBIT_NONFINITE;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = e[j] <= kMaxF32 ? e[j] * 0x1p-19f : 0.f;
-                auto bound = [&](int j) { return INTER ? e[j >> 1] : e[j & 3]; };
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -kMaxF32), kMaxF32);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    odd |= !(fabsf(v[j]) <= kMaxF32);
-                    v[j] = v[j] == v[j] ? v[j] : 0.f;
-                    lo[j >> 2] = fmaxf(lo[j >> 2], fabsf(v[j]) - bound(j));
-                    hi[j >> 2] = fmaxf(hi[j >> 2], fabsf(v[j]) + bound(j));
+                    for (int j = 0; j < 4; ++j) e[j] = e[j] <= kMaxF32 ? e[j] : 0.f;
                 }
-                if (odd) bits |= GDN_ERRBIT_NONFINITE;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] *= 0x1p-19f;
+                auto bound = [&](int j) { return INTER ? e[j >> 1] : e[j & 3]; };
+                float lo[2], hi[2];  // between which a chunk's largest lies
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float m = fmaxf(fmaxf(fabsf(v[4 * k]), fabsf(v[4 * k + 1])), fmaxf(fabsf(v[4 * k + 2]), fabsf(v[4 * k + 3])));
+                    const float d = INTER ? fmaxf(e[2 * k], e[2 * k + 1]) : fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+                    lo[k] = m - d, hi[k] = m + d;
+                }
                 // the maxima of a group's four chunks, whichever lanes hold them
                 float2* ex = s_ex[tid >> 5] + (tid & 31) / LPR * (D / 4);
                 ex[ch.a] = make_float2(lo[0], hi[0]);
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                 for (int k = 0; k < 2; ++k) {
                     const int c = k ? ch.b : ch.a;
                     const float4 m0 = *reinterpret_cast<const float4*>(ex + (c & ~3)), m1 = *reinterpret_cast<const float4*>(ex + (c & ~3) + 2);
-                    const float low = fmaxf(fmaxf(m0.x, m0.z), fmaxf(m1.x, m1.z)) * inv * (1.f / 6.f) * (1.f - 0x1p-21f);
+                    const float low = fmaxf(fmaxf(fmaxf(m0.x, m0.z), fmaxf(m1.x, m1.z)), 0.f) * inv * (1.f / 6.f) * (1.f - 0x1p-21f);
                     const float high = fmaxf(fmaxf(m0.y, m0.w), fmaxf(m1.y, m1.w)) * inv * (1.f / 6.f) * (1.f + 0x1p-21f);
                     const uint32_t sb = f32_to_e4m3(low);
                     diff |= sb ^ f32_to_e4m3(high);
@@ -490,10 +504,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                     uint32_t w = 0;
 #pragma unroll
                     for (int j = 4 * k; j < 4 * k + 4; j += 2) {
-                        const float a = fabsf(v[j]), b = fabsf(v[j + 1]);
-                        const uint32_t b0 = f32x2_to_e2m1(fmaxf(a - bound(j), 0.f) * rsc, fmaxf(b - bound(j + 1), 0.f) * rsc);
-                        diff |= b0 ^ f32x2_to_e2m1((a + bound(j)) * rsc, (b + bound(j + 1)) * rsc);
-                        w |= (b0 | (v[j] < 0.f ? 8u : 0u) | (v[j + 1] < 0.f ? 0x80u : 0u)) << (4 * (j & 3));
+                        // the codes of v and, sign apart, of both ends of where the exact value lies: the bounds grow with |v|,
+                        // so that the end towards 0 may pass it only where both ends' codes are 0
+                        const F2 q = mul(f2(v[j], v[j + 1]), f2(rsc, rsc));
+                        const float ea = bound(j) * rsc, eb = bound(j + 1) * rsc;
+                        const float2 low = split(add(q, f2(-ea, -eb))), high = split(add(q, f2(ea, eb)));
+                        const float2 mid = split(q);
+                        const uint32_t b0 = f32x2_to_e2m1(low.x, low.y), b1 = f32x2_to_e2m1(high.x, high.y);
+                        diff |= (b0 ^ b1) & 0x77u;
+                        w |= ((b0 & 0x77u) | (mid.x < 0.f ? 8u : 0u) | (mid.y < 0.f ? 0x80u : 0u)) << (4 * (j & 3));
                     }
                     *reinterpret_cast<uint16_t*>(p.kv.codes + row * (D / 2) + c * 2) = (uint16_t)w;
                     if ((c & 3) == 0) p.kv.scales[row * (D / 16) + c / 4] = (uint8_t)sb;
