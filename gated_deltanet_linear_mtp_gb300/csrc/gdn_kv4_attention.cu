@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + 8 * stage);
+            if (lane == 0 && !dead) mbar_arrive(empty + 8 * stage);  // (a stage whose copy never came is not filled again)
         }
 
         // ---- the warps' parts of the item joined, a group of rows of each warp at a time, and stored ---------------

@@ -203,6 +203,9 @@ __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUten
 #pragma unroll
                     for (int i = 0; i < KINDS; ++i) {
                         const int which = part + i;
+#ifdef GDN_TEST_MISSING_COPY
+                        if (blockIdx.x == 0 && it == 0 && which == 0 && lane == 0) continue;
+#endif
                         tma_load_4d(st + (i * C::TILE + lane * PR) * C::CB, map, 0, off, which * HK + y.hk, pg, bar);
                         const int64_t row = (((int64_t)pg * 2 + which) * HK + y.hk) * P + off;
                         bulk_g2s(st + KINDS * C::TILE * C::CB + (i * C::TILE + lane * PR) * C::SB, p.kv.scales + row * C::SB,

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     constexpr int D = C::D, MT = C::MT, TILE = C::TILE;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[kThreads / 32];
-    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kPairs + 7 * MT];
+    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kPairs + 8 * MT];
     __shared__ float s_sc[MT * 128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
@@ -173,14 +173,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8 * C::STAGES, kv_full = raw_empty + 8 * C::STAGES,
                    kv_empty = kv_full + 8 * kPairs, q_full = kv_empty + 8 * kPairs, s_full = q_full + 8 * MT,
-                   p_full = s_full + 16 * MT, pv_prev = p_full + 16 * MT, pv_last = pv_prev + 8 * MT;
-    // s_full, p_full: two for each 128 rows; pv_prev, pv_last: the last P V of a piece but one, and the last
+                   p_full = s_full + 16 * MT, pv_prev = p_full + 16 * MT, pv_last = pv_prev + 8 * MT,
+                   idle = pv_last + 8 * MT;
+    // s_full, p_full: two for each 128 rows; pv_prev, pv_last: the last P V of a piece but one, and the last; idle: all
+    // products are done
     uint32_t bits = 0;
 
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) mbar_init(raw_full + 8 * i, 1), mbar_init(raw_empty + 8 * i, C::UNPACK / 32);
         for (int i = 0; i < kPairs; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, MT);
-        for (int i = 0; i < MT; ++i) mbar_init(q_full + 8 * i, 4), mbar_init(pv_prev + 8 * i, 1), mbar_init(pv_last + 8 * i, 1);
+        for (int i = 0; i < MT; ++i) mbar_init(q_full + 8 * i, 4), mbar_init(pv_prev + 8 * i, 1), mbar_init(pv_last + 8 * i, 1), mbar_init(idle + 8 * i, 1);
         for (int i = 0; i < 2 * MT; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4);
         fence_mbar_init();
         s_dead = 0;
@@ -330,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 unit += units;
                 pair += n + 1;
             }
+            umma_commit(idle + 8 * m);  // no product outlives the CTA's memory, whatever wait ran out
+            if (!mbar_wait_bounded(idle + 8 * m, 0, GDN_WAIT_POLLS)) bits |= GDN_ERRBIT_TIMEOUT;
         }
     } else if (warp >= 4 * MT) {
         // ---- unpacking: thread (row, part of its dimensions) -------------------------------------------------
