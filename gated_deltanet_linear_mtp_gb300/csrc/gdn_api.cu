@@ -522,9 +522,11 @@ gdn_status gdn_page_plan(int32_t B, int32_t N, int32_t page_size, int32_t max_pa
                           (const void*)out->positions, (const void*)out->slot_map, (const void*)out->total_lens,
                           (const void*)out->held, (const void*)out->taken, (const void*)ticket, (const void*)err_word})
         if (!aligned(q, 4)) return GDN_ERR_ALIGN;
-    const PagePlanParams p{B,          N,     page_size,       max_pages,      num_pages,     kv_lens,         new_lens,
-                           block_tables, held, free_pages,      taken,          out->cu_seqlens, out->positions,
-                           out->slot_map, out->total_lens, out->held, out->taken, ticket,       err_word};
+    int shift = 4;
+    while (1 << shift < page_size) ++shift;
+    const PagePlanParams p{B,     N,       page_size, shift, max_pages, num_pages, kv_lens, new_lens, block_tables, held,
+                           free_pages, taken, out->cu_seqlens, out->positions, out->slot_map, out->total_lens, out->held,
+                           out->taken, ticket, err_word};
     return finish(launch_page_plan(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

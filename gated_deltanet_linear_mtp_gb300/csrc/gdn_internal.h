@@ -111,7 +111,7 @@ struct GatedNormParams {
 
 // One step's block tables, slot map, positions and offsets from the lanes' lengths (gdn_page_plan.cu).
 struct PagePlanParams {
-    int B, N, page_size, max_pages, num_pages;
+    int B, N, page_size, page_shift, max_pages, num_pages;
     const int32_t* kv_lens;
     const int32_t* new_lens;
     int32_t* block_tables;  // [B, max_pages]

@@ -7,7 +7,7 @@
 //
 // Latency bound: a step's lengths and tokens are a few KB to a few MB.  So one launch does everything: every CTA scans
 // all lanes' lengths by itself (B values from L2; cheaper than a second launch or a wait between CTAs) and then writes
-// its own slice of the lanes' tables and of the tokens, finding a token's lane by binary search in shared memory.  A
+// its own slice of the tables and of the tokens, finding a token's lane by binary search in shared memory.  A
 // new page is taken from the free list directly, so no CTA reads what another one writes; held and taken, which the
 // caller may update in place, are written by the last CTA to finish, after all have read them.
 #include <cuda_runtime.h>
@@ -28,13 +28,12 @@ struct LaneNeed {
     bool ok;       // its lengths are in range
 };
 
-__device__ __forceinline__ LaneNeed lane_need(const PagePlanParams& p, int b) {
+__device__ __forceinline__ LaneNeed lane_need(const PagePlanParams& p, int64_t old, int64_t add, int64_t held) {
     LaneNeed r;
-    const int64_t old = p.kv_lens[b], add = p.new_lens[b], held = p.held[b];
     r.add = add > 0 ? add : 0;
     r.ok = old >= 0 && add >= 0 && held >= 0 && held <= p.max_pages &&
            old + add <= (int64_t)p.max_pages * p.page_size && held * p.page_size >= old;
-    const int64_t want = (old + add + p.page_size - 1) / p.page_size - held;
+    const int64_t want = ((old + add + p.page_size - 1) >> p.page_shift) - held;
     r.need = r.ok && want > 0 ? want : 0;
     return r;
 }
@@ -64,8 +63,11 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     extern __shared__ int32_t smem[];
     __shared__ int64_t scan_sh[2 * kThreads / 32];
     __shared__ int last;
-    int32_t* cu = smem;             // [B + 1] first token of each lane
+    int32_t* cu = smem;              // [B + 1] first token of each lane
     int32_t* from = smem + p.B + 1;  // [B] place of its first new page in the free list; -1: the lane gets none
+    int32_t* kv = from + p.B;        // [B] cached tokens
+    int32_t* held = kv + p.B;        // [B] pages
+    int32_t* need = held + p.B;      // [B] new pages
     const int tid = threadIdx.x;
     const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     const int64_t taken0 = p.taken[0];
@@ -73,8 +75,11 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     const int64_t base = list_ok ? taken0 : 0, left = list_ok ? p.num_pages - taken0 : 0;
 
     int64_t toks = 0, pages = 0;
-    for (int b = b0; b < b1; ++b) {
-        const LaneNeed n = lane_need(p, b);
+    for (int b = b0; b < b1; ++b) {  // the lengths are read once; new_lens waits in cu
+        kv[b] = p.kv_lens[b];
+        held[b] = p.held[b];
+        cu[b] = p.new_lens[b];
+        const LaneNeed n = lane_need(p, kv[b], cu[b], held[b]);
         toks += n.add;
         pages += n.need;
     }
@@ -82,13 +87,18 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     block_scan2(toks, pages, all_toks, all_pages, scan_sh);
     uint32_t bits = list_ok ? 0u : (uint32_t)GDN_ERRBIT_INDEX;
     if (all_toks > p.N) bits |= GDN_ERRBIT_SEQLEN;
+    int64_t most = 0;  // pages that this thread's lanes bring the list to
     for (int b = b0; b < b1; ++b) {
-        const LaneNeed n = lane_need(p, b);
+        const int add = cu[b];
+        const LaneNeed n = lane_need(p, kv[b], add, held[b]);
         const bool got = n.ok && (n.need == 0 || pages + n.need <= left);
         cu[b] = (int32_t)min(toks, (int64_t)INT32_MAX);
         from[b] = got ? (int32_t)(base + pages) : -1;
+        need[b] = got ? (int32_t)n.need : 0;
         if (!n.ok) bits |= GDN_ERRBIT_SEQLEN;
         else if (!got) bits |= GDN_ERRBIT_PAGES;
+        if (got && n.need > 0) most = pages + n.need;
+        if (blockIdx.x == 0) p.total_lens[b] = got ? kv[b] + add : kv[b];
         toks += n.add;
         pages += n.need;
     }
@@ -96,16 +106,12 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     __syncthreads();
 
     const int gsize = gridDim.x * kThreads, gtid = blockIdx.x * kThreads + tid;
-    // lanes: offsets, lengths, new table entries (a warp a lane: its new pages side by side)
-    for (int b = gtid; b <= p.B; b += gsize) {
-        p.cu_seqlens[b] = cu[b];
-        if (b < p.B) p.total_lens[b] = from[b] >= 0 ? p.kv_lens[b] + p.new_lens[b] : p.kv_lens[b];
-    }
+    // offsets and new table entries (a warp a lane: its new pages side by side)
+    for (int b = gtid; b <= p.B; b += gsize) p.cu_seqlens[b] = cu[b];
     for (int b = gtid >> 5; b < p.B; b += gsize >> 5) {
         if (from[b] < 0) continue;
-        const int need = (int)lane_need(p, b).need, held = p.held[b];
-        for (int i = tid & 31; i < need; i += 32)
-            p.block_tables[(int64_t)b * p.max_pages + held + i] = p.free_pages[from[b] + i];
+        for (int i = tid & 31; i < need[b]; i += 32)
+            p.block_tables[(int64_t)b * p.max_pages + held[b] + i] = p.free_pages[from[b] + i];
     }
     // tokens
     const int64_t total = cu[p.B];
@@ -118,12 +124,12 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
                 if (cu[mid] <= t) lo = mid;
                 else hi = mid;
             }
-            pos = (int32_t)((uint32_t)p.kv_lens[lo] + (uint32_t)(t - cu[lo]));
+            pos = (int32_t)((uint32_t)kv[lo] + (uint32_t)(t - cu[lo]));
             if (from[lo] >= 0) {
-                const int col = pos / p.page_size, held = p.held[lo];
-                const int page = col < held ? p.block_tables[(int64_t)lo * p.max_pages + col]
-                                            : p.free_pages[from[lo] + col - held];
-                if (page >= 0 && page < p.num_pages) slot = page * p.page_size + pos % p.page_size;
+                const int col = pos >> p.page_shift;
+                const int page = col < held[lo] ? p.block_tables[(int64_t)lo * p.max_pages + col]
+                                                : p.free_pages[from[lo] + col - held[lo]];
+                if (page >= 0 && page < p.num_pages) slot = (page << p.page_shift) + (pos & (p.page_size - 1));
                 else bits |= GDN_ERRBIT_INDEX;
             }
         }
@@ -134,20 +140,16 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
 
     __syncthreads();
     if (tid == 0) {
-        __threadfence();
-        last = gridDim.x == 1 || atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
+        last = 1;
+        if (gridDim.x > 1) {
+            __threadfence();
+            last = atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
+        }
     }
     __syncthreads();
     if (!last) return;
     // every CTA has read held and taken: they may be updated in place now
-    int64_t most = 0;
-    int64_t run = 0;
-    for (int b = b0; b < b1; ++b) {
-        const LaneNeed n = lane_need(p, b);
-        if (from[b] >= 0 && n.need > 0) run = from[b] - base + n.need;
-        p.held_out[b] = p.held[b] + (from[b] >= 0 ? (int32_t)n.need : 0);
-    }
-    most = run;
+    for (int b = b0; b < b1; ++b) p.held_out[b] = held[b] + need[b];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const int64_t y = __shfl_xor_sync(~0u, most, o);
@@ -165,16 +167,16 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
 }  // namespace
 
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s) {
-    const size_t smem = ((size_t)2 * p.B + 1) * 4;
+    const size_t smem = ((size_t)5 * p.B + 1) * 4;
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(gdn_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    // a CTA for 2048 tokens or 128 lanes: fewer leave its threads with several dependent lookups each, more only
-    // repeat the scan
-    const int64_t want = ((int64_t)p.N + 2047) / 2048, lanes = (p.B + 127) / 128;
-    const int grid = (int)(want > lanes ? (want < 152 ? want : 152) : (lanes < 152 ? lanes : 152));
+    // One CTA while that leaves its threads a few tokens and lanes each: it needs no ticket.  Then a CTA for 2048 tokens or
+    // 128 lanes: more only repeat the scan.
+    const int64_t want = ((int64_t)p.N + 2047) / 2048, lanes = (p.B + 127) / 128, most = want > lanes ? want : lanes;
+    const int grid = p.N <= 4 * kThreads + 1024 && p.B <= kThreads ? 1 : (int)(most < 152 ? most : 152);
     gdn_page_plan_kernel<<<grid, kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
