@@ -307,9 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                     product_s(u);
                     if (u == C::UPT - 1) umma_commit(kv_empty + 8 * (pair % kPairs));
                 }
-                auto need_for = [&](int u) {  // P V of unit u, and the scores two units on
+                auto need_for = [&](int u) {  // P V of unit u, and the scores of unit u + 1
                     if (u < units) need(u / C::UPT + 1);
-                    if (u + 2 < units) need((u + 2) / C::UPT);
                 };
                 need_for(0);
                 for (int u = 0; u < units && go; ++u) {
@@ -322,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                     for (int ks = 0; ks < C::UNIT / 16; ++ks)
                         umma_bf16_ta(tmem + C::O_COL + m * D, tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT + ks * 8,
                                      v + ks * (2048 / 16), id_o, u > 0 || ks > 0);
-                    need_for(u + 1);  // while P V runs; then P is all that the next unit waits for
+                    need_for(u + 1);  // while P V runs; then P is all that the next unit waits for (no pair further on: its
+                                      // place in the ring is freed by the commit below)
                     if (!go) break;
                     if (u + 2 < units) product_s(u + 2);
                     else umma_commit((u + 1 < units ? pv_prev : pv_last) + 8 * m);  // scores two units on tell of the others
@@ -525,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
             float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
             const float inv = l > 0.f ? p.kv.v_scale / l : l != l ? l : 0.f;
-            // rows go out through Q's place in shared memory, a warp's own rows, so that a row's lanes store side by side
+            // rows go out through Q's place in shared memory, so that a row's lanes store side by side; in Q's layout, since then a
+            // warp's rows are its own and another warp may be at the next piece's Q already
             const int passes = whole ? 1 : 2;  // bf16, or fp32 in two halves
 #pragma unroll 1
             for (int pass = 0; pass < passes; ++pass) {
-                uint8_t* mine_at = stage + row * 2 * D;
 #pragma unroll 1
                 for (int c = 0; c < (whole ? D : D / 2); c += 16) {
                     float v[16];
@@ -538,13 +538,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                     if (whole) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            *reinterpret_cast<uint4*>(mine_at + (((c / 8 + j) ^ (row & 7)) << 4)) =
+                            *reinterpret_cast<uint4*>(stage + sw128(128, row, c / 8 + j)) =
                                 make_uint4(bf16x2_bits(v[8 * j] * inv, v[8 * j + 1] * inv), bf16x2_bits(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
                                            bf16x2_bits(v[8 * j + 4] * inv, v[8 * j + 5] * inv), bf16x2_bits(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<float4*>(mine_at + (((c / 4 + j) ^ (row & 7)) << 4)) =
+                            *reinterpret_cast<float4*>(stage + sw128(128, row, c / 4 + j)) =
                                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     }
                 }
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
 #pragma unroll 4
                 for (int i = 0; i < LR; ++i) {
                     const int lr = wrow + i * RPI + lane / LR, x = mt * 128 + lr;
-                    const uint4 w = *reinterpret_cast<const uint4*>(stage + lr * 2 * D + (((lane % LR) ^ (lr & 7)) << 4));
+                    const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(128, lr, lane % LR));
                     if (x >= nrows) continue;
                     if (whole) reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + place(x) * D)[lane % LR] = w;
                     else reinterpret_cast<uint4*>(part + (int64_t)x * D + pass * (D / 2))[lane % LR] = w;

@@ -494,3 +494,12 @@ def test_the_example_runs():
     p = subprocess.run([sys.executable, os.path.join(root, "examples", "attention_step.py")], capture_output=True, text=True,
                        cwd=root, timeout=300)
     assert p.returncode == 0 and "ok" in p.stdout, p.stdout + p.stderr
+
+
+@pytest.mark.parametrize("D,HQ,HK,T", [(64, 8, 2, 10), (64, 16, 2, 8), (128, 8, 2, 20), (128, 16, 2, 16), (256, 8, 2, 12), (256, 8, 2, 33)])
+def test_attention_runs_of_many_tiles(D, HQ, HK, T):
+    """Every CTA of the kernel for many rows takes a run of several items and of several tiles of each, of few rows and of
+    many in turn."""
+    rng = np.random.default_rng(D + T)
+    lens = [int(n) for n in rng.integers(1500, 2600, size=40)]
+    check_attend(attend(rng, [(T, 3 * T, 1, 7 * T // 2)[b % 4] for b in range(40)], lens, HQ, HK, D, 64), rows_per_lane=2)
