@@ -29,7 +29,6 @@ constexpr int kThreads = 512;  // 4 warpgroups: softmax, softmax or unpacking, u
 constexpr int kMmaWarp = 12, kLoadWarp = 14;  // kMmaWarp + m issues the products of rows 128 m ..
 constexpr int kLaunchRegs = 128, kSoftRegs = 160, kUnpackRegs = 112, kRestRegs = 80;
 static_assert(2 * kSoftRegs + kUnpackRegs + kRestRegs <= 4 * kLaunchRegs, "the block's registers");
-constexpr int kPairs = 2;  // places of the ring of unpacked tiles: V of one tile and K of the next
 
 template <int D_>
 struct Wide {
@@ -38,11 +37,12 @@ struct Wide {
     static constexpr int TILE = D == 256 ? 64 : 128;   // keys of a tile
     static constexpr int ROWS = MT * 128;
     static constexpr bool SPLIT = true;                // a stage of the copies holds keys or values
-    static constexpr int STAGES = 3;
+    static constexpr int PAIRS = D == 64 ? 4 : 2;      // places of the ring of unpacked tiles: V of one tile, K of the next
+    static constexpr int STAGES = D == 64 ? 6 : 3;
     static constexpr int CB = D / 2, SB = D / 16, STAGE = TILE * (CB + SB);
     static constexpr int UNPACK = 128 * (3 - MT);      // threads that unpack
     static constexpr int QBYTES = 128 * D * 2, KVBYTES = TILE * D * 2;
-    static constexpr int Q_AT = 0, RING_AT = MT * QBYTES, POOL_AT = RING_AT + 2 * kPairs * KVBYTES;
+    static constexpr int Q_AT = 0, RING_AT = MT * QBYTES, POOL_AT = RING_AT + 2 * PAIRS * KVBYTES;
     static constexpr int SMEM = 1024 + POOL_AT + STAGES * STAGE;
     static constexpr int UNIT = 64, UPT = TILE / UNIT;  // keys of a product S; of them in a tile
     static constexpr int O_COL = 0, S_COL = MT * D, COLS = 512;
@@ -156,14 +156,22 @@ __device__ __forceinline__ void locate(const Kv4AttentionParams& p, const int64_
     rt = (int)(i - at);
 }
 
+// An item of up to 128 rows: both warpgroups of the softmax and both issuing threads take all of its rows, each with half of
+// every tile's keys
+template <typename C>
+__device__ __forceinline__ bool in_halves(const Kv4AttentionParams& p, const Piece& y) {
+    return C::MT == 2 && y.x.qlen * p.G - y.r0 <= 128;
+}
+
 template <typename C>
 __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(const __grid_constant__ Kv4AttentionParams p,
                                                                              const __grid_constant__ CUtensorMap map) {
     constexpr int D = C::D, MT = C::MT, TILE = C::TILE;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[kThreads / 32];
-    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * kPairs + 8 * MT];
+    __shared__ uint64_t s_bar[2 * C::STAGES + 2 * C::PAIRS + 8 * MT + 2];
     __shared__ float s_sc[MT * 128];
+    __shared__ float2 s_ml[MT * 128];  // the two warpgroups' statistics of rows that they share
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -172,18 +180,19 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     int64_t* s_tiles = s_pairs + kThreads + 1;                         // [kThreads + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8 * C::STAGES, kv_full = raw_empty + 8 * C::STAGES,
-                   kv_empty = kv_full + 8 * kPairs, q_full = kv_empty + 8 * kPairs, s_full = q_full + 8 * MT,
+                   kv_empty = kv_full + 8 * C::PAIRS, q_full = kv_empty + 8 * C::PAIRS, s_full = q_full + 8 * MT,
                    p_full = s_full + 16 * MT, pv_prev = p_full + 16 * MT, pv_last = pv_prev + 8 * MT,
-                   idle = pv_last + 8 * MT;
+                   idle = pv_last + 8 * MT, told = idle + 8 * MT, read = told + 8;
     // s_full, p_full: two for each 128 rows; pv_prev, pv_last: the last P V of a piece but one, and the last; idle: all
-    // products are done
+    // products are done; told, read: both warpgroups' halves of shared rows are complete, and have been read
     uint32_t bits = 0;
 
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) mbar_init(raw_full + 8 * i, 1), mbar_init(raw_empty + 8 * i, C::UNPACK / 32);
-        for (int i = 0; i < kPairs; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, MT);
+        for (int i = 0; i < C::PAIRS; ++i) mbar_init(kv_full + 8 * i, C::UNPACK / 32), mbar_init(kv_empty + 8 * i, MT);
         for (int i = 0; i < MT; ++i) mbar_init(q_full + 8 * i, 4), mbar_init(pv_prev + 8 * i, 1), mbar_init(pv_last + 8 * i, 1), mbar_init(idle + 8 * i, 1);
         for (int i = 0; i < 2 * MT; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4);
+        mbar_init(told, 8), mbar_init(read, 8);
         fence_mbar_init();
         s_dead = 0;
     }
@@ -272,14 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             uint32_t pair = 0, piece = 0, unit = 0;  // ring pairs before this piece; pieces and units of these rows
             Piece y;
             bool go = true;
-            auto pair_wait = [&](uint32_t n) { return wait(kv_full + 8 * (n % kPairs), (n / kPairs) & 1); };
+            auto pair_wait = [&](uint32_t n) { return wait(kv_full + 8 * (n % C::PAIRS), (n / C::PAIRS) & 1); };
             // descriptors differ in their start address alone: 16 bytes count 1
             const uint64_t q_desc = umma_desc_sw128(base_u + C::Q_AT + m * C::QBYTES),
                            k_desc = umma_desc_sw128(base_u + C::RING_AT + C::KVBYTES),
                            v_desc = umma_desc_sw128_mn(base_u + C::RING_AT, TILE * 128);
+            int upt = C::UPT;  // units of a tile that these rows take
+            bool halves = false;
+            auto sub = [&](int u) { return halves ? m : u % C::UPT; };  // which of its tile's units unit u is
             auto product_s = [&](int u) {  // scores of unit u of the piece
-                const uint32_t n = pair + u / C::UPT, at = unit + u;
-                const uint64_t k = k_desc + (n % kPairs) * (2 * C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
+                const uint32_t n = pair + u / upt, at = unit + u;
+                const uint64_t k = k_desc + (n % C::PAIRS) * (2 * C::KVBYTES / 16) + sub(u) * (C::UNIT * 128 / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     umma_bf16(tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT, q_desc + ((ks / 4) * 128 * 128 + (ks % 4) * 32) / 16,
@@ -287,36 +299,31 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 umma_commit(s_full + 8 * (2 * m + (at & 1)));
             };
             while (go && walk.next(p, y)) {
-                const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0);
-                if (m * 128 >= nrows) {  // no rows here: the tiles pass by
-                    for (int i = 0; i <= n && go; ++i, ++pair) {
-                        go = pair_wait(pair);
-                        if (go) mbar_arrive(kv_empty + 8 * (pair % kPairs));
-                    }
-                    continue;
-                }
+                halves = in_halves<C>(p, y);
+                upt = halves ? 1 : C::UPT;
+                const int n = y.kt1 - y.kt0, units = n * upt;
                 int have = 0;  // pairs of the piece that are known to be there
                 auto need = [&](int q) {
                     for (; go && have <= q; ++have) go = pair_wait(pair + have);
                 };
                 for (int u = 0; u < 2 && u < units && go; ++u) {
-                    need(u / C::UPT);
+                    need(u / upt);
                     if (u == 0) go = go && wait(q_full + 8 * m, piece & 1);
                     if (!go) break;
                     tc_fence_after();
                     product_s(u);
-                    if (u == C::UPT - 1) umma_commit(kv_empty + 8 * (pair % kPairs));
+                    if (u == upt - 1) umma_commit(kv_empty + 8 * (pair % C::PAIRS));
                 }
                 auto need_for = [&](int u) {  // P V of unit u, and the scores of unit u + 1
-                    if (u < units) need(u / C::UPT + 1);
+                    if (u < units) need(u / upt + 1);
                 };
                 need_for(0);
                 for (int u = 0; u < units && go; ++u) {
-                    const uint32_t at = unit + u, nv = pair + u / C::UPT + 1;
+                    const uint32_t at = unit + u, nv = pair + u / upt + 1;
                     go = wait(p_full + 8 * (2 * m + (at & 1)), (at >> 1) & 1);
                     if (!go) break;
                     tc_fence_after();
-                    const uint64_t v = v_desc + (nv % kPairs) * (2 * C::KVBYTES / 16) + (u % C::UPT) * (C::UNIT * 128 / 16);
+                    const uint64_t v = v_desc + (nv % C::PAIRS) * (2 * C::KVBYTES / 16) + sub(u) * (C::UNIT * 128 / 16);
 #pragma unroll
                     for (int ks = 0; ks < C::UNIT / 16; ++ks)
                         umma_bf16_ta(tmem + C::O_COL + m * D, tmem + C::S_COL + (2 * m + (at & 1)) * C::UNIT + ks * 8,
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                     if (!go) break;
                     if (u + 2 < units) product_s(u + 2);
                     else umma_commit((u + 1 < units ? pv_prev : pv_last) + 8 * m);  // scores two units on tell of the others
-                    if (u % C::UPT == C::UPT - 1) umma_commit(kv_empty + 8 * (nv % kPairs));
+                    if (u % upt == upt - 1) umma_commit(kv_empty + 8 * (nv % C::PAIRS));
                 }
                 ++piece;
                 unit += units;
@@ -378,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         };
         while (go && walk.next(p, y)) {
             for (int kt = y.kt0; kt <= y.kt1 && go; ++kt, ++pair) {  // V of tile kt - 1, K of tile kt
-                const uint32_t at = pair % kPairs;
-                if (pair >= kPairs) go = warp_wait(kv_empty + 8 * at, (pair / kPairs - 1) & 1);
+                const uint32_t at = pair % C::PAIRS;
+                if (pair >= C::PAIRS) go = warp_wait(kv_empty + 8 * at, (pair / C::PAIRS - 1) & 1);
                 uint8_t* dst = smem + C::RING_AT + at * 2 * C::KVBYTES;
 #pragma unroll 1
                 for (int which = kt > y.kt0 ? 0 : 1; which < (kt < y.kt1 ? 2 : 1) && go; ++which)
@@ -396,12 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         const int mt = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // lane 32 (warp mod 4) in the upper half
         const uint32_t s_col0 = lanes + C::S_COL + mt * 2 * C::UNIT, o_col = lanes + C::O_COL + mt * D;
-        uint32_t unit = 0, piece = 0, prev = 0;  // of this tile of rows: units, pieces, and pieces of more than one unit
+        uint32_t unit = 0, piece = 0, prev = 0;  // of this warpgroup: units, pieces, and pieces of more than one unit
+        uint32_t shared = 0;                     // pieces in halves
         Piece y;
         bool go = true;
         while (go && walk.next(p, y)) {
-            const int n = y.kt1 - y.kt0, units = n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = mt * 128 + row;
-            if (mt > 0 && nrows <= 128) continue;
+            const bool halves = in_halves<C>(p, y);
+            const int row0 = halves ? 0 : mt * 128;  // the warpgroup's first row of the item
+            const int n = y.kt1 - y.kt0, units = halves ? n : n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = row0 + row;
             const bool mine = r < nrows;
             // where row x of the item lies in q and o: a row of 128 is loaded and stored by LR lanes, 16 bytes each
             constexpr int LR = D / 8, RPI = 32 / LR;
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 uint4 w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int x = mt * 128 + wrow + (i0 + i) * RPI + lane / LR;
+                    const int x = row0 + wrow + (i0 + i) * RPI + lane / LR;
                     w[i] = x < nrows ? reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + place(x) * D)[lane % LR] : make_uint4(0, 0, 0, 0);
                 }
                 uint32_t top[8];  // of each half of a word: magnitudes order as integers
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 if (!go) break;
                 tc_fence_after();
                 const uint32_t s_col = s_col0 + (unit & 1) * C::UNIT;
-                const int first = y.kt0 * TILE + u * C::UNIT;
+                const int first = halves ? (y.kt0 + u) * TILE + mt * C::UNIT : y.kt0 * TILE + u * C::UNIT;
                 const bool mask = first + C::UNIT > all_see;
                 F2 l2 = f2(0.f, 0.f);
                 // 16 columns at a time, P's 8 where S has been read, and not unrolled: the loop's instructions stay in the
@@ -522,19 +531,44 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             ++piece;
             prev += units > 1;
             tc_fence_after();
+            // rows in halves: the statistics joined; each warpgroup then puts out half of the dimensions
+            float fa = 1.f, fb = 1.f;  // factors of the first and the second warpgroup's O
+            if (halves) {
+                s_ml[mt * 128 + row] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(told);
+                go = warp_wait(told, shared & 1);
+                if (!go) break;
+                tc_fence_after();
+                const float2 a = s_ml[row], b = s_ml[(MT - 1) * 128 + row];
+                m = fmaxf(a.x, b.x);
+                fa = m == -INFINITY ? 1.f : exp2_fast(a.x - m);
+                fb = m == -INFINITY ? 1.f : exp2_fast(b.x - m);
+                l = fmaf(a.y, fa, b.y * fb);
+            }
             const bool whole = y.kt0 == 0 && y.kt1 == y.kts;
             float* part = parts + ((int64_t)blockIdx.x * 2 + (y.kt0 == 0 ? 1 : 0)) * part_floats(C::ROWS, D);
             const float inv = l > 0.f ? p.kv.v_scale / l : l != l ? l : 0.f;
             // rows go out through Q's place in shared memory, so that a row's lanes store side by side; in Q's layout, since then a
             // warp's rows are its own and another warp may be at the next piece's Q already
-            const int passes = whole ? 1 : 2;  // bf16, or fp32 in two halves
+            auto put_out = [&](int col0, int cols) {  // dimensions col0 ..; a row's place holds D bf16 or D / 2 fp32
 #pragma unroll 1
-            for (int pass = 0; pass < passes; ++pass) {
-#pragma unroll 1
-                for (int c = 0; c < (whole ? D : D / 2); c += 16) {
+                for (int c = 0; c < cols; c += 16) {
                     float v[16];
-                    tmem_ld16(o_col + pass * (D / 2) + c, v);
-                    tmem_wait_ld16(v);
+                    if (halves) {
+                        float v2[16];
+                        const uint32_t o_first = lanes + C::O_COL + col0 + c;
+                        tmem_ld16(o_first, v);
+                        tmem_ld16(o_first + (MT - 1) * D, v2);
+                        tmem_wait_ld16(v);
+                        tmem_wait_ld16(v2);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = fmaf(v[j], fa, v2[j] * fb);
+                    } else {
+                        tmem_ld16(o_col + col0 + c, v);
+                        tmem_wait_ld16(v);
+                    }
                     if (whole) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
@@ -548,18 +582,26 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     }
                 }
+                tc_fence_before();  // O is read before another product writes it
                 __syncwarp();
+                if (halves && lane == 0) mbar_arrive(read);
+                const int chunks = whole ? cols / 8 : cols / 4;  // of a row, 16 bytes each: 4, 8, 16 or 32
+                const int per = 32 / chunks, ch = lane & (chunks - 1);
 #pragma unroll 4
-                for (int i = 0; i < LR; ++i) {
-                    const int lr = wrow + i * RPI + lane / LR, x = mt * 128 + lr;
-                    const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(128, lr, lane % LR));
+                for (int i = 0; i < chunks; ++i) {
+                    const int lr = wrow + i * per + lane / chunks, x = row0 + lr;
+                    const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(128, lr, ch));
                     if (x >= nrows) continue;
-                    if (whole) reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + place(x) * D)[lane % LR] = w;
-                    else reinterpret_cast<uint4*>(part + (int64_t)x * D + pass * (D / 2))[lane % LR] = w;
+                    if (whole) reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + place(x) * D + col0)[ch] = w;
+                    else reinterpret_cast<uint4*>(part + (int64_t)x * D + col0)[ch] = w;
                 }
                 __syncwarp();
-            }
-            if (mine) {
+            };
+            if (halves) put_out(mt * (D / 2), D / 2);
+            else if (whole) put_out(0, D);
+            else
+                for (int half = 0; half < 2; ++half) put_out(half * (D / 2), D / 2);
+            if (mine && (mt == 0 || !halves)) {
                 if (!whole) *reinterpret_cast<float2*>(part + (int64_t)C::ROWS * D + 2 * r) = make_float2(m, l);
                 else if (p.lse) p.lse[place(r)] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             }
@@ -570,7 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 desc->r0 = y.r0;
                 desc->hk = y.hk;
             }
-            tc_fence_before();  // O is read before the next piece's first product writes it
+            if (halves) {  // the other warpgroup has read this one's O and statistics
+                go = warp_wait(read, shared & 1);
+                ++shared;
+            }
         }
     }
     if (bits && p.err) atomicOr(p.err, (int32_t)bits);
