@@ -156,6 +156,11 @@ __device__ __forceinline__ void locate(const Kv4AttentionParams& p, const int64_
     rt = (int)(i - at);
 }
 
+// 16 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
 // An item of up to 128 rows: both warpgroups of the softmax and both issuing threads take all of its rows, each with half of
 // every tile's keys
 template <typename C>
@@ -170,7 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[kThreads / 32];
     __shared__ uint64_t s_bar[2 * C::STAGES + 2 * C::PAIRS + 8 * MT + 2];
-    __shared__ float s_sc[MT * 128];
     __shared__ float2 s_ml[MT * 128];  // the two warpgroups' statistics of rows that they share
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
@@ -403,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         const int mt = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // lane 32 (warp mod 4) in the upper half
         const uint32_t s_col0 = lanes + C::S_COL + mt * 2 * C::UNIT, o_col = lanes + C::O_COL + mt * D;
+        const uint32_t magic = 65535u / (uint32_t)p.G + 1u;  // x / G = x * magic >> 16 for x < 256 and G <= 64
         uint32_t unit = 0, piece = 0, prev = 0;  // of this warpgroup: units, pieces, and pieces of more than one unit
         uint32_t shared = 0;                     // pieces in halves
         Piece y;
@@ -412,59 +417,54 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             const int row0 = halves ? 0 : mt * 128;  // the warpgroup's first row of the item
             const int n = y.kt1 - y.kt0, units = halves ? n : n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = row0 + row;
             const bool mine = r < nrows;
-            // where row x of the item lies in q and o: a row of 128 is loaded and stored by LR lanes, 16 bytes each
+            // rows of q and o lie at `first` + the row's `rel` rows; a row of 128 is loaded by LR lanes, 16 bytes each
             constexpr int LR = D / 8, RPI = 32 / LR;
             const int wrow = (warp & 3) * 32;  // the warp's first row of its 128
             uint8_t* stage = smem + C::Q_AT + mt * C::QBYTES;
-            const uint32_t magic = 65535u / (uint32_t)p.G + 1u;  // x / G = x * magic >> 16 for x < 256 and G <= 64
             const int t_first = y.r0 / p.G;
-            auto place = [&](int x) {
-                const int t = (int)((uint32_t)x * magic >> 16);
-                return (int64_t)(y.x.q0 + t_first + t) * p.HQ + y.hk * p.G + x - t * p.G;
-            };
-            // Q as f16, each row scaled by a power of two (and by the sign of p.scale)
-#pragma unroll 1
-            for (int i0 = 0; i0 < LR; i0 += 8) {
-                uint4 w[8];
+            const int64_t first_row = (int64_t)(y.x.q0 + t_first) * p.HQ + y.hk * p.G;
+            const int rt = (int)((uint32_t)r * magic >> 16), rel = mine ? rt * p.HQ + r - rt * p.G : 0;
+            // Q: the rows as they are, then each thread its own as f16, scaled by a power of two (and by the sign of p.scale).
+            // Short loops: a piece's start is cold code for the instruction cache (with the rows' maxima by shuffles
+            // and eight rows unrolled, 16 ragged prompts took 234 us).
+#pragma unroll 4
+            for (int i = 0; i < LR; ++i) {
+                const int at = i * RPI + lane / LR, lr = wrow + at;
+                const int64_t off = (first_row + __shfl_sync(~0u, rel, at)) * D + (lane % LR) * 8;
+                cp_async16(smem_u32(stage + sw128(128, lr, lane % LR)), (const __nv_bfloat16*)p.q + off, row0 + lr < nrows);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            uint32_t top2 = 0;  // of each half of a word: magnitudes order as integers
+#pragma unroll 4
+            for (int c = 0; c < LR; ++c) {
+                const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(128, row, c));
+                top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+            }
+            // the exponent, kept where its power of two and the reciprocal are normal numbers (NaN and infinity count as the
+            // largest)
+            uint32_t e = max(top2 & 0xffffu, top2 >> 16) >> 7;
+            e = e < 30 ? 30 : e > 224 ? 224 : e;
+            const float down = __uint_as_float((254u - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
+            // (at least 2^-120: a masked score of -inf must stay one)
+            const float sc = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
+#pragma unroll 2
+            for (int c = 0; c < LR; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(stage + sw128(128, row, c));
+                const uint4 w = *at;
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                uint32_t f[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int x = row0 + wrow + (i0 + i) * RPI + lane / LR;
-                    w[i] = x < nrows ? reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + place(x) * D)[lane % LR] : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = bf16x2_to_float2(ws[j]);
+                    f[j] = f16x2_bits(v.x * down, v.y * down);
                 }
-                uint32_t top[8];  // of each half of a word: magnitudes order as integers
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    top[i] = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-#pragma unroll
-                for (int o = LR / 2; o > 0; o >>= 1)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(~0u, top[i], o));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int lr = wrow + (i0 + i) * RPI + lane / LR;
-                    // the exponent, kept where its power of two and the reciprocal are normal numbers (NaN and infinity count
-                    // as the largest)
-                    uint32_t e = max(top[i] & 0xffffu, top[i] >> 16) >> 7;
-                    e = e < 30 ? 30 : e > 224 ? 224 : e;
-                    const float down = __uint_as_float((254u - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
-                    // (at least 2^-120: a masked score of -inf must stay one)
-                    if (lane % LR == 0)
-                        s_sc[mt * 128 + lr] = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
-                    const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t f[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = bf16x2_to_float2(ws[j]);
-                        f[j] = f16x2_bits(v.x * down, v.y * down);
-                    }
-                    *reinterpret_cast<uint4*>(stage + sw128(128, lr, lane % LR)) = make_uint4(f[0], f[1], f[2], f[3]);
-                }
+                *at = make_uint4(f[0], f[1], f[2], f[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + 8 * mt);
-            const float sc = s_sc[mt * 128 + row];
-            const int t = t_first + (int)((uint32_t)r * magic >> 16);
+            const int t = t_first + rt;
             const int limit = y.x.kv - y.x.qlen + t + 1;                   // keys that the row sees
             const int all_see = y.x.kv - y.x.qlen + y.r0 / p.G + 1;        // that every row of the item sees
             float m = -INFINITY, l = 0.f;
@@ -589,10 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 const int per = 32 / chunks, ch = lane & (chunks - 1);
 #pragma unroll 4
                 for (int i = 0; i < chunks; ++i) {
-                    const int lr = wrow + i * per + lane / chunks, x = row0 + lr;
+                    const int at = i * per + lane / chunks, lr = wrow + at, x = row0 + lr, xr = __shfl_sync(~0u, rel, at);
                     const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(128, lr, ch));
                     if (x >= nrows) continue;
-                    if (whole) reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + place(x) * D + col0)[ch] = w;
+                    if (whole) reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + (first_row + xr) * D + col0)[ch] = w;
                     else reinterpret_cast<uint4*>(part + (int64_t)x * D + col0)[ch] = w;
                 }
                 __syncwarp();
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 for (int half = 0; half < 2; ++half) put_out(half * (D / 2), D / 2);
             if (mine && (mt == 0 || !halves)) {
                 if (!whole) *reinterpret_cast<float2*>(part + (int64_t)C::ROWS * D + 2 * r) = make_float2(m, l);
-                else if (p.lse) p.lse[place(r)] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+                else if (p.lse) p.lse[first_row + rel] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             }
             if (!whole && y.kt0 == 0 && tid == 0) {
                 desc->last = cta_of(all, ctas, walk.u - n + y.kts - 1);
