@@ -155,10 +155,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 }
 
 // The copying warp: tiles of the run, page by page; lane i takes page i of a tile.  A stage holds a tile's keys and values
-// (codes of both, then scales of both), or with C::SPLIT its keys or its values.
+// (codes of both, then scales of both), or with C::SPLIT its keys or its values, which are then a warp's each (kind 0, 1):
+// with pages of 16 tokens one warp's 16 copies a stage are too slow for the prompts' kernel.
 template <typename C, typename W>
 __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUtensorMap* map, W walk, uint32_t pool,
-                                        uint8_t* pool_p, uint32_t full, uint32_t empty, uint32_t& bits) {
+                                        uint8_t* pool_p, uint32_t full, uint32_t empty, uint32_t& bits, int kind = 0) {
     constexpr int KINDS = C::SPLIT ? 1 : 2;  // of rows in a stage
     const int lane = threadIdx.x & 31, P = p.kv.page_size, HK = p.kv.HK;
     const int PR = P < C::TILE ? P : C::TILE;  // rows of a copy
@@ -175,6 +176,7 @@ __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUten
         for (int kt = y.kt0; kt < y.kt1 && !late; ++kt) {
             const int ahead = entry(kt + 1);
             for (int part = 0; part < 2 / KINDS; ++part, ++it) {
+                if (C::SPLIT && part != kind) continue;
                 const uint32_t s = it % C::STAGES, round = it / C::STAGES;
                 if (round > 0 && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, GDN_WAIT_POLLS))) {
                     bits |= GDN_ERRBIT_TIMEOUT;
