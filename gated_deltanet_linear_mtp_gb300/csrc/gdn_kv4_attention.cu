@@ -39,11 +39,15 @@ namespace {
 
 // NR: groups of 8 rows of an item; W: warps that compute (one of four more copies, and those four give their registers to
 // the others: LREG a thread at launch, then CREG and PREG); WT: tokens of a warp's step; TILE: tokens of a tile; STAGES: tiles
-// in the pipeline; CTAS: of an SM
-template <int D_, int NR_, int WT_, int TILE_, int STAGES_, int CTAS_>
+// in the pipeline; CTAS: of an SM; SWITCH: tiles that an item's begin and end (queries in, the warps' parts joined) count as in
+// the split of the work, so that CTAs with many short items are done with the others: 128 lanes of 4 tokens over up to 16384
+// keys, HQ 32, HK 4, D 128, 361 us with none, 304 with 6, 309 with 8; 64 lanes of one token, HQ 16, HK 2, D 256, 54, 48 (3), 49
+// (4); D 64 of one row group is best with none (92 us against 97 with 1)
+template <int D_, int NR_, int WT_, int TILE_, int STAGES_, int CTAS_, int SWITCH_>
 struct Cfg {
     static constexpr int D = D_, NR = NR_, W = 8, WT = WT_, TILE = TILE_, STAGES = STAGES_, CTAS = CTAS_;
     static constexpr bool SPLIT = false;  // a stage holds keys and values
+    static constexpr int SWITCH = SWITCH_;
     static constexpr int ROWS = 8 * NR, THREADS = 32 * (W + 4), STEPS = TILE / W / WT;
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a token's codes and scales
     static constexpr int STAGE = 2 * TILE * (CB + SB);
@@ -636,14 +640,14 @@ cudaError_t launch_kv4_attention(const Kv4AttentionParams& p, cudaStream_t s) {
     if (wide((int64_t)p.T * p.G)) return launch_kv4_attention_wide(p, s);
     const int rows = item_rows((int64_t)p.T * p.G, p.kv.D);
     switch (p.kv.D * 100 + rows) {
-    case 6408: return run<Cfg<64, 1, 32, 256, 3, 2>>(p, s);
-    case 6416: return run<Cfg<64, 2, 32, 256, 3, 2>>(p, s);
-    case 6432: return run<Cfg<64, 4, 16, 128, 4, 1>>(p, s);
-    case 12808: return run<Cfg<128, 1, 32, 256, 2, 2>>(p, s);
-    case 12816: return run<Cfg<128, 2, 32, 256, 4, 1>>(p, s);
-    case 12832: return run<Cfg<128, 4, 16, 128, 4, 1>>(p, s);
-    case 25608: return run<Cfg<256, 1, 16, 128, 3, 1>>(p, s);
-    default: return run<Cfg<256, 2, 16, 128, 3, 1>>(p, s);
+    case 6408: return run<Cfg<64, 1, 32, 256, 3, 2, 0>>(p, s);
+    case 6416: return run<Cfg<64, 2, 32, 256, 3, 2, 1>>(p, s);
+    case 6432: return run<Cfg<64, 4, 16, 128, 4, 1, 3>>(p, s);
+    case 12808: return run<Cfg<128, 1, 32, 256, 2, 2, 2>>(p, s);
+    case 12816: return run<Cfg<128, 2, 32, 256, 4, 1, 3>>(p, s);
+    case 12832: return run<Cfg<128, 4, 16, 128, 4, 1, 6>>(p, s);
+    case 25608: return run<Cfg<256, 1, 16, 128, 3, 1, 3>>(p, s);
+    default: return run<Cfg<256, 2, 16, 128, 3, 1, 5>>(p, s);
     }
 }
 

@@ -79,34 +79,38 @@ __device__ __forceinline__ int tiles_of(int kv) {
 
 template <typename C>
 __device__ __forceinline__ int64_t lane_tiles(const Kv4AttentionParams& p, const Lane& x) {
-    return ((int64_t)x.qlen * p.G + C::ROWS - 1) / C::ROWS * tiles_of<C>(x.kv) * p.kv.HK;
+    return ((int64_t)x.qlen * p.G + C::ROWS - 1) / C::ROWS * (tiles_of<C>(x.kv) + C::SWITCH) * p.kv.HK;
 }
 
-// Walks a CTA's run of tiles u .. u1 - 1; lane `b` holds tile `base` first
+// Walks a CTA's run of tiles u .. u1 - 1; lane `b` holds tile `base` first.  An item counts as C::SWITCH tiles more than it has,
+// which are its first: a piece of these alone is passed over.
 template <typename C>
 struct Walk {
     int64_t u, u1, base;
     int b;
     __device__ __forceinline__ bool next(const Kv4AttentionParams& p, Piece& y) {
-        if (u >= u1) return false;
         uint32_t ignored = 0;
-        y.x = lane_extent(p, b, ignored);
-        int64_t n = lane_tiles<C>(p, y.x);
-        while (base + n <= u) {
-            base += n;
-            y.x = lane_extent(p, ++b, ignored);
-            n = lane_tiles<C>(p, y.x);
+        while (u < u1) {
+            y.x = lane_extent(p, b, ignored);
+            int64_t n = lane_tiles<C>(p, y.x);
+            while (base + n <= u) {
+                base += n;
+                y.x = lane_extent(p, ++b, ignored);
+                n = lane_tiles<C>(p, y.x);
+            }
+            y.b = b;
+            y.kts = tiles_of<C>(y.x.kv);
+            const int64_t in = u - base, each = (int64_t)y.kts + C::SWITCH;
+            const int item = (int)(in / each);
+            const int64_t at = in - item * each, end = min(each, at + (u1 - u));
+            y.hk = item % p.kv.HK;
+            y.r0 = item / p.kv.HK * C::ROWS;
+            y.kt0 = (int)max(at - C::SWITCH, (int64_t)0);
+            y.kt1 = (int)max(end - C::SWITCH, (int64_t)0);
+            u += end - at;
+            if (y.kt1 > y.kt0) return true;
         }
-        y.b = b;
-        y.kts = tiles_of<C>(y.x.kv);
-        const int64_t in = u - base;
-        const int item = (int)(in / y.kts);
-        y.kt0 = (int)(in - (int64_t)item * y.kts);
-        y.hk = item % p.kv.HK;
-        y.r0 = item / p.kv.HK * C::ROWS;
-        y.kt1 = (int)min((int64_t)y.kts, y.kt0 + (u1 - u));
-        u += y.kt1 - y.kt0;
-        return true;
+        return false;
     }
 };
 
@@ -206,7 +210,7 @@ __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUten
                     for (int i = 0; i < KINDS; ++i) {
                         const int which = part + i;
 #ifdef GDN_TEST_MISSING_COPY
-                        if (blockIdx.x == 0 && it == 0 && which == 0 && lane == 0) continue;
+                        if (y.b == 0 && y.hk == 0 && y.r0 == 0 && kt == 0 && which == 0 && lane == 0) continue;
 #endif
                         tma_load_4d(st + (i * C::TILE + lane * PR) * C::CB, map, 0, off, which * HK + y.hk, pg, bar);
                         const int64_t row = (((int64_t)pg * 2 + which) * HK + y.hk) * P + off;

@@ -1,5 +1,5 @@
 """The bounded waits of the attention kernels over the 4-bit cache, made to run out without a fault: a test build leaves the
-first copy of the first CTA's first tile unissued, so that the wait for it can only run out.  The kernel reports
+copy of the first keys of the first lane unissued, so that the wait for it can only run out.  The kernel reports
 GDN_ERRBIT_TIMEOUT, drains the copies it did issue and ends; the product library then runs the same call correctly."""
 import numpy as np
 import pytest
