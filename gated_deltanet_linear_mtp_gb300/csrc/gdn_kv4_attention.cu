@@ -7,10 +7,14 @@
 // r % G, so the cached keys and values are read once for all of them.  An item is (lane, row tile, key head).
 //
 // Bound: the cache's 9/16 byte a number from HBM, and close behind it the issue slots of the unpacking (two conversions'
-// worth of instructions a pair of numbers); with 32 rows the tensor cores' rate for mma.sync (600 TFLOP/s measured).  More
-// rows go to gdn_kv4_attention_wide.cu.  Nothing is dequantised into memory: one warp brings packed tiles of 128 tokens into shared memory by TMA
-// (swizzled, a pipeline of several), and each lane of the others unpacks the codes of its own MMA fragments (cvt
-// e2m1x2 -> f16x2, one multiply by the group's scale; both exact).  Keys and values are the M operand and the rows are N:
+// worth of instructions a pair of numbers); with 32 rows the tensor cores' rate for mma.sync (600 TFLOP/s measured).  Measured
+// with the join, HBM's floor in brackets: one lane of 131071 tokens, HQ 32, HK 4, D 128, 28 us (11); 64 lanes of one token over
+// up to 8192, HQ 16, HK 2, D 256, 48 us (23), 3.3 TB/s; 128 lanes of 4 tokens over up to 16384, HQ 32, HK 4, D 128, 304 us
+// (93), 233 TFLOP/s.  More rows go to gdn_kv4_attention_wide.cu.
+// Nothing is dequantised into memory: one warp brings packed tiles of 128 or 256 tokens into shared memory by TMA (swizzled, a
+// pipeline of several), and each lane of the others unpacks the codes of its own MMA fragments (cvt e2m1x2 -> f16x2, one
+// multiply by the group's scale; both exact).  Issue: an eighth of a tile costs a warp about 760 instructions at 32 rows, D 128,
+// and registers leave two computing warps a scheduler (16 warps of half the rows each were not faster: 396 us against 371).  Keys and values are the M operand and the rows are N:
 // N goes by 8, so a decode's 8 rows waste nothing.  The products' summation index may be permuted freely, which makes the
 // fragments contiguous in storage:
 //   * S^T = K Q^T: lane (g, c) of a warp (g = lane / 4, c = lane % 4) supplies tokens g and g + 8 of a tile of 16; k step s
@@ -456,7 +460,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
 
 // Joins the parts of items that more than one CTA worked on: block (x, y) takes rows y, y + gridDim.y, .. of the item that
 // CTA x began and did not end.  Few parts: a warp takes a row.  Many: the block takes a row, D / 4 threads a part of it, and
-// as many parts side by side as that leaves room for.
+// as many parts side by side as that leaves room for.  Latency bound: 5.6 us for a decode's parts (12.5 us for 256 rows of D 128
+// from every CTA, 25 MB), of which the programmatic launch hides the start.
 constexpr int kJoinThreads = 128;
 constexpr int kFewParts = 4;
 constexpr int kMaxParts = 1024;
@@ -608,7 +613,8 @@ cudaError_t run(const Kv4AttentionParams& p, cudaStream_t s) {
 }
 
 // More rows than this go to the tcgen05 kernel, although 128 is what it wants: 256 lanes of 64 rows over 2100 keys, D 64, took
-// 278 us there and 352 us here; 128 lanes of 32 rows over 8500 keys, D 128, 535 us there and 354 us here.
+// 255 us there and 352 us here (160 us there now); 128 lanes of 32 rows over 8500 keys, D 128, 417 us there and 361 us here
+// (304 us here now), and of 20 rows 413 and 349 us.
 bool wide(int64_t rows) { return rows > 32; }
 
 // Rows of an item: 8, 16 or 32; of D 256 at most 16 (O^T takes D * rows / 32 registers a thread), more take several items

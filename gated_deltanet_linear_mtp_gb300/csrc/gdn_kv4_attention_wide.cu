@@ -3,15 +3,20 @@
 //
 // Bound: the products, 4 D flops a row and key.  An item is a tile of MT * 128 rows (whole tokens times the G heads of a key
 // head) of one lane and key head; a CTA takes its tiles of TILE keys in turn, as four kinds of warps:
-//   * one warp copies the packed tiles into shared memory by TMA (shared with the decode kernel);
+//   * two warps copy the packed tiles into shared memory by TMA, keys and values (shared with the decode kernel);
 //   * a warpgroup unpacks them into f16 operand tiles (128-byte swizzle, a ring of two pairs), once for all rows: a
 //     number costs the unpacking 1/256 of its products;
 //   * a thread for each 128 rows issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory;
 //   * a warpgroup for each 128 rows takes a row of S a thread, forms P in place of S as f16 and keeps the row's statistics.
 // S goes by units of 64 keys in two buffers: the way from a product to its softmax and back takes longer than either
 // (about 600 cycles each way), and with one buffer of 128 keys the tensor cores waited for it (665 us for two chunks of 2048
-// tokens behind 8192 keys, HQ 32, HK 4, D 128, against 573).  The running maximum moves only where a score passes it by more than
-// 2^8 (then that thread scales its row of O in tensor memory), so O stays in tensor memory throughout.
+// tokens behind 8192 keys, HQ 32, HK 4, D 128, against 573 then).  An item of up to 128 rows is worked on by both halves of the
+// CTA, each with half of every tile's keys (256 lanes of 64 rows over up to 4096 keys, D 64: 229 us against 255 then).
+// Measured: those two chunks 530 us, 1.17 PFLOP/s; 16 ragged prompts of up to 2048 tokens, HQ 16, HK 2, D 128, 135 us, 0.54
+// PFLOP/s; the 256 lanes 160 us, 0.98 TB/s.  What is left above the products: the waits of the issuing threads and the
+// softmax's way (2000 cycles a unit of 64 keys where the products take 1280), and an item's begin and end.
+// The running maximum moves only where a score passes it by more than 8 (in units of log 2; then that thread scales its row of
+// O in tensor memory), so O stays in tensor memory throughout.
 // Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16, fp32.
 //
 // Work split: all tiles of all items are numbered and each CTA (one an SM) takes an equal run of them, since the rows of a
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 const bool mask = first + C::UNIT > all_see;
                 F2 l2 = f2(0.f, 0.f);
                 // 16 columns at a time, P's 8 where S has been read, and not unrolled: the loop's instructions stay in the
-                // scheduler's cache, which four kinds of warps share (unrolled over all 64 columns 595 us against 540)
+                // scheduler's cache, which four kinds of warps share (unrolled over all 64 columns 595 us against 540 then)
 #pragma unroll 1
                 for (int c = 0; c < C::UNIT; c += 16) {
                     float x[16];
