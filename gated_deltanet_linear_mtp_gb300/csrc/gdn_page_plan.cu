@@ -10,7 +10,8 @@
 // its own slice of the tables and of the tokens, finding a token's lane by binary search in shared memory.  A
 // new page is taken from the free list directly, so no CTA reads what another one writes; held and taken, which the
 // caller may update in place, are written by the last CTA to finish, after all have read them.  Measured: 256 lanes of 8 new
-// tokens, and 64 prompts of 256 .. 4096 tokens (pages of 16), 10.6 us each, where an empty launch takes about 4.
+// tokens 8.6 us, 64 prompts of 256 .. 4096 tokens (pages of 16) 10.5 us, where an empty launch takes about 4 (10.6 us for the
+// former with one token of a thread at a time and a warp a lane for the new pages).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -65,10 +66,10 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     __shared__ int64_t scan_sh[2 * kThreads / 32];
     __shared__ int last;
     int32_t* cu = smem;              // [B + 1] first token of each lane
-    int32_t* from = smem + p.B + 1;  // [B] place of its first new page in the free list; -1: the lane gets none
+    int32_t* from = smem + p.B + 1;  // [B] new pages of the lanes before it
     int32_t* kv = from + p.B;        // [B] cached tokens
     int32_t* held = kv + p.B;        // [B] pages
-    int32_t* need = held + p.B;      // [B] new pages
+    int32_t* need = held + p.B;      // [B] new pages that it gets; -1: it gets none and its tokens no slots
     const int tid = threadIdx.x;
     const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     const int64_t taken0 = p.taken[0];
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
         const LaneNeed n = lane_need(p, kv[b], add, held[b]);
         const bool got = n.ok && (n.need == 0 || pages + n.need <= left);
         cu[b] = (int32_t)min(toks, (int64_t)INT32_MAX);
-        from[b] = got ? (int32_t)(base + pages) : -1;
-        need[b] = got ? (int32_t)n.need : 0;
+        from[b] = (int32_t)min(pages, (int64_t)INT32_MAX);
+        need[b] = got ? (int32_t)n.need : -1;
         if (!n.ok) bits |= GDN_ERRBIT_SEQLEN;
         else if (!got) bits |= GDN_ERRBIT_PAGES;
         if (got && n.need > 0) most = pages + n.need;
@@ -107,35 +108,44 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     __syncthreads();
 
     const int gsize = gridDim.x * kThreads, gtid = blockIdx.x * kThreads + tid;
-    // offsets and new table entries (a warp a lane: its new pages side by side)
     for (int b = gtid; b <= p.B; b += gsize) p.cu_seqlens[b] = cu[b];
-    for (int b = gtid >> 5; b < p.B; b += gsize >> 5) {
-        if (from[b] < 0) continue;
-        for (int i = tid & 31; i < need[b]; i += 32)
-            p.block_tables[(int64_t)b * p.max_pages + held[b] + i] = p.free_pages[from[b] + i];
+    // the last lane that begins at x or before: lanes without tokens (or new pages) are passed over
+    const int top = 1 << (31 - __clz(p.B));
+    auto lane_of = [&](const int32_t* begin, int x) {
+        int lo = 0;
+        for (int s = top; s > 0; s >>= 1)
+            if (lo + s < p.B && begin[lo + s] <= x) lo += s;
+        return lo;
+    };
+    // new table entries
+    const int fresh = (int)min(all_pages, left);
+    for (int g = gtid; g < fresh; g += gsize) {
+        const int b = lane_of(from, g);
+        if (need[b] > 0) p.block_tables[(int64_t)b * p.max_pages + held[b] + g - from[b]] = p.free_pages[base + g];
     }
-    // tokens
+    // tokens, four of a thread side by side for the latency of their search and their pages
     const int64_t total = cu[p.B];
-    for (int64_t t = gtid; t < p.N; t += gsize) {
-        int32_t pos = 0, slot = -1;
-        if (t < total) {
-            int lo = 0, hi = p.B;  // the last lane whose first token is <= t: lanes without tokens are passed over
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid] <= t) lo = mid;
-                else hi = mid;
-            }
-            pos = (int32_t)((uint32_t)kv[lo] + (uint32_t)(t - cu[lo]));
-            if (from[lo] >= 0) {
-                const int col = pos >> p.page_shift;
-                const int page = col < held[lo] ? p.block_tables[(int64_t)lo * p.max_pages + col]
-                                                : p.free_pages[from[lo] + col - held[lo]];
-                if (page >= 0 && page < p.num_pages) slot = (page << p.page_shift) + (pos & (p.page_size - 1));
-                else bits |= GDN_ERRBIT_INDEX;
-            }
+    for (int64_t t0 = gtid; t0 < p.N; t0 += 4 * (int64_t)gsize) {
+        int pos[4], page[4];
+        bool want[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t t = t0 + k * (int64_t)gsize;
+            const int b = lane_of(cu, (int)min(t, (int64_t)INT32_MAX - 1)), col0 = held[b];
+            pos[k] = t < total ? (int32_t)((uint32_t)kv[b] + (uint32_t)(t - cu[b])) : 0;
+            want[k] = t < total && t < p.N && need[b] >= 0;
+            const int col = pos[k] >> p.page_shift;
+            page[k] = !want[k] ? -1 : col < col0 ? p.block_tables[(int64_t)b * p.max_pages + col] : p.free_pages[base + from[b] + col - col0];
         }
-        p.positions[t] = pos;
-        p.slot_map[t] = slot;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t t = t0 + k * (int64_t)gsize;
+            if (t >= p.N) break;
+            const bool ok = page[k] >= 0 && page[k] < p.num_pages;
+            if (want[k] && !ok) bits |= GDN_ERRBIT_INDEX;
+            p.positions[t] = pos[k];
+            p.slot_map[t] = ok ? (page[k] << p.page_shift) + (pos[k] & (p.page_size - 1)) : -1;
+        }
     }
     if (bits && p.err) atomicOr(p.err, (int32_t)bits);
 
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
     __syncthreads();
     if (!last) return;
     // every CTA has read held and taken: they may be updated in place now
-    for (int b = b0; b < b1; ++b) p.held_out[b] = held[b] + need[b];
+    for (int b = b0; b < b1; ++b) p.held_out[b] = held[b] + max(need[b], 0);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const int64_t y = __shfl_xor_sync(~0u, most, o);
