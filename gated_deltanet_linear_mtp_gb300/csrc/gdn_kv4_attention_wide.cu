@@ -177,7 +177,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
 }
 
 // An item of up to 128 rows: both warpgroups of the softmax and both issuing threads take all of its rows, each with half of
-// every tile's keys
+// every tile's keys (a lane's last item alone has so few: 256 / G * G is above 192 for G <= 64)
 template <typename C>
 __device__ __forceinline__ bool in_halves(const Kv4AttentionParams& p, const Piece& y) {
     return C::MT == 2 && y.x.qlen * p.G - y.r0 <= 128;
@@ -430,7 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         while (go && walk.next(p, y)) {
             const bool halves = in_halves<C>(p, y);
             const int row0 = halves ? 0 : mt * 128;  // the warpgroup's first row of the item
-            const int n = y.kt1 - y.kt0, units = halves ? n : n * C::UPT, nrows = min(C::ROWS, y.x.qlen * p.G - y.r0), r = row0 + row;
+            // an item's rows are those of its whole tokens: where G does not divide the tile, the places behind them stay empty
+            // (what follows is the next item's, whose keys go further)
+            const int n = y.kt1 - y.kt0, units = halves ? n : n * C::UPT, nrows = min(walk.tt * p.G, y.x.qlen * p.G - y.r0), r = row0 + row;
             const bool mine = r < nrows;
             // rows of q and o lie at `first` + the row's `rel` rows; a row of 128 is loaded by LR lanes, 16 bytes each
             constexpr int LR = D / 8, RPI = 32 / LR;
