@@ -222,7 +222,7 @@ def lib() -> ctypes.CDLL:
                                        ip, vp]
         L.gdn_conv_commit.argtypes = [cdp, vp, ip, vp, ip, ip, vp]
         i32 = ctypes.c_int32
-        L.gdn_page_plan.argtypes = [i32] * 5 + [vp] * 9
+        L.gdn_page_plan.argtypes = [i32] * 5 + [vp] * 10
         L.gdn_qk_norm_rope.argtypes = [vp] * 14
         L.gdn_kv4_read.argtypes = [vp, i32] + [vp] * 5
         L.gdn_kv4_attention.argtypes = [vp] * 9 + [ctypes.c_int64, vp, vp]

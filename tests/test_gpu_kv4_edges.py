@@ -3,13 +3,18 @@ launch limits of the page plan, intervals of the store's rounding around zero, v
 long contexts.  References and bounds are those of tests/kv4_ref.py unless a test derives its own."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import gated_deltanet_linear_mtp_gb300 as gdn
 import kv4_ref as ref
-from test_gpu_kv4 import I32, attend, check_attend, err_word, f64
+from test_gpu_kv4 import I32, attend, check_attend, check_rotated, check_store, err_word, f64, pool
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +37,45 @@ def test_attention_row_tiles_that_whole_tokens_do_not_fill(D, G):
         r["lse"].fill_(5.0)
         r["call"]()
         assert torch.equal(r["o"], o) and torch.equal(r["lse"], lse)
+
+
+# ---- page plan -----------------------------------------------------------------------------------------------------
+def plan_of_ones(B):
+    """A plan of B lanes without a token that bring one each, its call's arguments, and the slots that it gives."""
+    plan = gdn.PagePlan(*(torch.full((n,), -9, **I32) for n in (B + 1, B, B, B, B, 1)))
+    args = (torch.zeros(B, **I32), torch.ones(B, **I32), 16, torch.full((B, 2), -1, **I32), torch.zeros(B, **I32),
+            torch.arange(B, **I32), torch.zeros(1, **I32), plan, torch.zeros(1, **I32))
+    return plan, args, torch.arange(0, 16 * B, 16, **I32)
+
+
+def test_page_plan_on_the_stream_of_another_thread():
+    """A stream that a second thread makes (its handle lies beyond 32 bits), as the current one and as an argument, and a graph."""
+    failed = []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            for given in (None, s):
+                with torch.cuda.stream(s if given is None else torch.cuda.default_stream()):
+                    plan, args, want = plan_of_ones(300)
+                torch.cuda.synchronize()
+                with torch.cuda.stream(s if given is None else torch.cuda.default_stream()):
+                    gdn.gdn_page_plan(*args, stream=given)
+                s.synchronize()
+                assert torch.equal(plan.slot_map, want)
+            plan, args, want = plan_of_ones(40)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                gdn.gdn_page_plan(*args)
+            assert (plan.slot_map == -9).all()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(plan.slot_map, want)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert not failed, failed
