@@ -509,7 +509,7 @@ gdn_status gdn_page_plan(int32_t B, int32_t N, int32_t page_size, int32_t max_pa
                          const int32_t* kv_lens, const int32_t* new_lens, int32_t* block_tables, const int32_t* held,
                          const int32_t* free_pages, const int32_t* taken, const gdn_page_plan_out* out, int32_t* ticket,
                          int32_t* err_word, gdn_stream_t stream) {
-    if (B < 0 || B > 8192 || N < 0 || num_pages < 1 || max_pages < 1) return GDN_ERR_SHAPE;
+    if (B < 0 || B > kPlanMaxLanes || N < 0 || num_pages < 1 || max_pages < 1) return GDN_ERR_SHAPE;
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return GDN_ERR_SHAPE;
     if ((int64_t)num_pages * page_size >= (int64_t)1 << 31 || (int64_t)max_pages * page_size >= (int64_t)1 << 31)
         return GDN_ERR_SHAPE;

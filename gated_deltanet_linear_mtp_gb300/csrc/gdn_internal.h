@@ -127,6 +127,7 @@ struct PagePlanParams {
     int32_t* ticket;      // [1]: 0 between calls
     int32_t* err;
 };
+constexpr int kPlanMaxLanes = 8192;
 
 // The paged 4-bit cache as the kernels see it (gdn_kv4.cuh): codes [num_pages, 2, HK, page_size, D / 2], scales
 // [num_pages, 2, HK, page_size, D / 16].

@@ -14,6 +14,7 @@
 // former with one token of a thread at a time and a warp a lane for the new pages).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "gdn_common.cuh"
@@ -23,6 +24,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr size_t smem_bytes(int lanes) { return ((size_t)5 * lanes + 1) * 4; }
 
 struct LaneNeed {
     int64_t add;   // tokens this lane has in the packed order
@@ -178,17 +180,22 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(PagePlanParams 
 }  // namespace
 
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s) {
-    const size_t smem = ((size_t)5 * p.B + 1) * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(gdn_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // Shared memory is opened once on each device, for the most lanes: the default limit counts the kernel's static bytes too, and a
+    // limit set by each call for its own lanes could be lowered by another thread before the launch.
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(gdn_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kPlanMaxLanes));
         if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     // One CTA while that leaves its threads a few tokens and lanes each: it needs no ticket.  Then a CTA for 2048 tokens or
     // 128 lanes: more only repeat the scan.
     const int64_t want = ((int64_t)p.N + 2047) / 2048, lanes = (p.B + 127) / 128, most = want > lanes ? want : lanes;
     const int grid = p.N <= 4 * kThreads + 1024 && p.B <= kThreads ? 1 : (int)(most < 152 ? most : 152);
-    gdn_page_plan_kernel<<<grid, kThreads, smem, s>>>(p);
+    gdn_page_plan_kernel<<<grid, kThreads, smem_bytes(p.B), s>>>(p);
     return cudaGetLastError();
 }
 

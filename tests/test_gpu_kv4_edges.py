@@ -79,3 +79,53 @@ def test_page_plan_on_the_stream_of_another_thread():
     t.start()
     t.join()
     assert not failed, failed
+
+
+PLAN_SIZES = """
+import sys
+sys.path.insert(0, "tests")
+import torch
+import gated_deltanet_linear_mtp_gb300 as gdn
+from test_gpu_kv4_edges import plan_of_ones
+for B in range(2440, 2462):  # ascending, in a process that has made no larger call
+    plan, args, want = plan_of_ones(B)
+    gdn.gdn_page_plan(*args)
+    assert torch.equal(plan.slot_map, want), B
+print("sizes ok")
+"""
+
+
+def test_page_plan_sizes_around_the_default_shared_memory():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", PLAN_SIZES], capture_output=True, text=True, cwd=root, timeout=300)
+    assert p.returncode == 0 and "sizes ok" in p.stdout, p.stdout + p.stderr
+
+
+def test_page_plan_of_two_sizes_from_two_threads():
+    """Each thread plans on its own stream and buffers, one with little shared memory and one with much; the library is called
+    directly, so that the calls meet."""
+    failed, start = [], threading.Barrier(2)
+
+    def work(B):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            plan, a, want = plan_of_ones(B)
+        s.synchronize()
+        args = (B, B, 16, 2, B, *(x.data_ptr() for x in (a[0], a[1], a[3], a[4], a[5], a[6])), plan.ref, a[8].data_ptr(), None, s.cuda_stream)
+        call = gdn.lib().gdn_page_plan
+        start.wait()
+        for _ in range(20000):
+            status = call(*args)
+            if status != 0:
+                failed.append((B, status))
+                break
+        s.synchronize()
+        if not torch.equal(plan.slot_map, want):
+            failed.append((B, "slots"))
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in (2600, 8192)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
