@@ -733,7 +733,8 @@ def gdn_page_plan(kv_lens, new_lens, page_size, block_tables, held, free_pages, 
                   stream=None) -> None:
     """Block tables, slot map, positions and offsets of a step: lane b has ``kv_lens[b]`` cached tokens in ``held[b]``
     pages and brings ``new_lens[b]`` more.  New pages come from ``free_pages[taken:]`` into ``block_tables``
-    ``[B, max_pages]``; the rest goes into ``plan`` (a ``PagePlan``).  ``ticket`` is one int32, 0 before the first call."""
+    ``[B, max_pages]``; the rest goes into ``plan`` (a ``PagePlan``).  ``ticket`` is one int32, 0 before the first call.  Of no
+    lanes at all (B = 0), the plan is that of a step without tokens."""
     import torch
 
     L = lib()
@@ -744,12 +745,18 @@ def gdn_page_plan(kv_lens, new_lens, page_size, block_tables, held, free_pages, 
     if plan.device.index != dev:
         raise ValueError(f"plan is on {plan.device}, kv_lens on GPU {dev}")
     max_pages, num_pages = block_tables.shape[1], free_pages.shape[0]
-    _run(dev, stream, L.gdn_page_plan,
-         (B, plan.N, page_size, max_pages, num_pages, _ptr(kv_lens, "kv_lens", i32, (B,), dev),
-          _ptr(new_lens, "new_lens", i32, (B,), dev), _ptr(block_tables, "block_tables", i32, (B, max_pages), dev),
-          _ptr(held, "held", i32, (B,), dev), _ptr(free_pages, "free_pages", i32, (num_pages,), dev),
-          _ptr(taken, "taken", i32, (1,), dev), plan.ref, _ptr(ticket, "ticket", i32, (1,), dev),
-          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_page_plan")
+    args = (B, plan.N, page_size, max_pages, num_pages, _ptr(kv_lens, "kv_lens", i32, (B,), dev),
+            _ptr(new_lens, "new_lens", i32, (B,), dev), _ptr(block_tables, "block_tables", i32, (B, max_pages), dev),
+            _ptr(held, "held", i32, (B,), dev), _ptr(free_pages, "free_pages", i32, (num_pages,), dev),
+            _ptr(taken, "taken", i32, (1,), dev), plan.ref, _ptr(ticket, "ticket", i32, (1,), dev),
+            _ptr(err_word, "err_word", i32, (1,), dev))
+    _run(dev, stream, L.gdn_page_plan, args, "gdn_page_plan")
+    if B == 0:  # the library writes nothing then, and an earlier step's slots must not stay
+        with torch.cuda.stream(stream):
+            plan.cu_seqlens.zero_()
+            plan.positions.zero_()
+            plan.slot_map.fill_(-1)
+            plan.taken.copy_(taken)
 
 
 def _rows(t, name: str, dtype, shape, dev: int):

@@ -381,7 +381,8 @@ typedef struct gdn_page_plan_out {
  * are negative, beyond max_pages pages or (cached) beyond its held pages is skipped likewise, with GDN_ERRBIT_SEQLEN; a
  * step of more than N tokens sets that bit too, and its tokens beyond N are not written.  A page outside
  * 0 .. num_pages - 1 gives slot -1 and GDN_ERRBIT_INDEX.  block_tables [B, max_pages], free_pages [num_pages].  ticket:
- * one int32, 0 before the first call and left 0, used by one call at a time.  B 0 .. 8192.
+ * one int32, 0 before the first call and left 0, used by one call at a time.  B 0 .. 8192; with B 0 nothing is enqueued and
+ * nothing written, so a caller that goes on to use the outputs of such a step sets them: cu_seqlens[0] = 0, slots -1.
  */
 GDN_API gdn_status gdn_page_plan(int32_t B, int32_t N, int32_t page_size, int32_t max_pages, int32_t num_pages,
                                  const int32_t* kv_lens, const int32_t* new_lens, int32_t* block_tables,

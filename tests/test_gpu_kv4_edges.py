@@ -129,3 +129,16 @@ def test_page_plan_of_two_sizes_from_two_threads():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("N", [0, 1, 5000])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_page_plan_of_no_lanes(N, inplace):
+    """A step without lanes leaves nothing of an earlier step in its buffers."""
+    taken = torch.full((1,), 2, **I32)
+    plan = gdn.PagePlan(torch.full((1,), 9, **I32), torch.full((N,), 9, **I32), torch.full((N,), 9, **I32), torch.zeros(0, **I32),
+                        torch.zeros(0, **I32), taken if inplace else torch.full((1,), 9, **I32))
+    ticket, err, none = torch.zeros(1, **I32), err_word(), torch.zeros(0, **I32)
+    gdn.gdn_page_plan(none, none, 16, torch.zeros((0, 4), **I32), none, torch.arange(7, **I32), taken, plan, ticket, err)
+    assert plan.cu_seqlens.tolist() == [0] and not plan.positions.any() and (plan.slot_map == -1).all()
+    assert int(plan.taken) == 2 and int(ticket) == 0 and int(err) == 0
