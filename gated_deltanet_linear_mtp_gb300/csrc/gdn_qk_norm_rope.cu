@@ -506,15 +506,16 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                     uint32_t w = 0;
 #pragma unroll
                     for (int j = 4 * k; j < 4 * k + 4; j += 2) {
-                        // the codes of v and, sign apart, of both ends of where the exact value lies: the bounds grow with |v|,
-                        // so that the end towards 0 may pass it only where both ends' codes are 0
+                        // the codes of v and of both ends of where the exact value lies.  The bound goes by both numbers of a
+                        // pair, so the ends may lie on both sides of 0, and equally far: signs count but for codes of 0
                         const F2 q = mul(f2(v[j], v[j + 1]), f2(rsc, rsc));
                         const float ea = bound(j) * rsc, eb = bound(j + 1) * rsc;
                         const float2 low = split(add(q, f2(-ea, -eb))), high = split(add(q, f2(ea, eb)));
                         const float2 mid = split(q);
                         const uint32_t b0 = f32x2_to_e2m1(low.x, low.y), b1 = f32x2_to_e2m1(high.x, high.y);
-                        diff |= (b0 ^ b1) & 0x77u;
-                        w |= ((b0 & 0x77u) | (mid.x < 0.f ? 8u : 0u) | (mid.y < 0.f ? 0x80u : 0u)) << (4 * (j & 3));
+                        const uint32_t m0 = b0 & 0x77u;
+                        diff |= (b0 ^ b1) & (0x77u | ((m0 + 0x77u) & 0x88u));  // (a magnitude + 7 reaches the sign's bit if it is not 0)
+                        w |= (m0 | (mid.x < 0.f ? 8u : 0u) | (mid.y < 0.f ? 0x80u : 0u)) << (4 * (j & 3));
                     }
                     *reinterpret_cast<uint16_t*>(p.kv.codes + row * (D / 2) + c * 2) = (uint16_t)w;
                     if ((c & 3) == 0) p.kv.scales[row * (D / 16) + c / 4] = (uint8_t)sb;

@@ -142,3 +142,50 @@ def test_page_plan_of_no_lanes(N, inplace):
     gdn.gdn_page_plan(none, none, 16, torch.zeros((0, 4), **I32), none, torch.arange(7, **I32), taken, plan, ticket, err)
     assert plan.cu_seqlens.tolist() == [0] and not plan.positions.any() and (plan.slot_map == -1).all()
     assert int(plan.taken) == 2 and int(ticket) == 0 and int(err) == 0
+
+
+# ---- the store's codes -----------------------------------------------------------------------------------------
+def store_keys(k, kw, pos, freq, k_scale=1.0, eps=1e-6, inter=False, v=None, v_scale=1.0):
+    """The keys (and values) of k [N, HK, D] stored at slots 0 .. N - 1 -> (cache, slots, error bits)."""
+    N, HK, D = k.shape
+    cache, slots, err = pool(-(-N // 16), HK, 16, D, k_scale, v_scale), np.arange(N, dtype=np.int32), err_word()
+    q = torch.ones((N, 1, D), dtype=k.dtype, device="cuda")
+    gdn.gdn_qk_norm_rope(q, k, kw, kw, pos, freq, torch.empty_like(q), v=k if v is None else v, cache=cache,
+                         slot_map=torch.tensor(slots, **I32), err_word=err, eps=eps, interleaved=inter)
+    return cache, slots, int(err)
+
+
+@pytest.mark.parametrize("exponent", [-8, -7])
+def test_keys_whose_interval_of_rounding_holds_zero(exponent):
+    """A number that is 0 but for the rounding of its far larger partner, which lies in another group, beside numbers so small
+    that this rounding passes their group's borders."""
+    small = np.geomspace(1e-6, 3e-5, 64)
+    x = np.zeros((len(small), 1, 128), np.float32)
+    x[:, 0, 0] = small
+    x[:, 0, 65] = x[:, 0, 70] = 1.0
+    k = torch.tensor(x).cuda()
+    w, freq = torch.ones(128, device="cuda"), torch.tensor(1e4 ** (-np.arange(0, 128, 2) / 128), dtype=torch.float32).cuda()
+    for at in (0, 12345):
+        pos = torch.full((len(small),), at, **I32)
+        cache, slots, bits = store_keys(k, w, pos, freq, 2.0 ** exponent)
+        want = ref.norm_rope(f64(k), f64(w), pos.cpu().numpy(), f64(freq), float(np.float32(1e-6)), False)[0]
+        check_store(cache, slots, 0, want, 2.0 ** exponent)
+        assert bits == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+def test_keys_of_many_magnitudes(dtype, inter):
+    """Numbers of one row over eight decades, a third of them 0, at cache scales down to their smallest."""
+    rng = np.random.default_rng(21)
+    for D, R in ((64, 64), (128, 64), (256, 256)):
+        x = rng.normal(size=(300, 2, D)) * 10.0 ** rng.uniform(-8, 0, size=(300, 2, D)) * (rng.random((300, 2, D)) > 0.33)
+        k = torch.tensor(x, dtype=torch.float32).to(dtype).cuda()
+        w = torch.tensor(1 + 0.2 * rng.normal(size=D), dtype=torch.float32).cuda()
+        freq = torch.tensor(1e4 ** (-np.arange(0, R, 2) / R), dtype=torch.float32).cuda()
+        pos = torch.tensor(rng.integers(0, 100000, 300) * (rng.random(300) > 0.3), **I32)
+        for e in (0, -6, -10, -16):
+            cache, slots, bits = store_keys(k, w, pos, freq, 2.0 ** e, inter=inter)
+            want = ref.norm_rope(f64(k), f64(w), pos.cpu().numpy(), f64(freq), float(np.float32(1e-6)), inter)[0]
+            check_store(cache, slots, 0, want, 2.0 ** e)
+            assert bits == 0
