@@ -385,6 +385,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                     top = fmaxf(top, __shfl_xor_sync(gmask, top, 1));
                     const uint32_t sb = f32_to_e4m3(div_odd(fminf(top / p.kv.v_scale, kMaxF32), 6.f));
                     const float s = e4m3_to_f32(sb) * p.kv.v_scale, inv = 1.f / s;
+                    if (sb == 0x7eu) {  // the largest scale: what passes the codes is cut first, so that no quotient passes the type
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(v[j], -8.f * s), 8.f * s);
+                    }
                     uint32_t w = 0;
                     if (sb) {
 #pragma unroll

@@ -189,3 +189,19 @@ def test_keys_of_many_magnitudes(dtype, inter):
             want = ref.norm_rope(f64(k), f64(w), pos.cpu().numpy(), f64(freq), float(np.float32(1e-6)), inter)[0]
             check_store(cache, slots, 0, want, 2.0 ** e)
             assert bits == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("exponent", [-32, -20, -9, -8, 0, 32])
+def test_values_beyond_the_cache_keep_their_sign(dtype, exponent):
+    """Infinities, and finite numbers whose quotient by the scale passes the type, are held as the largest number of their sign."""
+    v = torch.zeros((4, 1, 64), dtype=dtype, device="cuda")
+    v[0, 0, :4] = torch.tensor([float("-inf"), float("inf"), -3e38, 1.0])
+    v[1, 0, :4] = torch.tensor([-3e38, 3e38, -1e30, -1.0])
+    v[2, 0, 16:20] = torch.tensor([-1e10, 1e10, 5.0, float("-inf")])
+    v[3, 0, 40:44] = torch.tensor([-1e10, 3e10, -2e10, -2.5])
+    k, w = torch.ones((4, 1, 64), dtype=dtype, device="cuda"), torch.ones(64, device="cuda")
+    cache, slots, bits = store_keys(k, w, torch.zeros(4, **I32), torch.zeros(0, device="cuda"), v=v, v_scale=2.0 ** exponent)
+    with np.errstate(over="ignore"):
+        check_store(cache, slots, 1, f64(v), 2.0 ** exponent)
+    assert bits == gdn.ERRBIT_NONFINITE
