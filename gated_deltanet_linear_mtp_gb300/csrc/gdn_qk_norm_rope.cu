@@ -140,6 +140,13 @@ __device__ __forceinline__ float div_odd(float a, float b) {
     return fmaf(q, b, -a) != 0.f ? __uint_as_float(__float_as_uint(q) | 1u) : q;
 }
 
+// 1 / sqrt(x) of a normal number, to 2^-22 (rsqrtf has three instructions more, for subnormal ones); infinity of 0
+__device__ __forceinline__ float rsqrt_normal(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // The largest magnitude of eight numbers, by their bits: NaN where one is among them, else infinity
 __device__ __forceinline__ float largest(const float (&v)[8]) {
     uint32_t m = 0;
@@ -187,6 +194,23 @@ struct Chunks {
     }
 };
 
+// A row whose squares may leave fp32 is normed after a multiplication by a power of two, 1 / 2^E: 2^E is about the larger of the
+// row's largest magnitude `top` (its bits) and sqrt(eps), so that x' = x / 2^E, mean x'^2 and eps' = eps / 2^2E neither overflow nor
+// lose a square that counts, and x' / sqrt(mean x'^2 + eps') is the same number.
+constexpr float kLeastMean = 0x1p-100f;  // squares below fp32's normal numbers are lost beside it
+__device__ __forceinline__ float row_unit(uint32_t top, float eps) {
+    const uint32_t of_eps = eps > 0.f ? ((__float_as_uint(eps) >> 23) + 128u) >> 1 : 0u;
+    const uint32_t e = min(max(max(top >> 23, of_eps), 1u), 253u);
+    return __uint_as_float((254u - e) << 23);
+}
+// 1 / 2^E of a row of which these lanes hold 8 numbers each
+template <int D>
+__device__ __forceinline__ float row_unit(const float (&x)[8], float eps, uint32_t gmask) {
+    uint32_t top = __float_as_uint(largest(x));
+    for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(gmask, top, o));
+    return row_unit(top, eps);
+}
+
 // One key row in two-float arithmetic, by the D / 8 lanes that hold its dimensions: its codes and scales into the cache.
 // `ex`: a place for D / 4 chunks' maxima, of this row's lanes alone.
 template <typename T, int D, bool INTER>
@@ -194,26 +218,27 @@ __device__ __noinline__ void store_key_exact(const QkNormRopeParams& p, int t, i
     const Chunks<INTER> ch(l, p.R);
     const T* x = (const T*)p.k + (int64_t)t * p.k_stride + (int64_t)head * D;
     const int d[2] = {ch.a * 4, ch.b * 4};
+    float v[8];
+    for (int j = 0; j < 8; ++j) v[j] = to_f32(x[d[j >> 2] + (j & 3)]);
+    const float unit = row_unit<D>(v, p.eps, gmask);
     Df ss{0.f, 0.f};
     for (int j = 0; j < 8; ++j) {
-        const float v = to_f32(x[d[j >> 2] + (j & 3)]), q = __fmul_rn(v, v);
-        ss = df_add(ss, {q, __fmaf_rn(v, v, -q)});
+        v[j] *= unit;
+        const float q = __fmul_rn(v[j], v[j]);
+        ss = df_add(ss, {q, __fmaf_rn(v[j], v[j], -q)});
     }
     for (int o = D / 16; o > 0; o >>= 1) {
         const float h = __shfl_xor_sync(gmask, ss.h, o), lo = __shfl_xor_sync(gmask, ss.l, o);
         ss = df_add(ss, {h, lo});
     }
-    const Df mean = df_add({ss.h * (1.f / D), ss.l * (1.f / D)}, {p.eps, 0.f});
+    const Df mean = df_add({ss.h * (1.f / D), ss.l * (1.f / D)}, {p.eps * unit * unit, 0.f});
     const float r0 = rsqrtf(mean.h);
     const Df one = df_mul(df_mul(mean, {r0, 0.f}), {r0, 0.f});
     const float e = __fadd_rn(__fadd_rn(1.f, -one.h), -one.l);
     const Df rs = df_norm(r0, r0 * e * fmaf(0.375f, e, 0.5f));
     Df z[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int at = d[j >> 2] + (j & 3);
-        z[j] = df_mul(df_mul({to_f32(x[at]), 0.f}, rs), {p.kw[at], 0.f});
-    }
+    for (int j = 0; j < 8; ++j) z[j] = df_mul(df_mul({v[j], 0.f}, rs), {p.kw[d[j >> 2] + (j & 3)], 0.f});
     if (ch.rot) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -413,15 +438,31 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                 }
                 continue;
             }
-            F2 acc = mul(x[0][0], x[0][0]);
-            acc = fma(x[0][1], x[0][1], acc);
-            acc = fma(x[1][0], x[1][0], acc);
-            acc = fma(x[1][1], x[1][1], acc);
-            const float2 two = split(acc);
-            float ss = two.x + two.y;
+            auto squares = [&]() {  // of the row
+                F2 acc = mul(x[0][0], x[0][0]);
+                acc = fma(x[0][1], x[0][1], acc);
+                acc = fma(x[1][0], x[1][0], acc);
+                acc = fma(x[1][1], x[1][1], acc);
+                const float2 two = split(acc);
+                float ss = two.x + two.y;
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o);
-            const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o);
+                return ss;
+            };
+            float mean = fmaf(squares(), 1.f / D, p.eps);
+            if (!(mean >= kLeastMean && mean <= kMaxF32)) {  // the same for all lanes of a row
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = split(x[j >> 1][j & 1]);
+                    v[2 * j] = a.x, v[2 * j + 1] = a.y;
+                }
+                const float unit = row_unit<D>(v, p.eps, gmask);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j >> 1][j & 1] = mul(x[j >> 1][j & 1], f2(unit, unit));
+                mean = fmaf(squares(), 1.f / D, p.eps * unit * unit);
+            }
+            const float rs = rsqrt_normal(mean);
             const F2 rr = f2(rs, rs);
             const float4 wa = s_w[is_k][ch.a], wb = s_w[is_k][ch.b];
             F2 y[2][2], z[2][2];

@@ -205,3 +205,43 @@ def test_values_beyond_the_cache_keep_their_sign(dtype, exponent):
     with np.errstate(over="ignore"):
         check_store(cache, slots, 1, f64(v), 2.0 ** exponent)
     assert bits == gdn.ERRBIT_NONFINITE
+
+
+# ---- rows whose squares leave fp32 -----------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-33, 1e-6])
+@pytest.mark.parametrize("D,R,inter", [(64, 32, False), (128, 128, True), (256, 64, False)])
+def test_rows_whose_squares_leave_the_type(dtype, eps, D, R, inter):
+    """Rows whose sum of squares is beyond fp32 or below its normal numbers are normed, rotated and stored like others."""
+    rng = np.random.default_rng(D)
+    size = np.array([3e37, 1e30, 2e19, 1e10, 1.0, 1e-15, 1e-19, 1e-23, 1e-30, 1e-37, 4e-40])
+    x = rng.normal(size=(len(size), 2, D)) * size[:, None, None]
+    x[2, 1] *= rng.random(D) > 0.9  # beside numbers of another size
+    x[2, 1, 5] = 1e38
+    x[8, 1, ::3] = 1e-38
+    k = torch.tensor(x, dtype=torch.float32).to(dtype).cuda()
+    w = torch.tensor(1 + 0.2 * rng.normal(size=D), dtype=torch.float32).cuda()
+    freq = torch.tensor(1e4 ** (-np.arange(0, R, 2) / R), dtype=torch.float32).cuda()
+    pos = torch.tensor(rng.integers(0, 10000, len(size)), **I32)
+    q_out, k_out = torch.full_like(k, 7.0), torch.full_like(k, 7.0)
+    e32 = float(np.float32(eps))
+    gdn.gdn_qk_norm_rope(k, k, w, w, pos, freq, q_out, k_out, eps=eps, interleaved=inter)
+    want = check_rotated(q_out, k, w, pos, freq, e32, inter, dtype, "q")
+    check_rotated(k_out, k, w, pos, freq, e32, inter, dtype, "k")
+    for e in (0, -12):
+        cache, slots, bits = store_keys(k, w, pos, freq, 2.0 ** e, eps, inter, v=torch.zeros_like(k))
+        check_store(cache, slots, 0, want, 2.0 ** e)
+        assert bits == 0
+
+
+def test_rows_of_zeros_without_epsilon_and_infinite_rows():
+    """0 / 0 is no number, whatever the path: such keys are held as 0 with their bit; so is what stands beside an infinity."""
+    k = torch.ones((3, 1, 64), device="cuda")
+    k[0] = 0.0
+    k[1, 0, 7] = float("inf")
+    w, pos, freq = torch.ones(64, device="cuda"), torch.zeros(3, **I32), torch.zeros(0, device="cuda")
+    out = torch.empty_like(k)
+    gdn.gdn_qk_norm_rope(k, k, w, w, pos, freq, out, torch.empty_like(k), eps=0.0)
+    assert out[0].isnan().all() and out[1, 0, 7].isnan() and not out[1, 0, :7].any() and (out[2] == 1.0).all()
+    cache, _, bits = store_keys(k, w, pos, freq, eps=0.0)
+    assert bits == gdn.ERRBIT_NONFINITE and not cache.codes[0, 0, 0, :2].any() and not cache.scales[0, 0, 0, :2].any()
