@@ -16,7 +16,12 @@ namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;  // a score may pass the running maximum by 2^kSlack before that moves
+// P = 2^(s - m) with the reference m = (running maximum) - kLift, which moves only where a score passes that maximum by more than
+// kSlack (in units of log 2): P reaches 2^15, which f16 holds, and its subnormal steps of 2^-24 are 2^-31 of the row's largest or
+// less.  With m at the maximum itself, keys below 2^-25 of the largest vanished from P V while they counted in l: with 16 keys
+// above a million of them at e^-19, o lost all of its 3.5e-4.
+constexpr float kSlack = 8.f;
+constexpr float kLift = 7.f;
 
 // Byte offset of 16-byte chunk c of token row r in a tile of codes, as TMA's swizzle of the row's size leaves it
 template <int D>

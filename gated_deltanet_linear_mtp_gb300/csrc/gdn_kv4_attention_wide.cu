@@ -15,9 +15,9 @@
 // Measured: those two chunks 530 us, 1.17 PFLOP/s; 16 ragged prompts of up to 2048 tokens, HQ 16, HK 2, D 128, 135 us, 0.54
 // PFLOP/s; the 256 lanes 160 us, 0.98 TB/s.  What is left above the products: the waits of the issuing threads and the
 // softmax's way (2000 cycles a unit of 64 keys where the products take 1280), and an item's begin and end.
-// The running maximum moves only where a score passes it by more than 8 (in units of log 2; then that thread scales its row of
-// O in tensor memory), so O stays in tensor memory throughout.
-// Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16, fp32.
+// The reference m of P = 2^(s - m) moves only where a score passes the running maximum by more than 8 (in units of log 2; then
+// that thread scales its row of O in tensor memory), so O stays in tensor memory throughout.
+// Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16 lifted by kLift, fp32.
 //
 // Work split: all tiles of all items are numbered and each CTA (one an SM) takes an equal run of them, since the rows of a
 // prompt see anything from few to all keys and items of whole rows leave SMs idle at the end; parts are joined by the decode
@@ -510,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
 #pragma unroll
                     for (int j = 4; j < 16; ++j) t4[j & 3] = fmaxf(t4[j & 3], x[j]);
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
-                    const bool move = top > m + kSlack;
+                    const bool move = top > m + (kSlack + kLift);
                     if (__any_sync(~0u, move)) {
-                        const float mn = move ? top : m;
+                        const float mn = move ? top - kLift : m;
                         const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
                         m = mn;
                         l *= f;

@@ -245,3 +245,36 @@ def test_rows_of_zeros_without_epsilon_and_infinite_rows():
     assert out[0].isnan().all() and out[1, 0, 7].isnan() and not out[1, 0, :7].any() and (out[2] == 1.0).all()
     cache, _, bits = store_keys(k, w, pos, freq, eps=0.0)
     assert bits == gdn.ERRBIT_NONFINITE and not cache.codes[0, 0, 0, :2].any() and not cache.scales[0, 0, 0, :2].any()
+
+
+# ---- long contexts -----------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 12, 20, 40])  # with one head: each size of item of either kernel
+@pytest.mark.parametrize("L,gap", [(131072, 18.0), (1000003, 19.0), (65536, 12.0)])
+def test_attention_many_small_weights_beside_large_ones(D, T, L, gap):
+    """Every 16th of the first 256 keys has score `gap` and value 0, the others score 0 and value 1: o = n e^-gap / (16 + n e^-gap)
+    for the n of these that a token sees; lanes enough for each CTA to hold a whole one.  P is held in f16 at 2^7 times (at
+    least) its share of the row's largest, so a weight is off by 2^-11 of itself or by 2^-25 2^-7; the exponentials are off
+    by 2^-18 at most, and the sums, in L / 16 steps at most, by 2^-23 a step."""
+    B, page = 304, 256
+    codes = torch.zeros((2, 2, 1, page, D // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((2, 2, 1, page, D // 16), 0x38, dtype=torch.uint8, device="cuda")  # 1.0
+    codes[0, 0, 0, ::16, 0] = 0x02  # 1.0 in the first dimension
+    codes[:, 1] = 0x22              # the values: 1.0
+    codes[0, 1, 0, ::16] = 0
+    table = torch.ones((B, -(-L // page)), **I32)
+    table[:, 0] = 0
+    q = torch.zeros((B * T, 1, D), dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = gap  # exact in bf16
+    o, lse, err = torch.full_like(q, 9.0), torch.full((B * T, 1), 9.0, device="cuda"), err_word()
+    gdn.gdn_kv4_attention(q, gdn.Kv4Cache(codes, scales), table, torch.full((B,), L, **I32), o,
+                          gdn.kv4_attention_workspace(B, T, 1, 1, D), lse=lse, scale=1.0, err_word=err)
+    n = L - T + np.arange(T, dtype=np.float64) - 15
+    l = 16 + n * np.exp(-gap)
+    want = (l - 16) / l
+    sums = L / 16 * 2.0 ** -23
+    bound = 2.0 ** -8 * want + (want * (2.0 ** -11 + 2.0 ** -18 + sums) + n * 2.0 ** -32 / l) * (1 + 2.0 ** -8)
+    d = np.abs(f64(o).reshape(B, T, D) - want[:, None])
+    assert (d <= bound[:, None]).all(), (float(d.max()), float(want.max()), float(bound.max()))
+    assert (np.abs(f64(lse).reshape(B, T) - gap - np.log(l)) <= 2.0 ** -21 * (gap + 4) + 2.0 ** -18 + sums).all()
+    assert int(err) == 0
