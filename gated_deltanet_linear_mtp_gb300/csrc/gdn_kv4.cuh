@@ -64,6 +64,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Two f16 numbers, a NaN as 0
+__device__ __forceinline__ uint32_t nan_as_zero(uint32_t a) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&a);
+    return a & __heq2_mask(h, h);
+}
+
 __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);

@@ -360,10 +360,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
                             if (kt * C::TILE + rb >= y.x.kv) z = 0;
                         }
                         if constexpr (D == 256) {
-                            sv[i][0] = e4m3x2_to_f16(__byte_perm(x, z, 0x0040));
-                            sv[i][1] = e4m3x2_to_f16(__byte_perm(x, z, 0x0051));
+                            sv[i][0] = nan_as_zero(e4m3x2_to_f16(__byte_perm(x, z, 0x0040)));
+                            sv[i][1] = nan_as_zero(e4m3x2_to_f16(__byte_perm(x, z, 0x0051)));
                         } else {
-                            sv[i][0] = e4m3x2_to_f16(x | (z << 8));
+                            sv[i][0] = nan_as_zero(e4m3x2_to_f16(x | (z << 8)));
                         }
                     }
 #pragma unroll

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
         uint32_t pair = 0, stage = 0;  // ring pairs; stages of the copies
         Piece y{};
         bool go = true;
-        auto tile = [&](int kt, uint8_t* dst) {  // the next stage into an operand tile
+        auto tile = [&](int kt, bool values, uint8_t* dst) {  // the next stage into an operand tile
             const uint32_t st = stage % C::STAGES;
             go = warp_wait(raw_full + 8 * st, (stage / C::STAGES) & 1);
             if (!go) return;
@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
             }
 #pragma unroll
             for (int c = 0; c < RUN / 32; ++c) {
-                const uint32_t f2 = e4m3x2_to_f16(two[c]);
+                uint32_t f2 = e4m3x2_to_f16(two[c]);
+                if (values) f2 = nan_as_zero(f2);  // a token that does not see the value has 0 for P
                 const uint32_t sf[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
                 const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 uint8_t* dst = smem + C::RING_AT + at * 2 * C::KVBYTES;
 #pragma unroll 1
                 for (int which = kt > y.kt0 ? 0 : 1; which < (kt < y.kt1 ? 2 : 1) && go; ++which)
-                    tile(kt - 1 + which, dst + which * C::KVBYTES);
+                    tile(kt - 1 + which, which == 0, dst + which * C::KVBYTES);
                 if (!go) break;
                 fence_proxy_async_smem();
                 __syncwarp();

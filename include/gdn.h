@@ -444,11 +444,12 @@ typedef struct gdn_kv4_attention_dims {
  *     o = sum_j p_j v_j / sum_j p_j,  lse = log sum_j exp(scale q . k_j)
  * q, o [N, HQ, D] bf16 on 16 bytes; lse [N, HQ] fp32 or NULL; cu_seqlens [B + 1] or NULL (then N = B * max_q and lane b
  * holds rows b * max_q ..); kv_lens [B]: cached tokens, the step's included; block_tables [B, max_pages] (entries beyond a
- * lane's tokens are not read).  A token that sees no key gets o = 0 and lse = -inf.  Softmax statistics and sums are fp32.  Bounds that are negative,
- * decreasing, longer than max_q or beyond N, and a kv_len outside 0 .. max_pages * page_size, skip the lane
- * (GDN_ERRBIT_SEQLEN; its rows stay as they are); the keys and values of a page outside the cache count as zeros
- * (GDN_ERRBIT_INDEX).  workspace: at least gdn_kv4_attention_workspace bytes on 16 bytes, used by one call at a time; its
- * contents need not be kept.
+ * lane's tokens are not read).  A token that sees no key gets o = 0 and lse = -inf.  A scale byte of NaN (no store writes one)
+ * counts as 0 in the values, so that it does not reach tokens which do not see it; in the keys it makes NaN of the tokens
+ * that see it.  Softmax statistics and sums are fp32.  Bounds that are negative, decreasing, longer than max_q or beyond N, and
+ * a kv_len outside 0 .. max_pages * page_size, skip the lane (GDN_ERRBIT_SEQLEN; its rows stay as they are); the keys and
+ * values of a page outside the cache count as zeros (GDN_ERRBIT_INDEX).  workspace: at least gdn_kv4_attention_workspace bytes
+ * on 16 bytes, used by one call at a time; its contents need not be kept.
  */
 GDN_API gdn_status gdn_kv4_attention(const gdn_kv4_attention_dims* dims, const gdn_kv4_cache* cache, const void* q,
                                      const int32_t* cu_seqlens, const int32_t* block_tables, const int32_t* kv_lens,

@@ -278,3 +278,39 @@ def test_attention_many_small_weights_beside_large_ones(D, T, L, gap):
     assert (d <= bound[:, None]).all(), (float(d.max()), float(want.max()), float(bound.max()))
     assert (np.abs(f64(lse).reshape(B, T) - gap - np.log(l)) <= 2.0 ** -21 * (gap + 4) + 2.0 ** -18 + sums).all()
     assert int(err) == 0
+
+
+# ---- what a cache may hold -----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,HQ", [(3, 2), (4, 4), (8, 4), (40, 2), (150, 2)])
+def test_attention_values_with_a_nan_scale(D, T, HQ):
+    """A scale byte of NaN, which no store writes, in the values: its 16 numbers count as 0, so that the tokens which do not see
+    them keep their bits."""
+    rng = np.random.default_rng(D + T)
+    r = attend(rng, [T, 1], [T + 61, 30], HQ, 1, D, 64, spoil=False)
+    base = r["o"].clone()
+    L = T + 61
+    for j, groups in ((L - 1, slice(None)), (L - 2, slice(1, 2)), (5, slice(0, 1))):
+        page, row = int(r["tables"][0, j // 64]), j % 64
+        r["cache"].scales[page, 1, 0, row, groups] = 0x7F if j != L - 2 else 0xFF
+        view = r["num"][page, 1, 0, row].reshape(-1, 16)
+        view[groups] = 0.0
+        if j == L - 2:
+            r["call"]()
+            assert torch.equal(r["o"][:T - 2], base[:T - 2]) and torch.equal(r["o"][T:], base[T:])
+    r["call"]()
+    check_attend(r)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,HQ", [(4, 4), (40, 2)])
+def test_attention_keys_with_a_nan_scale(D, T, HQ):
+    """In the keys it makes NaN of the tokens that see it, and of no other."""
+    rng = np.random.default_rng(D + T)
+    r = attend(rng, [T, 1], [T + 61, 30], HQ, 1, D, 64, spoil=False)
+    base = r["o"].clone()
+    j = T + 61 - 2
+    r["cache"].scales[int(r["tables"][0, j // 64]), 0, 0, j % 64, 1] = 0x7F
+    r["call"]()
+    assert torch.equal(r["o"][:T - 2], base[:T - 2]) and torch.equal(r["o"][T:], base[T:])
+    assert r["o"][T - 2:T].isnan().all() and r["lse"][T - 2:T].isnan().all() and not r["lse"][:T - 2].isnan().any()
