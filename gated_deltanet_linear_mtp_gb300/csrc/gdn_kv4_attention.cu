@@ -147,11 +147,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) gdn_kv4_attention_kernel(
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            // top's power of two, kept where it and its reciprocal are normal numbers
-            uint32_t e = __float_as_uint(top) >> 23;
-            e = e < 30 ? 30 : e > 224 ? 224 : e;
-            const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
-            if (lane == 0) s_sc[r] = up * p.scale * p.kv.k_scale * kLog2e;
+            const uint32_t e = row_exponent(__float_as_uint(top) >> 23);
+            const float down = __uint_as_float((254u - e) << 23);
+            if (lane == 0) s_sc[r] = row_scale(p, e, p.scale);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 // dimension d belongs to lane c's run: for D 128 c = d / 32 and k step (d % 32) / 4; for 64 runs of 16;

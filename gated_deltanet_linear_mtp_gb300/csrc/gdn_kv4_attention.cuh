@@ -23,6 +23,15 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;
 constexpr float kLift = 7.f;
 
+// A query row is held in f16 over the power of two of its largest number: the biased exponent, kept where the power and its
+// reciprocal are normal numbers (NaN and infinity count as the largest), so a finite row loses nothing at either end of bf16.
+__device__ __forceinline__ uint32_t row_exponent(uint32_t e) { return e < 1 ? 1 : e > 253 ? 253 : e; }
+// What a score of such a row is multiplied by; finite, so that a score of 0 stays one
+__device__ __forceinline__ float row_scale(const Kv4AttentionParams& p, uint32_t e, float scale) {
+    const float x = __uint_as_float(e << 23) * scale * p.kv.k_scale * kLog2e;
+    return fminf(fmaxf(x, -3.402823466e38f), 3.402823466e38f);
+}
+
 // Byte offset of 16-byte chunk c of token row r in a tile of codes, as TMA's swizzle of the row's size leaves it
 template <int D>
 __device__ __forceinline__ int code_off(int r, int c) {

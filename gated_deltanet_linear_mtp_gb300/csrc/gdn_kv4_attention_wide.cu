@@ -459,13 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv4_attention_wide_kernel(con
                 const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(128, row, c));
                 top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
             }
-            // the exponent, kept where its power of two and the reciprocal are normal numbers (NaN and infinity count as the
-            // largest)
-            uint32_t e = max(top2 & 0xffffu, top2 >> 16) >> 7;
-            e = e < 30 ? 30 : e > 224 ? 224 : e;
+            const uint32_t e = row_exponent(max(top2 & 0xffffu, top2 >> 16) >> 7);
             const float down = __uint_as_float((254u - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
             // (at least 2^-120: a masked score of -inf must stay one)
-            const float sc = fmaxf(__uint_as_float(e << 23) * fabsf(p.scale) * p.kv.k_scale * kLog2e, 0x1p-120f);
+            const float sc = fmaxf(row_scale(p, e, fabsf(p.scale)), 0x1p-120f);
 #pragma unroll 2
             for (int c = 0; c < LR; ++c) {
                 uint4* at = reinterpret_cast<uint4*>(stage + sw128(128, row, c));

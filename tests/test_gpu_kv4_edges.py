@@ -314,3 +314,23 @@ def test_attention_keys_with_a_nan_scale(D, T, HQ):
     r["call"]()
     assert torch.equal(r["o"][:T - 2], base[:T - 2]) and torch.equal(r["o"][T:], base[T:])
     assert r["o"][T - 2:T].isnan().all() and r["lse"][T - 2:T].isnan().all() and not r["lse"][:T - 2].isnan().any()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("exponent", [120, 100, -100, -115])
+def test_attention_queries_of_any_size(D, T, exponent):
+    """Queries times a power of two, and the scale by its reciprocal: the same scores."""
+    rng = np.random.default_rng(D + T)
+    r = attend(rng, [T, T], [T + 200, T], 4, 2, D, 64)
+    r["q"][r["q"].abs() < 2.0 ** -9] = 0.0  # what is left is a normal number after the smallest factor too
+    r["call"]()
+    check_attend(r, rows_per_lane=4)
+    base = r["o"].clone(), r["lse"].clone()
+    q = (r["q"].float() * 2.0 ** exponent).bfloat16()
+    assert torch.equal(q.float() * 2.0 ** -exponent, r["q"].float())
+    o, lse, err = torch.full_like(q, 9.0), torch.full_like(r["lse"], 9.0), err_word()
+    gdn.gdn_kv4_attention(q, r["cache"], torch.tensor(r["tables"], **I32), torch.tensor(r["kvlens"], **I32), o,
+                          gdn.kv4_attention_workspace(2, T, 4, 2, D), cu_seqlens=torch.tensor(r["cu"], **I32), max_q=T, lse=lse,
+                          scale=r["scale"] * 2.0 ** -exponent, err_word=err)
+    assert torch.equal(o, base[0]) and torch.equal(lse, base[1]) and int(err) == 0
