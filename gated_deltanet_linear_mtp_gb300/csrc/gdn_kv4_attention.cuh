@@ -216,6 +216,7 @@ __device__ __forceinline__ void produce(const Kv4AttentionParams& p, const CUten
                     fence_proxy_async_smem();
                 }
                 const uint32_t n = __popc(__ballot_sync(~0u, ok));
+                __syncwarp();  // the lanes' zeros come before the arrival that tells of them (a vote orders no memory)
                 if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)(KINDS * PR * (C::CB + C::SB)));
                 __syncwarp();
                 if (ok) {
