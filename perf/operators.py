@@ -182,7 +182,7 @@ def prepare(case, seed):
                   max_q=max(1, int(new.max())),
                   o=torch.zeros((N, HQ, D), dtype=torch.bfloat16, device="cuda"),
                   lse=torch.zeros((N, HQ), dtype=torch.float32, device="cuda"))
-        if st["max_q"] <= 16 and not case["padded"]:
+        if st["max_q"] <= 16 and st["even_q"]:
             st["cu_arg"] = None  # the same number of tokens for each lane
         else:
             st["cu_arg"] = st["cu"]
