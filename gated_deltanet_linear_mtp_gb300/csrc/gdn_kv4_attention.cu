@@ -6,15 +6,17 @@
 // The T tokens and the G = HQ / HK query heads of one key head are the rows of one product: row r is token r / G, head
 // r % G, so the cached keys and values are read once for all of them.  An item is (lane, row tile, key head).
 //
-// Bound: the cache's 9/16 byte a number from HBM, and close behind it the issue slots of the unpacking (two conversions'
-// worth of instructions a pair of numbers); with 32 rows the tensor cores' rate for mma.sync (600 TFLOP/s measured).  Measured
-// with the join, HBM's floor in brackets: one lane of 131071 tokens, HQ 32, HK 4, D 128, 28 us (11); 64 lanes of one token over
-// up to 8192, HQ 16, HK 2, D 256, 48 us (23), 3.3 TB/s; 128 lanes of 4 tokens over up to 16384, HQ 32, HK 4, D 128, 304 us
-// (93), 233 TFLOP/s.  More rows go to gdn_kv4_attention_wide.cu.
+// Floor: the cache's 9/16 byte a number from HBM.  Measured with the join (graph replays, HBM's floor in brackets): one lane of 131071
+// tokens, HQ 32, HK 4, D 128, 28 us (11); 64 lanes of one token over up to 8192, HQ 16, HK 2, D 256, 48 us (23), 3.3 TB/s; 128 lanes
+// of 4 tokens over up to 16384, HQ 32, HK 4, D 128, 307 us (94), 230 TFLOP/s; the same with HQ 16, HK 2, D 256, whose 32 rows are
+// two items that each read the cache, 319 us (94).  What lies above: nothing is full (128 lanes of 4: issue slots 44 %, the tensor
+// pipe 39 %, DRAM 26 %).  Each of the two computing warps of a scheduler runs unpacking (two conversions' worth of instructions a
+// pair of numbers), S, softmax and P V one after the other, and O's registers leave no place for a third.  More rows go to
+// gdn_kv4_attention_wide.cu.
 // Nothing is dequantised into memory: one warp brings packed tiles of 128 or 256 tokens into shared memory by TMA (swizzled, a
 // pipeline of several), and each lane of the others unpacks the codes of its own MMA fragments (cvt e2m1x2 -> f16x2, one
-// multiply by the group's scale; both exact).  Issue: an eighth of a tile costs a warp about 760 instructions at 32 rows, D 128,
-// and registers leave two computing warps a scheduler (16 warps of half the rows each were not faster: 396 us against 371).  Keys and values are the M operand and the rows are N:
+// multiply by the group's scale; both exact).  Issue: an eighth of a tile costs a warp about 760 instructions at 32 rows, D 128
+// (16 warps of half the rows each were not faster: 396 us against 371 then).  Keys and values are the M operand and the rows are N:
 // N goes by 8, so a decode's 8 rows waste nothing.  The products' summation index may be permuted freely, which makes the
 // fragments contiguous in storage:
 //   * S^T = K Q^T: lane (g, c) of a warp (g = lane / 4, c = lane % 4) supplies tokens g and g + 8 of a tile of 16; k step s
@@ -44,9 +46,17 @@ namespace {
 // NR: groups of 8 rows of an item; W: warps that compute (one of four more copies, and those four give their registers to
 // the others: LREG a thread at launch, then CREG and PREG); WT: tokens of a warp's step; TILE: tokens of a tile; STAGES: tiles
 // in the pipeline; CTAS: of an SM; SWITCH: tiles that an item's begin and end (queries in, the warps' parts joined) count as in
-// the split of the work, so that CTAs with many short items are done with the others: 128 lanes of 4 tokens over up to 16384
-// keys, HQ 32, HK 4, D 128, 361 us with none, 304 with 6, 309 with 8; 64 lanes of one token, HQ 16, HK 2, D 256, 54, 48 (3), 49
-// (4); D 64 of one row group is best with none (92 us against 97 with 1)
+// the split of the work, so that CTAs with many short items are done with the others.  Readings in us with 0, 1, 2, 3, 4, 5, 6, 8
+// (* the one taken), ragged contexts up to the given one, HQ 32 and HK 4, at D 256 16 and 2:
+//   D 64,  8 rows,  64 lanes, 8192:   39* 36 37 38 39 41 41 43 (of another batch of lanes 92* 97 with 0 and 1)
+//   D 64,  16 rows, 128 lanes, 8192:  86 76* 72 72 72 74 76 78
+//   D 64,  32 rows, 128 lanes, 16384: 259 254 248 244* 235 230 222 215;  64 lanes, 4096: 62 60 58 55* 51 49 47 49
+//   D 128, 8 rows,  64 lanes, 8192:   53 48 49* 49 51 54 53 57
+//   D 128, 16 rows, 128 lanes, 8192:  135 119 111 109* 111 112 115 117
+//   D 128, 32 rows, 128 lanes, 16384: 361 354 345 337 323 314 306* 312
+//   D 256, 8 rows,  64 lanes, 8192:   54 51 49 47* 49 49 50 52
+//   D 256, 16 rows, 128 lanes, 8192:  121 111 106 103 99 100* 102 103;  32 rows, 16384: 361 347 338 328 318 319* 321 328
+// At D 64 a larger one reads better with 32 rows (12 %) and with 16 (6 %).
 template <int D_, int NR_, int WT_, int TILE_, int STAGES_, int CTAS_, int SWITCH_>
 struct Cfg {
     static constexpr int D = D_, NR = NR_, W = 8, WT = WT_, TILE = TILE_, STAGES = STAGES_, CTAS = CTAS_;
@@ -614,8 +624,8 @@ cudaError_t run(const Kv4AttentionParams& p, cudaStream_t s) {
 }
 
 // More rows than this go to the tcgen05 kernel, although 128 is what it wants: 256 lanes of 64 rows over 2100 keys, D 64, took
-// 255 us there and 352 us here (160 us there now); 128 lanes of 32 rows over 8500 keys, D 128, 417 us there and 361 us here
-// (304 us here now), and of 20 rows 413 and 349 us.
+// 255 us there and 352 us here (160 us there now).  17 to 32 rows stay here; there and here, 128 lanes over up to 16384 keys: 32 rows of
+// D 64 254 and 244 us, of D 128 391 and 307, of D 256 396 and 319; 20 rows of D 64 246 and 225, of D 256 382 and 307.
 bool wide(int64_t rows) { return rows > 32; }
 
 // Rows of an item: 8, 16 or 32; of D 256 at most 16 (O^T takes D * rows / 32 registers a thread), more take several items

@@ -12,9 +12,11 @@
 // (about 600 cycles each way), and with one buffer of 128 keys the tensor cores waited for it (665 us for two chunks of 2048
 // tokens behind 8192 keys, HQ 32, HK 4, D 128, against 573 then).  An item of up to 128 rows is worked on by both halves of the
 // CTA, each with half of every tile's keys (256 lanes of 64 rows over up to 4096 keys, D 64: 229 us against 255 then).
-// Measured: those two chunks 530 us, 1.17 PFLOP/s; 16 ragged prompts of up to 2048 tokens, HQ 16, HK 2, D 128, 135 us, 0.54
-// PFLOP/s; the 256 lanes 160 us, 0.98 TB/s.  What is left above the products: the waits of the issuing threads and the
-// softmax's way (2000 cycles a unit of 64 keys where the products take 1280), and an item's begin and end.
+// Measured (graph replays): those two chunks 531 us, 1.17 PFLOP/s; 16 ragged prompts of up to 2048 tokens, HQ 16, HK 2, D 128, 136 us,
+// 0.54 PFLOP/s; the 256 lanes 160 us, 0.98 TB/s.  At other head dimensions: the two chunks at D 64 488 us, and with HQ 16, HK 2, D 256
+// 873 us; the ragged prompts at D 64 113 us, at D 256 333 us.  What is left above the products is waiting: a unit of 64 keys takes 2000
+// cycles where its products take 1280 (128 rows each), since a warp's softmax is one chain of loads, maxima, exponentials and stores
+// with two warps a scheduler to cover it; and an item's begin and end.
 // The reference m of P = 2^(s - m) moves only where a score passes the running maximum by more than 8 (in units of log 2; then
 // that thread scales its row of O in tensor memory), so O stays in tensor memory throughout.
 // Queries, P and statistics are held as in the decode kernel: f16 by a power of two a row, f16 lifted by kLift, fp32.
@@ -33,8 +35,8 @@ namespace {
 constexpr int kThreads = 512;  // 4 warpgroups: softmax, softmax or unpacking, unpacking, MMA and copies
 constexpr int kMmaWarp = 12, kLoadWarp = 14;  // kMmaWarp + m issues the products of rows 128 m ..; two warps copy
 // Tiles that the begin and the end of an item count as in the split of the work (a piece of n tiles takes about 4.2 n + 10.7
-// thousand cycles at D 128): 16 ragged prompts of up to 2048 tokens, HQ 16, HK 2, D 128, took 217 us without, 171, 145, 135 and
-// 136 us with 1, 2, 3 and 4.
+// thousand cycles at D 128).  16 ragged prompts of up to 2048 tokens, HQ 16, HK 2, in us with 0 to 5: D 128 220, 171, 146, 135, 135,
+// 139; D 64 162, 127, 109, 114, 115, 119; D 256 489, 412, 380, 333, 314, 322.  Chunks of 2048 behind 8192 keys differ by 2 % at most.
 constexpr int kSwitch = 3;
 constexpr int kLaunchRegs = 128, kSoftRegs = 160, kUnpackRegs = 112, kRestRegs = 80;
 static_assert(2 * kSoftRegs + kUnpackRegs + kRestRegs <= 4 * kLaunchRegs, "the block's registers");

@@ -6,8 +6,10 @@
 //     (i, i + R / 2) or (2 i, 2 i + 1) of the first R dimensions
 //
 // Each head row is read and written once; at 8192 tokens, HQ 32, HK 8, D 128, bf16, that is 25 us of HBM, and 50 us (3.4 TB/s)
-// were measured: issue slots bound it (about 187 warp instructions for two rows of 128), so the layout keeps instructions few.
-// With the store 16381 tokens of that shape take 150 us (65 us of HBM) and their read-back 22 us.
+// were measured; in fp32 68 us (50).  Neither the issue slots (60 %) nor DRAM (31 %) are full: after a group's first token each row is
+// loaded where it is used, and four CTAs of 64 registers cover part of that.  Few instructions (about 187 a warp for two rows of
+// 128) still pay, since they leave more of the time to the loads.  With the store 16381 tokens of that shape take 152 us (66 us of
+// HBM with their read-back, which takes 22 us); in fp32 210 us.
 // A row belongs to D / 8 lanes of one warp, and a lane holds both numbers of its four pairs (two chunks of 4 dimensions,
 // half the rotated part apart), so a rotation exchanges nothing and only the sum of squares is shuffled; the arithmetic is
 // two fp32 numbers an instruction.  The angles are those of a token, not of a head: a CTA takes several tokens, forms
