@@ -166,7 +166,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // cuTensorMapEncodeTiled from the driver, looked up once (no link-time dependency on libcuda)
-inline EncodeTiledFn encode_tiled_fn() {
+inline EncodeTiledFn driver_encode_tiled() {
     static const EncodeTiledFn fn = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -178,5 +178,20 @@ inline EncodeTiledFn encode_tiled_fn() {
     }();
     return fn;
 }
+
+// The encoder wants a current context, which a thread has from its first launch or allocation on; in a thread without one the
+// runtime's is made current (cudaSetDevice with the device that is the thread's anyway) and the encoder called again
+inline CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* base, const cuuint64_t* dims,
+                             const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* steps, CUtensorMapInterleave il,
+                             CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2, CUtensorMapFloatOOBfill fill) {
+    const EncodeTiledFn fn = driver_encode_tiled();
+    const CUresult r = fn(map, type, rank, base, dims, strides, box, steps, il, swizzle, l2, fill);
+    int dev = 0;
+    if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+    return fn(map, type, rank, base, dims, strides, box, steps, il, swizzle, l2, fill);
+}
+
+// encode_tiled; nullptr where the driver has no such encoder
+inline EncodeTiledFn encode_tiled_fn() { return driver_encode_tiled() != nullptr ? encode_tiled : nullptr; }
 
 }  // namespace gdn
