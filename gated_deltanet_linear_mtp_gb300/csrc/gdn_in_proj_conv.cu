@@ -522,13 +522,17 @@ IpTiling cached_tiling(int B, int T, int H, int64_t C) {
     return g;
 }
 
+// Dynamic shared memory opened for every shape: all beside the kernel's 1 KiB.  Not each call's own size, since the limit belongs to all
+// host threads, and another's smaller call would lower it between this one's setting and launch.
+constexpr int kIpOpenSmem = 226 * 1024;
+
 template <int K>
 cudaError_t launch_in_proj_k(const InProjConvParams& p, const CUtensorMap& wmap, cudaStream_t s) {
     auto kernel = gdn_in_proj_conv_kernel<K>;
     // the ring of this shape (the split does not change it), opened before the occupancy queries see the kernel
     const IpTiling b = base_tiling(p.B, p.T, p.H, K);
     const uint32_t smem = ip_smem_bytes(b.N, b.stages, b.pf_lanes, K);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kIpOpenSmem);
     if (e != cudaSuccess) return e;
     const IpTiling g = cached_tiling<K>(p.B, p.T, p.H, p.C);
     if (!ring_holds(g, p.T)) return cudaErrorInvalidConfiguration;  // ks = 1 always fits: lanes x T <= N

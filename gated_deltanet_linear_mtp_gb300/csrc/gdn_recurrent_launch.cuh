@@ -121,12 +121,14 @@ int resident_ctas_per_sm(Kernel kernel, int threads, size_t smem) {
 // decode and T = 4 verify): each CTA keeps its SM slot through the epilogue, waiting on the slowest CTA of its
 // cluster, while the next CTA's state load could use it; inside one wave the fused launch saved 2-3 us of the
 // norm's own launch.
+// Shared memory beyond the default is opened as far as it goes (the kernels have no static shared memory), not for this call's
+// T alone: the limit belongs to all host threads, and a call of another with fewer tokens would lower it before the launch.
 template <typename KPlain, typename KNorm>
 cudaError_t launch_rank1(KPlain plain, KNorm fused, dim3 grid, int threads, size_t smem, size_t smem_norm,
                          const RecurrentParams& p, int B, cudaStream_t s) {
     if (p.nz != nullptr && grid.x <= (unsigned)kNormMaxCluster) {
         if (smem_norm > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(fused, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_norm);
+            const cudaError_t e = cudaFuncSetAttribute(fused, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkMaxSmem);
             if (e != cudaSuccess) return e;
         }
         const int64_t ctas = (int64_t)grid.x * grid.y * grid.z;
@@ -136,7 +138,7 @@ cudaError_t launch_rank1(KPlain plain, KNorm fused, dim3 grid, int threads, size
     RecurrentParams q = p;
     q.nz = nullptr;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(plain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(plain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkMaxSmem);
         if (e != cudaSuccess) return e;
     }
     plain<<<grid, threads, smem, s>>>(q);

@@ -1,4 +1,5 @@
 """Calls from host threads other than the main one: as a thread's first CUDA call, which finds no context, and from two at once."""
+import ctypes
 import threading
 
 import numpy as np
@@ -71,3 +72,33 @@ def test_in_proj_conv_as_a_threads_first_call():
     a = InProj(8)
     in_thread(a.call)
     assert a.same()
+
+
+def test_in_proj_conv_of_two_row_counts_from_two_threads(monkeypatch):
+    """8 rows and 64, whose rings differ: a kernel's limit of shared memory belongs to all threads, so neither may lower it
+    between the other's setting and launch.  The binding marshals each call once; the threads repeat it."""
+    failed, start, streams = [], threading.Barrier(2), [torch.cuda.Stream() for _ in range(2)]
+    a, made = [InProj(8), InProj(64)], []
+    with monkeypatch.context() as m:
+        m.setattr(gdn, "_launch", lambda device, stream, fn, args, what: made.append((fn, args)))
+        for x in a:
+            x.call()
+    torch.cuda.synchronize()
+
+    def work(i):
+        fn, args = made[i]
+        s = ctypes.c_void_p(streams[i].cuda_stream)
+        start.wait()
+        for n in range(20000):
+            status = fn(*args, s)
+            if status != 0:
+                failed.append((i, n, status, gdn.lib().gdn_last_cuda_error()))
+                break
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and all(x.same() for x in a), failed
