@@ -30,6 +30,20 @@ and, for the softmax-attention layers between the recurrent ones, over a paged 4
                       scale=None, err_word=None)
     kv4_attention_workspace(B, max_q, HQ, HK, D, device=None)
 
+for linear-attention layers with a fixed decay for each head, on the same state pools:
+
+    gdn_linear_decode(q, k, v, log_decay, state_pool, state_indices, o, err_word=None, *, out_indices=None, scale=1.0)
+    gdn_linear_verify(q, k, v, log_decay, state_pool, state_indices, o, intermediate_states=None, err_word=None, *, scale=1.0)
+    gdn_linear_commit(k, v, log_decay, state_pool, state_indices, accept_len, err_word=None, *, out_indices=None)
+    gdn_linear_prefill(q, k, v, log_decay, state_pool, state_indices, cu_seqlens, o, workspace, has_initial_state=None,
+                       err_word=None, *, out_indices=None, scale=1.0)
+    linear_prefill_workspace(N, B, HV, DK, DV, device=None)
+
+and for the sampling that ends a step:
+
+    gdn_token_probs(logits, temperature, probs, err_word=None)
+    gdn_draft_accept(target_probs, draft_tokens, uniform, state_indices, accept_len, tokens, draft_probs=None, err_word=None)
+
 Shapes and semantics are those of ``include/gdn.h``: q, k ``[B,T,HK,DK]``; v, o ``[B,T,HV,DV]``; a, b
 ``[B,T,HV]``; A_log, dt_bias ``[HV]`` fp32; state_pool ``[num_slots,HV,DV,DK]``; state_indices, accept_len
 ``[B]`` int32; intermediate_states ``[B,T,HV,DV,DK]``; err_word a 1-element int32 device tensor.  Prefill takes
@@ -51,7 +65,8 @@ __all__ = ["gdn_decode", "gdn_decode_gated", "gdn_mtp_verify", "gdn_commit", "gd
            "gdn_prefill", "gdn_gated_rmsnorm", "gdn_in_proj_conv", "gdn_conv_commit", "InProjOut", "GdnError", "GdnDims", "lib", "STATUS", "ERRBIT_INDEX", "ERRBIT_ACCEPT_LEN", "ERRBIT_TIMEOUT",
            "ERRBIT_SEQLEN", "ERRBIT_PAGES", "ERRBIT_NONFINITE", "MAX_T", "EXPORTS",
            "gdn_page_plan", "gdn_qk_norm_rope", "gdn_kv4_read", "gdn_kv4_attention", "kv4_attention_workspace", "Kv4Cache",
-           "PagePlan"]
+           "PagePlan", "gdn_linear_decode", "gdn_linear_verify", "gdn_linear_commit", "gdn_linear_prefill",
+           "linear_prefill_workspace", "gdn_token_probs", "gdn_draft_accept"]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_DTYPE", 4: "GDN_ERR_ALIGN",
           5: "GDN_ERR_UNSUPPORTED", 6: "GDN_ERR_CUDA", 7: "GDN_ERR_VALUE"}
@@ -66,7 +81,9 @@ F32, BF16 = 0, 1
 EXPORTS = ("gdn_decode", "gdn_decode_gated", "gdn_mtp_verify", "gdn_commit", "gdn_commit_replay",
            "gdn_mtp_verify_commit", "gdn_mtp_verify_gated", "gdn_prefill",
            "gdn_gated_rmsnorm", "gdn_in_proj_conv", "gdn_conv_commit", "gdn_page_plan", "gdn_qk_norm_rope",
-           "gdn_kv4_read", "gdn_kv4_attention", "gdn_kv4_attention_workspace", "gdn_status_string",
+           "gdn_kv4_read", "gdn_kv4_attention", "gdn_kv4_attention_workspace", "gdn_linear_decode", "gdn_linear_verify",
+           "gdn_linear_commit", "gdn_linear_prefill", "gdn_linear_prefill_workspace", "gdn_token_probs", "gdn_draft_accept",
+           "gdn_status_string",
            "gdn_last_cuda_error", "gdn_abi_version")
 
 
@@ -185,6 +202,16 @@ class _Kv4AttentionDimsC(ctypes.Structure):
                 ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class _TokenDimsC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("logits_stride", ctypes.c_int64), ("probs_stride", ctypes.c_int64)]
+
+
+class _AcceptDimsC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("V", ctypes.c_int32), ("target_stride", ctypes.c_int64),
+                ("draft_stride", ctypes.c_int64)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -230,6 +257,17 @@ def lib() -> ctypes.CDLL:
         L.gdn_kv4_attention_workspace.restype = ctypes.c_int64
         for f in (L.gdn_in_proj_conv, L.gdn_conv_commit, L.gdn_page_plan, L.gdn_qk_norm_rope, L.gdn_kv4_read,
                   L.gdn_kv4_attention):
+            f.restype = ctypes.c_int
+        L.gdn_linear_decode.argtypes = [vp] * 11
+        L.gdn_linear_verify.argtypes = [vp] * 10 + [vp]
+        L.gdn_linear_commit.argtypes = [vp] * 10
+        L.gdn_linear_prefill.argtypes = [vp] * 12 + [ctypes.c_int64, vp, vp]
+        L.gdn_linear_prefill_workspace.argtypes = [i32] * 5
+        L.gdn_linear_prefill_workspace.restype = ctypes.c_int64
+        L.gdn_token_probs.argtypes = [vp] * 6
+        L.gdn_draft_accept.argtypes = [vp] * 10
+        for f in (L.gdn_linear_decode, L.gdn_linear_verify, L.gdn_linear_commit, L.gdn_linear_prefill, L.gdn_token_probs,
+                  L.gdn_draft_accept):
             f.restype = ctypes.c_int
         for f in (L.gdn_decode, L.gdn_decode_gated, L.gdn_mtp_verify, L.gdn_commit, L.gdn_commit_replay, L.gdn_mtp_verify_commit,
                   L.gdn_mtp_verify_gated, L.gdn_prefill, L.gdn_gated_rmsnorm):
@@ -860,3 +898,170 @@ def gdn_kv4_attention(q, cache, block_tables, kv_lens, o, workspace, *, cu_seqle
           _ptr(lse, "lse", torch.float32, (N, HQ), dev),
           _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel(),
           _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_kv4_attention")
+
+
+# ---- linear attention with a fixed decay for each head ----------------------------------------------
+def _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, lead, scale):
+    """GPU, gdn_dims and pointers of k, v, log_decay, state_pool and the slots of a linear-attention call whose tokens have
+    the leading shape `lead` ([B, T], or [N] packed)."""
+    import torch
+
+    dev = _gpu(k, "k")
+    if k.dim() != len(lead) + 2 or v.dim() != len(lead) + 2 or state_pool.dim() != 4:
+        raise ValueError("q, k, v and o are [B,T,heads,dim] (prefill: [N,heads,dim]), state_pool is [num_slots,HV,DV,DK]")
+    HK, DK = k.shape[-2:]
+    num_slots, HV, DV, _ = state_pool.shape
+    B, f32, i32, code = state_indices.shape[0], torch.float32, torch.int32, _code(k, "k")
+    sd = _code(state_pool, "state_pool")
+    d = GdnDims(B, lead[-1], HK, HV, DK, DV, num_slots, code, sd, code, float(scale), 0.0)
+    ptrs = dict(k=_ptr(k, "k", k.dtype, (*lead, HK, DK), dev), v=_ptr(v, "v", k.dtype, (*lead, HV, DV), dev),
+                log_decay=_ptr(log_decay, "log_decay", f32, (HV,), dev),
+                pool=_ptr(state_pool, "state_pool", state_pool.dtype, (num_slots, HV, DV, DK), dev),
+                idx=_ptr(state_indices, "state_indices", i32, (B,), dev),
+                out=_ptr(out_indices, "out_indices", i32, (B,), dev))
+    return dev, d, ptrs
+
+
+def _linear_io(q, k, o, d, dev):
+    """Pointers of q (k's type and shape) and o (fp32 or bf16, [.., HV, DV]); o's type goes into the dims."""
+    d.out_dtype = _code(o, "o")
+    return (_ptr(q, "q", k.dtype, k.shape, dev), _ptr(o, "o", o.dtype, (*k.shape[:-2], d.HV, d.DV), dev))
+
+
+def _lanes(k, state_indices):
+    if k.dim() != 4 or state_indices.dim() != 1 or k.shape[0] != state_indices.shape[0]:
+        raise ValueError("q, k, v and o are [B,T,heads,dim], state_indices [B]")
+    return tuple(k.shape[:2])
+
+
+def gdn_linear_decode(q, k, v, log_decay, state_pool, state_indices, o, err_word=None, *, out_indices=None, scale=1.0,
+                      stream=None) -> None:
+    """T tokens (normally 1) of ``S = exp(log_decay) S + v k^T``, ``o = scale S q`` from ``state_pool[state_indices[b]]``; the
+    final state goes into slot ``out_indices[b]`` (the same slot if not given; -1 writes none)."""
+    import torch
+
+    L = lib()
+    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, _lanes(k, state_indices), scale)
+    qp, op = _linear_io(q, k, o, d, dev)
+    _run(dev, stream, L.gdn_linear_decode,
+         (ctypes.byref(d), qp, a["k"], a["v"], a["log_decay"], a["pool"], a["idx"], a["out"], op,
+          _ptr(err_word, "err_word", torch.int32, (1,), dev)), "gdn_linear_decode")
+
+
+def gdn_linear_verify(q, k, v, log_decay, state_pool, state_indices, o, intermediate_states=None, err_word=None, *, scale=1.0,
+                      stream=None) -> None:
+    """The same for T draft tokens from states that are only read; ``intermediate_states`` ``[B,T,HV,DV,DK]`` (state_pool's
+    type) receives the state after every token, for ``gdn_commit``."""
+    import torch
+
+    L = lib()
+    lead = _lanes(k, state_indices)
+    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, None, lead, scale)
+    qp, op = _linear_io(q, k, o, d, dev)
+    _run(dev, stream, L.gdn_linear_verify,
+         (ctypes.byref(d), qp, a["k"], a["v"], a["log_decay"], a["pool"], a["idx"], op,
+          _ptr(intermediate_states, "intermediate_states", state_pool.dtype, (*lead, d.HV, d.DV, d.DK), dev),
+          _ptr(err_word, "err_word", torch.int32, (1,), dev)), "gdn_linear_verify")
+
+
+def gdn_linear_commit(k, v, log_decay, state_pool, state_indices, accept_len, err_word=None, *, out_indices=None,
+                      stream=None) -> None:
+    """The state after the first ``accept_len[b]`` of a verify's tokens, into the lane's slot (or ``out_indices[b]``)."""
+    import torch
+
+    L = lib()
+    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, _lanes(k, state_indices), 1.0)
+    _run(dev, stream, L.gdn_linear_commit,
+         (ctypes.byref(d), a["k"], a["v"], a["log_decay"], a["pool"], a["idx"], a["out"],
+          _ptr(accept_len, "accept_len", torch.int32, (d.B,), dev), _ptr(err_word, "err_word", torch.int32, (1,), dev)),
+         "gdn_linear_commit")
+
+
+def linear_prefill_workspace(N, B, HV, DK, DV, device=None):
+    """A workspace for ``gdn_linear_prefill`` calls of these sizes (one call at a time)."""
+    import torch
+
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        n = lib().gdn_linear_prefill_workspace(B, N, HV, DK, DV)
+    if n < 0:
+        raise ValueError(f"linear_prefill_workspace: sizes out of range (N {N}, B {B}, HV {HV}, DK {DK}, DV {DV})")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def gdn_linear_prefill(q, k, v, log_decay, state_pool, state_indices, cu_seqlens, o, workspace, has_initial_state=None,
+                       err_word=None, *, out_indices=None, scale=1.0, stream=None) -> None:
+    """Packed prompts (q, k ``[N,HK,DK]``; v, o ``[N,HV,DV]``; prompt b is tokens ``cu_seqlens[b] .. cu_seqlens[b+1]-1``) from
+    ``state_pool[state_indices[b]]``, or from zero where ``has_initial_state[b]`` is 0; o at their tokens, the final state into
+    slot ``out_indices[b]`` (the same slot if not given)."""
+    import torch
+
+    L = lib()
+    if k.dim() != 3 or state_indices.dim() != 1:
+        raise ValueError("q, k [N,HK,DK], v, o [N,HV,DV], state_indices [B]")
+    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, (k.shape[0],), scale)
+    qp, op = _linear_io(q, k, o, d, dev)
+    i32 = torch.int32
+    _run(dev, stream, L.gdn_linear_prefill,
+         (ctypes.byref(d), _ptr(cu_seqlens, "cu_seqlens", i32, (d.B + 1,), dev), qp, a["k"], a["v"], a["log_decay"], a["pool"],
+          a["idx"], a["out"], _ptr(has_initial_state, "has_initial_state", i32, (d.B,), dev), op,
+          _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel(),
+          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_linear_prefill")
+
+
+# ---- the sampling that ends a speculative step ---------------------------------------------------------
+def _prob_rows(t, name: str, dtype, shape, dev: int):
+    """Address and row stride of a tensor ``[B, T, V]`` whose rows are contiguous and evenly spaced over (B, T)."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}, as the other tensors of the call are: it is on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    B, T, V = shape
+    lane, row, one = t.stride()
+    step = row if T > 1 else lane if B > 1 else V
+    if (one != 1 and V > 1) or (B > 1 and T > 1 and lane != T * row) or step < V:
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced (strides {t.stride()})")
+    return t.data_ptr(), step
+
+
+def gdn_token_probs(logits, temperature, probs, err_word=None, *, stream=None) -> None:
+    """``probs`` ``[B,T,V]`` fp32: the softmax of ``logits`` ``[B,T,V]`` (fp32 or bf16) divided by ``temperature`` ``[B]`` fp32
+    (0: 1 at the first of the largest logits).  Rows may have room between them (``x[..., :V]``)."""
+    import torch
+
+    L = lib()
+    dev = _gpu(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits and probs are [B,T,V]")
+    code, shape = _code(logits, "logits"), logits.shape
+    lp, ls = _prob_rows(logits, "logits", logits.dtype, shape, dev)
+    pp, ps = _prob_rows(probs, "probs", torch.float32, shape, dev)
+    d = _TokenDimsC(*shape, code, ls, ps)
+    _run(dev, stream, L.gdn_token_probs,
+         (ctypes.byref(d), lp, _ptr(temperature, "temperature", torch.float32, (shape[0],), dev), pp,
+          _ptr(err_word, "err_word", torch.int32, (1,), dev)), "gdn_token_probs")
+
+
+def gdn_draft_accept(target_probs, draft_tokens, uniform, state_indices, accept_len, tokens, draft_probs=None, err_word=None, *,
+                     stream=None) -> None:
+    """Drafts ``draft_tokens`` ``[B,T-1]`` accepted against ``target_probs`` ``[B,T,V]`` with the numbers ``uniform`` ``[B,T]``
+    in [0, 1) and the probabilities ``draft_probs`` ``[B,T-1,V]`` they were drawn from (None: drafted for certain).  ``accept_len``
+    ``[B]`` gets 1 + the accepted drafts, ``tokens`` ``[B,T]`` those drafts, the token drawn after them, then -1.  Lanes
+    whose ``state_indices`` is -1 are skipped (None: no lane is)."""
+    import torch
+
+    L = lib()
+    dev = _gpu(target_probs, "target_probs")
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs is [B,T,V]")
+    (B, T, V), f32, i32 = target_probs.shape, torch.float32, torch.int32
+    tp, ts = _prob_rows(target_probs, "target_probs", f32, (B, T, V), dev)
+    dp, ds = (None, V) if draft_probs is None else _prob_rows(draft_probs, "draft_probs", f32, (B, T - 1, V), dev)
+    d = _AcceptDimsC(B, T, V, ts, ds)
+    _run(dev, stream, L.gdn_draft_accept,
+         (ctypes.byref(d), tp, _ptr(draft_tokens, "draft_tokens", i32, (B, T - 1), dev), dp,
+          _ptr(uniform, "uniform", f32, (B, T), dev), _ptr(state_indices, "state_indices", i32, (B,), dev),
+          _ptr(accept_len, "accept_len", i32, (B,), dev), _ptr(tokens, "tokens", i32, (B, T), dev),
+          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_draft_accept")

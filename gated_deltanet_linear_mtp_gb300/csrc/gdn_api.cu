@@ -256,6 +256,61 @@ gdn_status verify_commit(const gdn_dims* dims, const gdn_replay_tokens* prev, co
                                 err_word, stream);
 }
 
+// The sizes of the linear-attention calls: those of check_dims, without the epsilon, which they do not read.
+gdn_status check_linear(const gdn_dims* d, bool prefill) {
+    if (d == nullptr) return GDN_ERR_NULL;
+    gdn_dims e = *d;
+    e.l2_eps = 0.f;
+    return check_dims(&e, true, prefill);
+}
+
+gdn_status linear_call(const gdn_dims* d, const void* q, const void* k, const void* v, const float* log_decay, void* pool,
+                       const int32_t* idx, const int32_t* out_idx, const int32_t* steps, const int32_t* cu_seqlens,
+                       const int32_t* has_init, void* o, void* cache, bool write, bool outputs, int32_t* err,
+                       LinearParams* out) {
+    if ((outputs && (!q || !o)) || !k || !v || !log_decay || !pool || !idx) return GDN_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(pool, 16) || !aligned(cache, 16)) return GDN_ERR_ALIGN;
+    if (!aligned(v, dtype_bytes(d->qkv_dtype)) || !aligned(o, dtype_bytes(d->out_dtype))) return GDN_ERR_ALIGN;
+    for (const void* x : {(const void*)log_decay, (const void*)idx, (const void*)out_idx, (const void*)steps,
+                          (const void*)cu_seqlens, (const void*)has_init, (const void*)err})
+        if (!aligned(x, 4)) return GDN_ERR_ALIGN;
+    LinearParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.log_decay = log_decay;
+    p.pool = pool;
+    p.indices = idx;
+    p.out_indices = out_idx;
+    p.write = write;
+    p.steps = steps;
+    p.cu_seqlens = cu_seqlens;
+    p.has_init = has_init;
+    p.o = o;
+    p.cache = cache;
+    p.err = err;
+    p.B = d->B;
+    p.T = d->T;
+    p.N = d->T;
+    p.HK = d->HK;
+    p.HV = d->HV;
+    p.DK = d->DK;
+    p.DV = d->DV;
+    p.num_slots = d->num_slots;
+    p.out_bf16 = d->out_dtype == GDN_BF16;
+    p.v_vec = aligned(v, 16) && ((int64_t)d->DV * (int64_t)dtype_bytes(d->qkv_dtype)) % 16 == 0;
+    p.scale = d->scale;
+    *out = p;
+    return GDN_OK;
+}
+
+gdn_status run_linear(const gdn_dims* d, const LinearParams& p, gdn_stream_t stream) {
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool qkv_bf16 = d->qkv_dtype == GDN_BF16;
+    return finish(d->state_dtype == GDN_F32 ? launch_linear_f32state(p, qkv_bf16, st)
+                                            : launch_linear_bf16state(p, qkv_bf16, st));
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -648,6 +703,98 @@ gdn_status gdn_kv4_attention(const gdn_kv4_attention_dims* dims, const gdn_kv4_c
     p.scale = dims->scale;
     p.err = err_word;
     return finish(launch_kv4_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_linear_decode(const gdn_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                             void* state_pool, const int32_t* state_indices, const int32_t* out_indices, void* o,
+                             int32_t* err_word, gdn_stream_t stream) {
+    gdn_status s = check_linear(dims, false);
+    if (s != GDN_OK || dims->B == 0) return s;
+    LinearParams p;
+    s = linear_call(dims, q, k, v, log_decay, state_pool, state_indices, out_indices, nullptr, nullptr, nullptr, o, nullptr,
+                    true, true, err_word, &p);
+    return s != GDN_OK ? s : run_linear(dims, p, stream);
+}
+
+gdn_status gdn_linear_verify(const gdn_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                             const void* state_pool, const int32_t* state_indices, void* o, void* intermediate_states,
+                             int32_t* err_word, gdn_stream_t stream) {
+    gdn_status s = check_linear(dims, false);
+    if (s != GDN_OK || dims->B == 0) return s;
+    LinearParams p;
+    s = linear_call(dims, q, k, v, log_decay, const_cast<void*>(state_pool), state_indices, nullptr, nullptr, nullptr, nullptr,
+                    o, intermediate_states, false, true, err_word, &p);
+    return s != GDN_OK ? s : run_linear(dims, p, stream);
+}
+
+gdn_status gdn_linear_commit(const gdn_dims* dims, const void* k, const void* v, const float* log_decay, void* state_pool,
+                             const int32_t* state_indices, const int32_t* out_indices, const int32_t* accept_len,
+                             int32_t* err_word, gdn_stream_t stream) {
+    gdn_status s = check_linear(dims, false);
+    if (s != GDN_OK || dims->B == 0) return s;
+    if (!accept_len) return GDN_ERR_NULL;
+    LinearParams p;
+    s = linear_call(dims, nullptr, k, v, log_decay, state_pool, state_indices, out_indices, accept_len, nullptr, nullptr,
+                    nullptr, nullptr, true, false, err_word, &p);
+    return s != GDN_OK ? s : run_linear(dims, p, stream);
+}
+
+int64_t gdn_linear_prefill_workspace(int32_t B, int32_t N, int32_t HV, int32_t DK, int32_t DV) {
+    if (B < 0 || B > 65535 || N < 0 || HV < 1 || HV > 65535 || DV < 1 || !supported_dk(DK)) return -1;
+    return linear_prefill_workspace(B, N, HV, DK, DV);
+}
+
+gdn_status gdn_linear_prefill(const gdn_dims* dims, const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
+                              const float* log_decay, void* state_pool, const int32_t* state_indices,
+                              const int32_t* out_indices, const int32_t* has_initial_state, void* o, void* workspace,
+                              int64_t workspace_bytes, int32_t* err_word, gdn_stream_t stream) {
+    gdn_status s = check_linear(dims, true);
+    if (s != GDN_OK || dims->B == 0 || (dims->T == 0 && !out_indices)) return s;
+    if (!cu_seqlens) return GDN_ERR_NULL;
+    const int64_t need = linear_prefill_workspace(dims->B, dims->T, dims->HV, dims->DK, dims->DV);
+    if (need > 0 && !workspace) return GDN_ERR_NULL;
+    if (!aligned(workspace, 16)) return GDN_ERR_ALIGN;
+    if (workspace_bytes < need) return GDN_ERR_SHAPE;
+    if (dims->T == 0) q = o = nullptr, k = v = state_pool;  // no tokens, states to copy: nothing of these is read
+    LinearParams p;
+    s = linear_call(dims, q, k, v, log_decay, state_pool, state_indices, out_indices, nullptr, cu_seqlens, has_initial_state, o,
+                    nullptr, true, dims->T > 0, err_word, &p);
+    return s != GDN_OK ? s : run_linear(dims, p, stream);
+}
+
+gdn_status gdn_token_probs(const gdn_token_dims* dims, const void* logits, const float* temperature, float* probs,
+                           int32_t* err_word, gdn_stream_t stream) {
+    if (dims == nullptr) return GDN_ERR_NULL;
+    if (dims->B < 0 || dims->B > 65535 || dims->T < 1 || dims->V < 1 || dims->V > 1 << 30) return GDN_ERR_SHAPE;
+    if ((int64_t)dims->B * dims->T >= (int64_t)1 << 31) return GDN_ERR_SHAPE;
+    if (!valid_dtype(dims->dtype)) return GDN_ERR_DTYPE;
+    if (dims->logits_stride < dims->V || dims->probs_stride < dims->V) return GDN_ERR_SHAPE;
+    if (dims->logits_stride > (int64_t)1 << 31 || dims->probs_stride > (int64_t)1 << 31) return GDN_ERR_SHAPE;
+    if (dims->B == 0) return GDN_OK;
+    if (!logits || !temperature || !probs) return GDN_ERR_NULL;
+    if (!aligned(logits, dtype_bytes(dims->dtype)) || !aligned(temperature, 4) || !aligned(probs, 4) || !aligned(err_word, 4))
+        return GDN_ERR_ALIGN;
+    const TokenProbsParams p{dims->B, dims->T, dims->V, dims->dtype == GDN_BF16, logits, dims->logits_stride, temperature, probs,
+                             dims->probs_stride, err_word};
+    return finish(launch_token_probs(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_draft_accept(const gdn_accept_dims* dims, const float* target_probs, const int32_t* draft_tokens,
+                            const float* draft_probs, const float* uniform, const int32_t* state_indices,
+                            int32_t* accept_len, int32_t* tokens, int32_t* err_word, gdn_stream_t stream) {
+    if (dims == nullptr) return GDN_ERR_NULL;
+    if (dims->B < 0 || dims->B > 65535 || dims->T < 1 || dims->T > GDN_MAX_T || dims->V < 1 || dims->V > 1 << 30)
+        return GDN_ERR_SHAPE;
+    if (dims->target_stride < dims->V || dims->target_stride > (int64_t)1 << 31) return GDN_ERR_SHAPE;
+    if (draft_probs && (dims->draft_stride < dims->V || dims->draft_stride > (int64_t)1 << 31)) return GDN_ERR_SHAPE;
+    if (dims->B == 0) return GDN_OK;
+    if (!target_probs || !uniform || !accept_len || !tokens || (dims->T > 1 && !draft_tokens)) return GDN_ERR_NULL;
+    for (const void* x : {(const void*)target_probs, (const void*)draft_tokens, (const void*)draft_probs, (const void*)uniform,
+                          (const void*)state_indices, (const void*)accept_len, (const void*)tokens, (const void*)err_word})
+        if (!aligned(x, 4)) return GDN_ERR_ALIGN;
+    const DraftAcceptParams p{dims->B, dims->T, dims->V, target_probs, dims->target_stride, draft_probs, dims->draft_stride,
+                              draft_tokens, uniform, state_indices, accept_len, tokens, err_word};
+    return finish(launch_draft_accept(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char* gdn_status_string(gdn_status status) {

@@ -181,6 +181,60 @@ struct Kv4AttentionParams {
     int32_t* err;
 };
 
+// Linear attention with a decay for each head (gdn_linear.cu, gdn_linear_prefill.cu).
+struct LinearParams {
+    const void* q;            // nullptr: no outputs (commit)
+    const void* k;
+    const void* v;
+    const float* log_decay;   // [HV]
+    void* pool;
+    const int32_t* indices;
+    const int32_t* out_indices;  // slots of the final states; nullptr: indices
+    int write;                // the final states are written (0: verify)
+    const int32_t* steps;     // nullptr: T tokens per lane; else steps[b] in 0..T (commit)
+    const int32_t* cu_seqlens;   // prefill: packed tokens; else nullptr
+    const int32_t* has_init;  // prefill, nullable
+    void* o;
+    void* cache;              // nullptr: no intermediate states
+    int32_t* err;
+    int B, T, N, HK, HV, DK, DV, num_slots;  // N: packed tokens (prefill)
+    int out_bf16;
+    int v_vec;                // v starts on 16 bytes and DV * sizeof(v) % 16 == 0
+    float scale;
+};
+// bytes that launch_linear_prefill wants for prompts cut into pieces
+int64_t linear_prefill_workspace(int B, int N, int HV, int DK, int DV);
+cudaError_t launch_linear_f32state(const LinearParams& p, bool qkv_bf16, cudaStream_t s);
+cudaError_t launch_linear_bf16state(const LinearParams& p, bool qkv_bf16, cudaStream_t s);
+
+// Softmax of logits rows with a temperature a lane (gdn_token_probs.cu).
+struct TokenProbsParams {
+    int B, T, V, bf16;
+    const void* logits;
+    int64_t logits_stride;  // elements from one row to the next
+    const float* temperature;
+    float* probs;
+    int64_t probs_stride;
+    int32_t* err;
+};
+cudaError_t launch_token_probs(const TokenProbsParams& p, cudaStream_t s);
+
+// Acceptance of drafts and the token after them (gdn_draft_accept.cu).
+struct DraftAcceptParams {
+    int B, T, V;
+    const float* target;    // [B, T] rows of V
+    int64_t target_stride;
+    const float* draft;     // [B, T - 1] rows of V, nullable
+    int64_t draft_stride;
+    const int32_t* drafts;  // [B, T - 1]
+    const float* uniform;   // [B, T]
+    const int32_t* indices;  // [B], nullable: lanes of -1 are skipped
+    int32_t* accept_len;    // [B]
+    int32_t* tokens;        // [B, T]
+    int32_t* err;
+};
+cudaError_t launch_draft_accept(const DraftAcceptParams& p, cudaStream_t s);
+
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s);
 cudaError_t launch_qk_norm_rope(const QkNormRopeParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t s);

@@ -460,6 +460,96 @@ GDN_API gdn_status gdn_kv4_attention(const gdn_kv4_attention_dims* dims, const g
  * size is out of range. */
 GDN_API int64_t gdn_kv4_attention_workspace(int32_t B, int32_t max_q, int32_t HQ, int32_t HK, int32_t D);
 
+/*
+ * Linear attention with a fixed decay for each head, on the state pools, lanes and drafts of the calls above (a hybrid model runs
+ * such layers where it does not need the delta rule):
+ *     S = g S + v k^T,   o = scale S q,   g = exp(log_decay[h])          (S [DV, DK] in fp32, q and k as they are)
+ * log_decay [HV] fp32, at most 0 (-inf: no memory); HV / HK consecutive value heads share a query and key head.  dims, layouts,
+ * alignment, padded lanes, errors and bf16 rounding are those of gdn_decode, gdn_mtp_verify, gdn_commit_replay and gdn_prefill
+ * (l2_eps is not read).  out_indices [B], where a call takes it, names the slots that the final states go to, so that the
+ * state read stays as it is (a cached prefix); NULL: state_indices.  There -1 writes no state, and anything else outside the
+ * pool skips the lane (GDN_ERRBIT_INDEX).  Active lanes write distinct slots, and none that another lane reads.
+ *
+ * gdn_linear_decode -- T tokens (1 .. GDN_MAX_T) from state_pool[state_indices[b]]: o, and the final state.
+ */
+GDN_API gdn_status gdn_linear_decode(const gdn_dims* dims, const void* q, const void* k, const void* v,
+                                     const float* log_decay, void* state_pool, const int32_t* state_indices,
+                                     const int32_t* out_indices, void* o, int32_t* err_word, gdn_stream_t stream);
+
+/* gdn_linear_verify -- T draft tokens from states that are only read: o and, if intermediate_states [B, T, HV, DV, DK] is not
+ * NULL, the state after every token (which gdn_commit takes).  Lanes may share a slot. */
+GDN_API gdn_status gdn_linear_verify(const gdn_dims* dims, const void* q, const void* k, const void* v,
+                                     const float* log_decay, const void* state_pool, const int32_t* state_indices, void* o,
+                                     void* intermediate_states, int32_t* err_word, gdn_stream_t stream);
+
+/* gdn_linear_commit -- the first accept_len[b] of a verify's T tokens again, without outputs: the final state.  accept_len 0
+ * leaves the slot as it is (and copies the state where out_indices names another); outside 0 .. T the lane is skipped
+ * (GDN_ERRBIT_ACCEPT_LEN). */
+GDN_API gdn_status gdn_linear_commit(const gdn_dims* dims, const void* k, const void* v, const float* log_decay,
+                                     void* state_pool, const int32_t* state_indices, const int32_t* out_indices,
+                                     const int32_t* accept_len, int32_t* err_word, gdn_stream_t stream);
+
+/* gdn_linear_prefill -- packed prompts as in gdn_prefill (dims->T = N tokens in all): o at their tokens and the final states.
+ * A prompt of no tokens leaves its slot as it is (and copies its initial state where out_indices names another).  workspace: at
+ * least gdn_linear_prefill_workspace bytes on 16 bytes (may be NULL if that is 0), used by one call at a time; its contents
+ * need not be kept. */
+GDN_API gdn_status gdn_linear_prefill(const gdn_dims* dims, const int32_t* cu_seqlens, const void* q, const void* k,
+                                      const void* v, const float* log_decay, void* state_pool, const int32_t* state_indices,
+                                      const int32_t* out_indices, const int32_t* has_initial_state, void* o,
+                                      void* workspace, int64_t workspace_bytes, int32_t* err_word, gdn_stream_t stream);
+
+/* Workspace bytes of gdn_linear_prefill on the current device for calls of exactly these sizes; -1 if one is out of range. */
+GDN_API int64_t gdn_linear_prefill_workspace(int32_t B, int32_t N, int32_t HV, int32_t DK, int32_t DV);
+
+/*
+ * The sampling that ends a speculative step: the logits of its rows become probabilities (gdn_token_probs), drafts are accepted
+ * against them and one more token is drawn (gdn_draft_accept), and accept_len goes to the commits above.  T is the step's: the
+ * last token and T - 1 drafts; T = 1 is a decode step without drafts.
+ */
+typedef struct gdn_token_dims {
+    int32_t B;             /* lanes, 0 .. 65535 */
+    int32_t T;             /* rows per lane, >= 1; B * T < 2^31 */
+    int32_t V;             /* tokens of the vocabulary, 1 .. 2^30 */
+    int32_t dtype;         /* gdn_dtype of the logits */
+    int64_t logits_stride; /* elements from one row to the next, >= V */
+    int64_t probs_stride;  /* likewise */
+} gdn_token_dims;
+
+/*
+ * gdn_token_probs -- probs[b, t, v] = exp((x_v - max x) / temperature[b]) / sum_u exp((x_u - max x) / temperature[b]) of the
+ * row x = logits[b, t], in fp32.  A temperature of 0 (below the smallest normal number) puts 1 at the first of the largest
+ * logits and 0 elsewhere.  Logits of -inf (forbidden tokens) get 0, and a row of nothing else is all 0.  A row with NaN or +inf,
+ * or of a lane whose temperature is negative or not finite, is all 0 and sets GDN_ERRBIT_NONFINITE.  logits and probs on their
+ * element size; the two must not overlap; room between rows is neither read nor written.
+ */
+GDN_API gdn_status gdn_token_probs(const gdn_token_dims* dims, const void* logits, const float* temperature, float* probs,
+                                   int32_t* err_word, gdn_stream_t stream);
+
+typedef struct gdn_accept_dims {
+    int32_t B;             /* lanes, 0 .. 65535 */
+    int32_t T;             /* rows per lane, 1 .. GDN_MAX_T: T - 1 drafts */
+    int32_t V;             /* tokens of the vocabulary, 1 .. 2^30 */
+    int64_t target_stride; /* elements from one row of target_probs to the next, >= V */
+    int64_t draft_stride;  /* likewise (read only with draft_probs) */
+} gdn_accept_dims;
+
+/*
+ * gdn_draft_accept -- target_probs [B, T] rows p_t of V fp32; draft_tokens [B, T - 1] x_t with the probabilities q_t they
+ * were drawn from, draft_probs [B, T - 1] rows (NULL: 1 at the draft, as for drafts taken greedily); uniform [B, T] numbers
+ * u_t in [0, 1).  Draft t is accepted while u_t q_t(x_t) < p_t(x_t).  With a drafts accepted the next token is drawn from
+ * row a: r = max(p_a - q_a, 0) if draft a was refused, p_a after the last draft (and where r is all 0), and the token is the first v
+ * with r_v > 0 and r_0 + .. + r_v > u_{T-1} (r_0 + .. + r_{V-1}).  Differences, products and sums are good to 2^-40 of the whole.
+ *     accept_len[b] = a + 1 (the tokens to commit: the step's first and the accepted drafts)
+ *     tokens[b]     = the a accepted drafts, the drawn token, then -1
+ * A draft of -1 ends its lane's drafts there (lanes may have fewer), as does one outside the vocabulary, which sets
+ * GDN_ERRBIT_INDEX.  Probabilities that are not finite count as 0 in r, and a row of which nothing is left draws -1: both set
+ * GDN_ERRBIT_NONFINITE.  Lanes with state_indices[b] = -1 are skipped, their outputs left as they are (below -1:
+ * GDN_ERRBIT_INDEX too); state_indices may be NULL.  Only the rows' needed parts are read.  All arrays on 4 bytes.
+ */
+GDN_API gdn_status gdn_draft_accept(const gdn_accept_dims* dims, const float* target_probs, const int32_t* draft_tokens,
+                                    const float* draft_probs, const float* uniform, const int32_t* state_indices,
+                                    int32_t* accept_len, int32_t* tokens, int32_t* err_word, gdn_stream_t stream);
+
 /* Static string naming a status; never NULL. */
 GDN_API const char* gdn_status_string(gdn_status status);
 
