@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_recurrent_f32.cu", "gdn_recurrent_bf16.cu", "gdn_commit.cu", "gdn_prefill.cu",
            "gdn_prefill_chunked.cu", "gdn_gated_norm.cu", "gdn_in_proj_conv.cu",
            "gdn_page_plan.cu", "gdn_qk_norm_rope.cu", "gdn_kv4_attention.cu",
-           "gdn_kv4_attention_wide.cu", "gdn_linear_f32.cu", "gdn_linear_bf16.cu", "gdn_token_probs.cu",
+           "gdn_kv4_attention_wide.cu", "gdn_linear_f32.cu", "gdn_linear_bf16.cu", "gdn_linear_prefill.cu", "gdn_token_probs.cu",
            "gdn_draft_accept.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # hidden visibility: only the GDN_API functions of gdn.h are exported, so that internal symbols (template

@@ -759,7 +759,12 @@ gdn_status gdn_linear_prefill(const gdn_dims* dims, const int32_t* cu_seqlens, c
     LinearParams p;
     s = linear_call(dims, q, k, v, log_decay, state_pool, state_indices, out_indices, nullptr, cu_seqlens, has_initial_state, o,
                     nullptr, true, dims->T > 0, err_word, &p);
-    return s != GDN_OK ? s : run_linear(dims, p, stream);
+    if (s != GDN_OK) return s;
+    cudaError_t e = cudaSuccess;
+    if (launch_linear_prefill(p, dims->qkv_dtype == GDN_BF16, dims->state_dtype == GDN_BF16, static_cast<float*>(workspace),
+                              reinterpret_cast<cudaStream_t>(stream), e))
+        return finish(e);
+    return run_linear(dims, p, stream);
 }
 
 gdn_status gdn_token_probs(const gdn_token_dims* dims, const void* logits, const float* temperature, float* probs,

@@ -202,6 +202,8 @@ struct LinearParams {
     int v_vec;                // v starts on 16 bytes and DV * sizeof(v) % 16 == 0
     float scale;
 };
+// prompts on the tensor cores (DK 64 or 128, bf16 in and out); false (nothing launched) where the call is outside its range
+bool launch_linear_prefill(const LinearParams& p, bool qkv_bf16, bool state_bf16, float* ws, cudaStream_t s, cudaError_t& err);
 // bytes that launch_linear_prefill wants for prompts cut into pieces
 int64_t linear_prefill_workspace(int B, int N, int HV, int DK, int DV);
 cudaError_t launch_linear_f32state(const LinearParams& p, bool qkv_bf16, cudaStream_t s);

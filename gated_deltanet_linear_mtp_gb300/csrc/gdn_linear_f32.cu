@@ -7,6 +7,4 @@ cudaError_t launch_linear_f32state(const LinearParams& p, bool qkv_bf16, cudaStr
     return launch_linear<float>(p, qkv_bf16, s);
 }
 
-int64_t linear_prefill_workspace(int, int, int, int, int) { return 0; }
-
 }  // namespace gdn
