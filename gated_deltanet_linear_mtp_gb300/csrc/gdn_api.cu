@@ -299,6 +299,8 @@ gdn_status linear_call(const gdn_dims* d, const void* q, const void* k, const vo
     p.num_slots = d->num_slots;
     p.out_bf16 = d->out_dtype == GDN_BF16;
     p.v_vec = aligned(v, 16) && ((int64_t)d->DV * (int64_t)dtype_bytes(d->qkv_dtype)) % 16 == 0;
+    p.v_pair = d->DV % 2 == 0 && aligned(v, 2 * dtype_bytes(d->qkv_dtype));
+    p.o_pair = d->DV % 2 == 0 && aligned(o, 2 * dtype_bytes(d->out_dtype));
     p.scale = d->scale;
     *out = p;
     return GDN_OK;

@@ -9,8 +9,9 @@
 // vocabulary of 2^17 too: p - q is taken exactly (as a pair of floats) and summed in pairs of floats (about 2^-46 of the sum, where
 // 64-bit additions of every element would take longer than the reads), the sums of tiles and the search inside one in 64 bits.
 //
-// Bytes bound it: of all the rows a lane reads T - 1 numbers of p and of q, and then one row of each.  One CTA a lane: its
-// warps sum tiles of the row, one warp finds the tile that the threshold falls into and searches that tile again.
+// Bytes bound it: of all the rows a lane reads T - 1 numbers of p and of q, and then one row of each.  A cluster takes a lane:
+// its CTAs' warps sum tiles of the row, the CTAs put their sums into each other's shared memory, and a warp of the one that the
+// threshold falls into finds the tile and reads that tile again.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -23,9 +24,11 @@ namespace gdn {
 
 namespace {
 
-constexpr int kAcceptThreads = 512;
+constexpr int kAcceptThreads = 256;
 constexpr int kAcceptWarps = kAcceptThreads / 32;
-constexpr int kAcceptTiles = 1024;  // tiles of a row at most
+constexpr int kAcceptBlock = 256;     // elements that a warp sums at a time: 8 a lane
+constexpr int kAcceptTiles = 1024;    // tiles of a CTA's part of a row at most
+constexpr int kAcceptMaxCluster = 8;
 
 // a + b exactly, as a rounded sum and its error
 __device__ __forceinline__ float2 two_sum(float a, float b) {
@@ -51,25 +54,49 @@ struct RowPair {
     }
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ double scan(double x, int lane) {  // inclusive, over the warp
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    for (int m = 1; m < 32; m <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x, m);
+        if (lane >= m) x += y;
+    }
     return x;
 }
 
-__global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const DraftAcceptParams p, const int tile) {
-    __shared__ double sums[kAcceptTiles];
+// a pair's sum with another pair, to about 2^-46
+__device__ __forceinline__ void add_pair(float2& a, float2 b) {
+    const float2 s = two_sum(a.x, b.x);
+    a = make_float2(s.x, s.y + (a.y + b.y));
+}
+
+__device__ __forceinline__ uint32_t shared_of(const void* p, uint32_t rank) {  // the same variable in another CTA of the cluster
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// tile: elements of a tile, a multiple of kAcceptBlock; CTA `rank` of the lane's cluster has tiles rank * per ..
+__global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const DraftAcceptParams p, const int tile,
+                                                                          const int per) {
+    __shared__ float2 sums[kAcceptTiles];
+    __shared__ double part[2][kAcceptMaxCluster];  // the CTAs' sums, of either pass
     __shared__ int sh_n;
     __shared__ bool sh_refused;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x, T = p.T, V = p.V;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.T, V = p.V;
+    const int ncta = gridDim.x, rank = blockIdx.x, b = blockIdx.y;
     if (p.indices != nullptr) {
         const int slot = p.indices[b];
-        if (slot == -1) return;
-        if (slot < -1) {
-            if (tid == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
+        if (slot < 0) {  // the whole cluster leaves
+            if (slot < -1 && tid == 0 && rank == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
             return;
         }
     }
+    // shared memory of another CTA is there once that CTA runs: arrived at here, waited for before the first exchange
+    if (ncta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int32_t* drafts = p.drafts + (int64_t)b * (T - 1);
     const float* target = p.target + (int64_t)b * T * p.target_stride;
     const float* draft = p.draft != nullptr ? p.draft + (int64_t)b * (T - 1) * p.draft_stride : nullptr;
@@ -78,9 +105,7 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
         if (lane < T - 1) {
             const int x = drafts[lane];
             real = x >= 0 && x < V;
-            if (x < -1 || x >= V) {
-                if (p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
-            }
+            if ((x < -1 || x >= V) && rank == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
             if (real) {
                 const float px = target[lane * p.target_stride + x];
                 const float qx = draft != nullptr ? draft[lane * p.draft_stride + x] : 1.f;
@@ -103,26 +128,50 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
         else
             r.certain = drafts[n];
     }
-    const int tiles = (V + tile - 1) / tile;
+    const int tiles = (V + tile - 1) / tile, first = rank * per, mine = max(0, min(per, tiles - first));
     bool bad = false;
-    double total = 0.;
+    double before = 0., total = 0., own = 0.;  // sums of the CTAs before this one, of all, of this one
     for (int pass = 0; pass < 2; ++pass) {
-        for (int k = warp; k < tiles; k += kAcceptWarps) {
-            float hi = 0.f, lo = 0.f;
-            const int end = min(V, (k + 1) * tile);
-            for (int v = k * tile + lane; v < end; v += 32) {
-                const float2 x = r.at(v, bad);
-                const float2 s = two_sum(hi, x.x);
-                hi = s.x;
-                lo += s.y + x.y;
+        for (int k = warp; k < mine; k += kAcceptWarps) {
+            float2 acc = make_float2(0.f, 0.f);
+            const int end = min(V, (first + k + 1) * tile);
+            for (int v0 = (first + k) * tile; v0 < end; v0 += kAcceptBlock) {
+                float pv[8], qv[8];  // all loads before any arithmetic
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int v = v0 + 32 * i + lane;
+                    pv[i] = v < end ? r.p[v] : 0.f;
+                    qv[i] = r.q != nullptr && v < end ? r.q[v] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    add_pair(acc, residual(pv[i], v0 + 32 * i + lane == r.certain ? 1.f : qv[i], bad));
             }
-            const double sum = warp_sum((double)hi + (double)lo);
-            if (lane == 0) sums[k] = sum;
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1)
+                add_pair(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, m), __shfl_xor_sync(0xffffffffu, acc.y, m)));
+            if (lane == 0) sums[k] = acc;
         }
         __syncthreads();
-        total = 0.;
-        for (int k = lane; k < tiles; k += 32) total += sums[k];
-        total = warp_sum(total);
+        // every warp forms the same sums, in the same order
+        own = 0.;
+        for (int k = lane; k < mine; k += 32) own += (double)sums[k].x + (double)sums[k].y;
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) own += __shfl_xor_sync(0xffffffffu, own, m);
+        before = 0.;
+        total = own;
+        if (ncta > 1) {  // every CTA puts its sum into every other's shared memory
+            if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            if (tid < ncta)
+                asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(shared_of(&part[pass][rank], (uint32_t)tid)), "d"(own)
+                             : "memory");
+            cluster_sync();
+            total = 0.;
+            for (int c = 0; c < ncta; ++c) {
+                if (c == rank) before = total;
+                total += part[pass][c];
+            }
+        }
         if (total > 0. || (r.q == nullptr && r.certain < 0)) break;
         r.q = nullptr;  // nothing is left of p - q: p itself
         r.certain = -1;
@@ -131,50 +180,71 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
     if (__syncthreads_or(bad) && tid == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_NONFINITE);
     if (warp != 0) return;
 
-    // the first v whose running sum passes the threshold; where rounding leaves none, the last v with r_v > 0
+    // The CTA whose part the threshold falls into draws the token: the first v whose running sum passes it.  Where rounding
+    // leaves none, the last v with r_v > 0, which is in the last CTA with a sum.
     const double threshold = (double)p.uniform[(int64_t)b * T + T - 1] * total;
-    double before = 0.;
+    bool writer = rank == 0, past = false;
+    if (total > 0.) {
+        int winner = 0;
+        if (ncta > 1) {
+            double upto = 0.;
+            int found = -1, last = 0;
+            for (int c = 0; c < ncta; ++c) {
+                const double s = part[r.q == nullptr && r.certain < 0 && sh_refused ? 1 : 0][c];
+                upto += s;
+                if (s > 0.) last = c;
+                if (found < 0 && s > 0. && upto > threshold) found = c;
+            }
+            past = found < 0;
+            winner = past ? last : found;
+        }
+        writer = rank == winner;
+    }
+    if (!writer) return;
     int token = -1;
     if (total > 0.) {
         int found = -1, last = -1;
-        for (int k0 = 0; k0 < tiles && found < 0; k0 += 32) {
-            const double own = k0 + lane < tiles ? sums[k0 + lane] : 0.;
-            double upto = own;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, upto, m);
-                if (lane >= m) upto += y;
-            }
-            upto += before;
-            const unsigned hit = __ballot_sync(0xffffffffu, own > 0. && upto > threshold);
-            const unsigned some = __ballot_sync(0xffffffffu, own > 0.);
+        for (int k0 = 0; k0 < mine && found < 0; k0 += 32) {
+            const double s = k0 + lane < mine ? (double)sums[k0 + lane].x + (double)sums[k0 + lane].y : 0.;
+            const double upto = before + scan(s, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, s > 0. && upto > threshold);
+            const unsigned some = __ballot_sync(0xffffffffu, s > 0.);
             if (some != 0u) last = k0 + 31 - __clz(some);
-            if (hit != 0u) {
+            if (hit != 0u && !past) {
                 found = k0 + __ffs(hit) - 1;
-                before = __shfl_sync(0xffffffffu, upto - own, __ffs(hit) - 1);
+                before = __shfl_sync(0xffffffffu, upto - s, __ffs(hit) - 1);
             } else {
                 before = __shfl_sync(0xffffffffu, upto, 31);
             }
         }
-        const bool past = found < 0;
-        const int k = past ? last : found;
-        const int end = min(V, (k + 1) * tile);
+        if (found < 0) past = true;
+        const int k = first + (past ? last : found), end = min(V, (k + 1) * tile);
         bool dummy = false;
-        for (int v0 = k * tile; v0 < end; v0 += 32) {
-            const float2 x = v0 + lane < end ? r.at(v0 + lane, dummy) : make_float2(0.f, 0.f);
-            const double own = (double)x.x + (double)x.y;
-            double upto = own;
+        for (int v0 = k * tile; v0 < end; v0 += kAcceptBlock) {  // 8 neighbours a lane
+            float2 x[8];
+            double s = 0.;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, upto, m);
-                if (lane >= m) upto += y;
+            for (int i = 0; i < 8; ++i) {
+                const int v = v0 + 8 * lane + i;
+                x[i] = v < end ? r.at(v, dummy) : make_float2(0.f, 0.f);
+                s += (double)x[i].x + (double)x[i].y;
             }
-            upto += before;
-            const unsigned hit = __ballot_sync(0xffffffffu, own > 0. && upto > threshold);
-            const unsigned some = __ballot_sync(0xffffffffu, own > 0.);
-            if (some != 0u) token = v0 + 31 - __clz(some);  // the last so far
-            if (!past && hit != 0u) {
-                token = v0 + __ffs(hit) - 1;
+            double upto = before + scan(s, lane) - s;
+            int hit = INT32_MAX, some = -1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const double own_i = (double)x[i].x + (double)x[i].y;
+                upto += own_i;
+                if (own_i > 0.) {
+                    some = v0 + 8 * lane + i;
+                    if (upto > threshold) hit = min(hit, some);
+                }
+            }
+            some = __reduce_max_sync(0xffffffffu, some);
+            hit = __reduce_min_sync(0xffffffffu, hit);
+            if (some >= 0) token = some;  // the last so far
+            if (!past && hit != INT32_MAX) {
+                token = hit;
                 break;
             }
             before = __shfl_sync(0xffffffffu, upto, 31);
@@ -189,10 +259,25 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
 }  // namespace
 
 cudaError_t launch_draft_accept(const DraftAcceptParams& p, cudaStream_t s) {
-    int tile = 256;
-    while ((int64_t)tile * kAcceptTiles < p.V) tile *= 2;
-    gdn_draft_accept_kernel<<<p.B, kAcceptThreads, 0, s>>>(p, tile);
-    return cudaGetLastError();
+    // CTAs a lane: at least 4 blocks a warp while there are lanes enough, fewer where there are not
+    int ncta = 1;
+    while (ncta < kAcceptMaxCluster &&
+           (int64_t)p.V > (int64_t)ncta * kAcceptBlock * kAcceptWarps * ((int64_t)p.B * ncta < 608 ? 1 : 4))
+        ncta *= 2;
+    int tile = kAcceptBlock;
+    while ((int64_t)tile * kAcceptTiles * ncta < p.V) tile *= 2;
+    const int tiles = (p.V + tile - 1) / tile, per = (tiles + ncta - 1) / ncta;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ncta, (unsigned)p.B);
+    cfg.blockDim = dim3(kAcceptThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ncta;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ncta > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, gdn_draft_accept_kernel, p, tile, per);
 }
 
 }  // namespace gdn

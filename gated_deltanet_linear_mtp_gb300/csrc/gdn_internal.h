@@ -200,6 +200,7 @@ struct LinearParams {
     int B, T, N, HK, HV, DK, DV, num_slots;  // N: packed tokens (prefill)
     int out_bf16;
     int v_vec;                // v starts on 16 bytes and DV * sizeof(v) % 16 == 0
+    int v_pair, o_pair;       // DV is even, and v (o) starts on two elements: neighbouring rows go together
     float scale;
 };
 // prompts on the tensor cores (DK 64 or 128, bf16 in and out); false (nothing launched) where the call is outside its range

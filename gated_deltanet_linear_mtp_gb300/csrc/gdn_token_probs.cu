@@ -5,8 +5,14 @@
 // -inf logits (forbidden tokens) get 0; a row of nothing else gets zeros.  A NaN or +inf logit, or a temperature that is
 // negative or not finite, makes the row zeros and sets GDN_ERRBIT_NONFINITE.
 //
-// Bytes bound it: a row is read once from DRAM and written once.  A CTA takes a row: a first pass with the running maximum
-// and sum, a second over the row again (from L2) that writes.
+// Bytes bound it: a row is read once from DRAM and written once.  A thread-block cluster takes a row, each CTA a run of it:
+// a first pass with the running maximum and sum, 8 or 16 numbers at a time, one exchange of (maximum, sum, index) within the
+// cluster, and a second pass that reads the run again (from L1 or L2, where it still is) and writes.
+//
+// exp((x - m) / T) = 2^(c x - o), c = log2(e) / T and o = c m rounded: one multiply-add that rounds its result alone, and a
+// common error of o that the division by the sum takes out again.  ex2.approx.ftz adds 2^-22 and takes what is below 2^-126 as 0.
+// That needs |o| <= 2^20 (o's error stays below 1/16): a row whose largest logit lies beyond, one with NaN or +inf, and one
+// whose largest entries are the type's lowest value go through the first pass again with differences x - m, and checks.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,89 +28,253 @@ namespace {
 
 constexpr int kProbThreads = 512;
 constexpr int kProbWarps = kProbThreads / 32;
+constexpr int kProbMaxCluster = 8;
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// (x - top) / T: the quotient to within one rounding from the reciprocal and one correction
-__device__ __forceinline__ float over_t(float d, float T, float rT) {
-    const float q = d * rT;
-    return fmaf(fmaf(-q, T, d), rT, q);
+// 16 bytes of logits as numbers
+__device__ __forceinline__ void unpack16(const uint4& r, float (&f)[4]) {
+    f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack16(const uint4& r, float (&f)[8]) {  // bf16: element 2i in the lower half of word i
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
 }
 
-__device__ __forceinline__ float weight(float x, float top, float T, float rT) {
-    const float d = x - top;
-    // below e^-104 fp32 has nothing left; d may be -inf, whose quotient is not formed
-    return d * rT < -104.f ? 0.f : expf(over_t(d, T, rT));
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// what a part of a row has: its largest logit, the sum against it, the place of the first largest, and whether it is not sound
+struct Part {
+    float m, s;
+    int at, bad;
+};
+
+// Weights of a row.  kFar: from differences to the maximum, for logits of any size; else from c x - o.
+template <bool kFar>
+struct Weights {
+    float c;
+    __device__ __forceinline__ float offset(float m) const { return kFar ? m : fmaxf(c * m, -1048576.f); }
+    __device__ __forceinline__ float operator()(float x, float o) const {
+        if (!kFar) return ex2(fmaf(c, x, -o));
+        const float d = x - o;  // -inf where x is, or where it lies that far below
+        return d > -FLT_MAX ? ex2(c * d) : 0.f;
+    }
+    __device__ __forceinline__ float ratio(float o, float o2) const {  // of the weights against o to those against o2 >= o
+        return kFar ? (*this)(o, o2) : ex2(o - o2);
+    }
+    // a part joined with another: the sums against the larger maximum
+    __device__ __forceinline__ void join(Part& a, const Part& b) const {
+        const float m = fmaxf(a.m, b.m);
+        if (m > -INFINITY) {
+            const float o = offset(m);
+            a.s = (a.m > -INFINITY ? a.s * ratio(offset(a.m), o) : 0.f) + (b.m > -INFINITY ? b.s * ratio(offset(b.m), o) : 0.f);
+        }
+        a.at = b.m > a.m || (b.m == a.m && b.at < a.at) ? b.at : a.at;
+        a.m = m;
+        a.bad |= b.bad;
+    }
+};
+
+__device__ __forceinline__ uint32_t shared_of(const void* p, uint32_t rank) {  // the same variable in another CTA of the cluster
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
 }
 
 template <typename InT>
-__global__ void __launch_bounds__(kProbThreads) gdn_token_probs_kernel(const TokenProbsParams p) {
-    __shared__ float sh_m[kProbWarps], sh_s[kProbWarps];
-    __shared__ int sh_i[kProbWarps];
+__global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const TokenProbsParams p, const int run) {
+    constexpr int EPC = 16 / sizeof(InT);  // elements of a 16-byte piece
+    constexpr int U = 4;                   // pieces in flight a thread
+    __shared__ Part warps[2][kProbWarps];  // of the first pass, and of its repetition
+    __shared__ Part parts[2][kProbMaxCluster];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t row = blockIdx.x;
+    const int ncta = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
+    const int64_t row = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    if (row >= (int64_t)p.B * p.T) return;  // the whole cluster leaves
+    // shared memory of another CTA is there once that CTA runs: arrived at here, waited for before the exchange
+    if (ncta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const InT* x = static_cast<const InT*>(p.logits) + row * p.logits_stride;
     float* y = p.probs + row * p.probs_stride;
     const float T = p.temperature[row / p.T];
     const bool greedy = T >= 0.f && T < FLT_MIN;
-    const float rT = greedy ? 1.f : 1.f / T;
-    bool bad = !(T >= 0.f) || T > FLT_MAX;
+    const float c = 1.44269504f / (greedy ? 1.f : T);
+    // this CTA's elements lo .. hi - 1, of them whole pieces a .. b - 1
+    const int lo = (int)min((int64_t)rank * run, (int64_t)p.V), hi = (int)min((int64_t)lo + run, (int64_t)p.V);
+    const int off = (int)((reinterpret_cast<uintptr_t>(x + lo) & 15u) / sizeof(InT));
+    const int a = min(hi, lo + (off == 0 ? 0 : EPC - off)), b = a + (hi - a) / EPC * EPC;
+    const uint4* xv = reinterpret_cast<const uint4*>(x + a);
+    const int pieces = (b - a) / EPC;
+    const int edge = (a - lo) + (hi - b);  // elements in no piece
+    auto edge_at = [&](int i) { return i < a - lo ? lo + i : b + i - (a - lo); };
 
-    float m = -INFINITY, s = 0.f;
-    int at = p.V;
-    for (int i = tid; i < p.V; i += kProbThreads) {
-        const float f = as_f32(x[i]);
-        bad |= !(f <= FLT_MAX);
-        if (f > m) {
-            if (m > -INFINITY) s *= weight(m, f, T, rT);
-            m = f;
-            at = i;
+    auto first_pass = [&](auto wf) -> Part {
+        constexpr bool kFar = sizeof(wf) != sizeof(float);
+        const Weights<kFar> w{c};
+        float m = -INFINITY, o = 0.f, s = 0.f;
+        int at = INT32_MAX;
+        bool bad = false;
+        auto raise = [&](float top) {  // a new maximum
+            const float o2 = w.offset(top);
+            s = m > -INFINITY ? s * w.ratio(o, o2) : 0.f;
+            m = top;
+            o = o2;
+        };
+        for (int c0 = tid; c0 < pieces; c0 += U * kProbThreads) {
+            uint4 raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * kProbThreads < pieces) raw[u] = xv[c0 + u * kProbThreads];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * kProbThreads >= pieces) break;
+                float f[EPC];
+                unpack16(raw[u], f);
+                float top = f[0];
+#pragma unroll
+                for (int i = 1; i < EPC; ++i) top = fmaxf(top, f[i]);
+                if (top > m) {
+                    raise(top);
+                    if (greedy)
+#pragma unroll
+                        for (int i = EPC - 1; i >= 0; --i)
+                            if (f[i] == top) at = a + (c0 + u * kProbThreads) * EPC + i;
+                }
+                if (kFar)
+#pragma unroll
+                    for (int i = 0; i < EPC; ++i) bad |= !(f[i] <= FLT_MAX);
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < EPC; i += 2) {
+                    s0 += w(f[i], o);
+                    s1 += w(f[i + 1], o);
+                }
+                s += s0 + s1;
+            }
         }
-        if (m > -INFINITY) s += weight(f, m, T, rT);
-    }
-    bad = __syncthreads_or(bad);
-    auto join = [&](float m2, float s2, int at2) {
-        const float t = fmaxf(m, m2);
-        if (t > -INFINITY && !bad && !greedy) s = (s > 0.f ? s * weight(m, t, T, rT) : 0.f) + (s2 > 0.f ? s2 * weight(m2, t, T, rT) : 0.f);
-        at = m2 > m || (m2 == m && at2 < at) ? at2 : at;
-        m = t;
+        if (tid < edge) {  // the ends, one element a thread
+            const int v = edge_at(tid);
+            const float f = as_f32(x[v]);
+            if (f == m) at = min(at, v);
+            if (f > m) {
+                raise(f);
+                at = v;
+            }
+            bad |= kFar && !(f <= FLT_MAX);
+            s += w(f, o);
+        }
+        Part all{m, s, at, bad};
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1)
+            w.join(all, Part{__shfl_xor_sync(0xffffffffu, all.m, k), __shfl_xor_sync(0xffffffffu, all.s, k),
+                             __shfl_xor_sync(0xffffffffu, all.at, k), __shfl_xor_sync(0xffffffffu, all.bad, k)});
+        if (lane == 0) warps[kFar][warp] = all;
+        __syncthreads();
+        all = warps[kFar][lane % kProbWarps];
+#pragma unroll
+        for (int k = kProbWarps / 2; k >= 1; k >>= 1)
+            w.join(all, Part{__shfl_xor_sync(0xffffffffu, all.m, k), __shfl_xor_sync(0xffffffffu, all.s, k),
+                             __shfl_xor_sync(0xffffffffu, all.at, k), __shfl_xor_sync(0xffffffffu, all.bad, k)});
+        if (ncta > 1) {  // every CTA puts its part into every other's shared memory
+            if (!kFar) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            if (tid < ncta) {
+                const uint32_t to = shared_of(&parts[kFar][rank], (uint32_t)tid);
+                asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(__float_as_uint(all.m)),
+                             "r"(__float_as_uint(all.s)), "r"(all.at), "r"(all.bad)
+                             : "memory");
+            }
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            all = parts[kFar][0];
+            for (int r = 1; r < ncta; ++r) w.join(all, parts[kFar][r]);
+        }
+        return all;
     };
+    Part all = first_pass(float{});
+    // every thread of the cluster has the same sums, and takes the same way
+    const bool far = !(fabsf(c * all.m) <= 1048576.f) || !(all.s > 0.f && all.s <= FLT_MAX);
+    if (far && all.m != -INFINITY) all = first_pass(double{});
+    all.bad |= !(T >= 0.f) || T > FLT_MAX || !(all.s <= FLT_MAX);
+    if (all.bad && tid == 0 && rank == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_NONFINITE);
+    const bool none = all.bad || !(all.m > -INFINITY);
+    if (none || greedy) {  // zeros, and a 1 at the place of the first largest
+        for (int v = lo + tid; v < hi; v += kProbThreads) y[v] = !none && v == all.at ? 1.f : 0.f;
+        return;
+    }
+    auto second_pass = [&](auto wf) {
+        const Weights<sizeof(wf) != sizeof(float)> w{c};
+        const float o = w.offset(all.m), f = 1.f / all.s;
+        if ((reinterpret_cast<uintptr_t>(y + a) & 15u) == 0) {
+            for (int c0 = tid; c0 < pieces; c0 += U * kProbThreads) {
+                uint4 raw[U];
 #pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, k), s2 = __shfl_xor_sync(0xffffffffu, s, k);
-        join(m2, s2, __shfl_xor_sync(0xffffffffu, at, k));
-    }
-    if (lane == 0) sh_m[warp] = m, sh_s[warp] = s, sh_i[warp] = at;
-    __syncthreads();
-    m = sh_m[lane % kProbWarps], s = sh_s[lane % kProbWarps], at = sh_i[lane % kProbWarps];
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * kProbThreads < pieces) raw[u] = xv[c0 + u * kProbThreads];
 #pragma unroll
-    for (int k = 1; k < kProbWarps; k <<= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, k), s2 = __shfl_xor_sync(0xffffffffu, s, k);
-        join(m2, s2, __shfl_xor_sync(0xffffffffu, at, k));
-    }
-    if (bad && tid == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_NONFINITE);
-    const bool none = bad || !(m > -INFINITY);
-    const float rs = none ? 0.f : 1.f / s;
-    for (int i = tid; i < p.V; i += kProbThreads) {
-        float f = 0.f;
-        if (greedy)
-            f = !none && i == at ? 1.f : 0.f;
-        else if (!none)
-            f = weight(as_f32(x[i]), m, T, rT) * rs;
-        y[i] = f;
-    }
+                for (int u = 0; u < U; ++u) {
+                    if (c0 + u * kProbThreads >= pieces) break;
+                    float e[EPC];
+                    unpack16(raw[u], e);
+                    float4* dst = reinterpret_cast<float4*>(y + a + (c0 + u * kProbThreads) * EPC);
+#pragma unroll
+                    for (int i = 0; i < EPC; i += 4)
+                        __stcs(dst + i / 4, make_float4(w(e[i], o) * f, w(e[i + 1], o) * f, w(e[i + 2], o) * f,
+                                                        w(e[i + 3], o) * f));
+                }
+            }
+            if (tid < edge) y[edge_at(tid)] = w(as_f32(x[edge_at(tid)]), o) * f;
+        } else {  // the places of x and y differ: neighbours a warp
+            for (int v0 = lo + tid; v0 < hi; v0 += 8 * kProbThreads) {
+                InT raw[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (v0 + u * kProbThreads < hi) raw[u] = x[v0 + u * kProbThreads];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (v0 + u * kProbThreads < hi) __stcs(y + v0 + u * kProbThreads, w(as_f32(raw[u]), o) * f);
+            }
+        }
+    };
+    if (far)
+        second_pass(double{});
+    else
+        second_pass(float{});
+}
+
+template <typename InT>
+cudaError_t launch_t(const TokenProbsParams& p, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.B * p.T;
+    // CTAs a row.  Runs of up to 32768 elements where rows fill the GPU (512 rows of 131072 bf16: 4 CTAs 96 us, 2 98, 8 122; of 32768:
+    // 1 CTA 25 us, 2 30, 4 41: a CTA's start and the exchange cost some microseconds), of 4096 where they do not (one row of 131072:
+    // 8 CTAs 9.0 us, 4 12.7, 1 27.6)
+    int ncta = 1;
+    while (ncta < kProbMaxCluster && ((int64_t)p.V > (int64_t)ncta * 32768 || (rows * ncta < 152 && p.V > ncta * 4096))) ncta *= 2;
+    const int run = (int)(((int64_t)p.V + ncta * 64 - 1) / (ncta * 64) * 64);
+    const unsigned gy = (unsigned)(rows < 32768 ? rows : 32768);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ncta, gy, (unsigned)((rows + gy - 1) / gy));
+    cfg.blockDim = dim3(kProbThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ncta;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ncta > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, gdn_token_probs_kernel<InT>, p, run);
 }
 
 }  // namespace
 
 cudaError_t launch_token_probs(const TokenProbsParams& p, cudaStream_t s) {
-    const unsigned rows = (unsigned)(p.B * p.T);
-    if (p.bf16)
-        gdn_token_probs_kernel<__nv_bfloat16><<<rows, kProbThreads, 0, s>>>(p);
-    else
-        gdn_token_probs_kernel<float><<<rows, kProbThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.bf16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
 }
 
 }  // namespace gdn
