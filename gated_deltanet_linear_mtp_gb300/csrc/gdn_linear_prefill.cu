@@ -16,9 +16,12 @@
 // 2^-17 of each term for a bf16 pool and, in three parts, to 2^-25 for an fp32 pool, whose states keep fp32's digits.  P is
 // rounded to bf16 as o is: its rounding errors are those of single terms of a sum.
 //
-// Ten warps: 0-3 form P from the scores and write o (thread = row i), 4-7 form V' from V and the state (thread = token, then
-// dk), 8 brings the tiles by TMA (two stages), 9 issues the products.  The order of products in a step, inter, update, intra and
-// the next chunk's scores, leaves the state's conversion (the only serial chain between chunks) the time of the last two.
+// Three groups of eight warps: the first forms P from the scores (thread = row i and a half of the columns), the second keeps the
+// state (thread = dk and 32 dv), the third forms V' from V (thread = token and 32 dv) and takes o from the products (thread = row i and 32 dv); warp 24
+// brings the tiles by TMA (two stages), 25 issues the products, 26 stores o by TMA from where V was.  A group's work on a chunk is a few hundred dependent
+// instructions, at which one warp issues every sixth cycle or so: eight warps a group take half the time of four.  For the same
+// reason code is kept short (unrolled to 95 KB, the warps waited for instructions).  The only serial chain between chunks is
+// state -> inter -> state and V' -> update -> state; the scores of the next chunk and the intra product fill the tensor cores.
 //
 // Few prompts and heads leave SMs without work: then prompts are cut into pieces (linear_split), a first launch forms what
 // each piece adds to the state (K and V only), and the second starts every piece from the sum of those before it.
@@ -34,24 +37,28 @@ namespace {
 
 constexpr int kLC = 128;   // tokens of a chunk
 constexpr int kLDv = 64;   // value dimensions of a CTA
-constexpr int kLThreads = 320;
+constexpr int kLGroup = 256;                 // threads of a group
+constexpr int kLThreads = 3 * kLGroup + 96;
+constexpr int kLHalf = kLDv / 2;              // value dimensions of a thread
 constexpr uint32_t kLPolls = GDN_WAIT_POLLS;
 
-enum { kFull = 0, kEmpty = 2, kScFull = 4, kIFull, kUFull, kOFull, kDrain, kPReady, kVReady, kLReady, kSReady, kOFree, kNumLBars };
+// barriers (the first ones: one for each of two stages or score buffers); a stage's K and Q are free before its V
+enum { kQkFull = 0, kVFull = 2, kEmptyQk = 4, kEmptyV = 6, kScFull = 8, kIFull = 10, kUFull, kOFull, kStFree, kDrain, kPReady, kVReady = kPReady + 2, kUFree, kSReady, kOFree,
+       kStaged, kNumLBars };
 // tensor memory: scores (P over them) of two chunks, intra, inter, update
 constexpr uint32_t kScCol = 0, kO1Col = 256, kO2Col = 320, kUCol = 384, kLCols = 512;
 
-template <int DK>
+template <int DK, int NP>
 struct LinearPlan {
     static constexpr uint32_t BOX = kLC * 128;             // 64 columns of 128 rows
     static constexpr uint32_t QK = DK / 64 * BOX;
     static constexpr uint32_t Q_OFF = 0, K_OFF = QK, V_OFF = 2 * QK, STAGE = 2 * QK + BOX;
-    static constexpr uint32_t VP_OFF = 2 * STAGE;          // V' hi, then its second part
-    static constexpr uint32_t SH_OFF = VP_OFF + 2 * BOX;   // S hi, then lo: DK rows of 128 bytes each
-    static constexpr uint32_t SPART = DK * 128;
-    // the third part of V' lies over S (and behind it): the product that reads S is complete before it is written
-    static constexpr uint32_t S_BYTES = 2 * SPART > BOX ? 2 * SPART : BOX;
-    static constexpr uint32_t PW_OFF = SH_OFF + S_BYTES;   // g^0 .. g^128
+    static constexpr uint32_t VP_OFF = 2 * STAGE;          // the parts of V'
+    static constexpr uint32_t SH_OFF = VP_OFF + NP * BOX;  // S: DK rows of 128 bytes
+    // o on its way out: a place of its own where there is room (all but fp32 pools of DK = 128), else where V was
+    static constexpr bool OWN = DK == 64 || NP == 2;
+    static constexpr uint32_t O_OFF = SH_OFF + DK * 128;
+    static constexpr uint32_t PW_OFF = O_OFF + (OWN ? BOX : 0) + 128;  // g^0 .. g^128, behind 32 floats that are read and not used
     static constexpr uint32_t BAR_OFF = PW_OFF + 132 * 4;
     static constexpr uint32_t END = BAR_OFF + 8 * kNumLBars + 32;
     static constexpr uint32_t BYTES = END + 1024;          // the base is aligned to 1024
@@ -59,7 +66,7 @@ struct LinearPlan {
 };
 
 struct LinearMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 // (x, y) as bf16 in one word, and what that leaves of them
@@ -69,26 +76,60 @@ __device__ __forceinline__ uint32_t take_bf16(float2& x) {
     return w;
 }
 
+// One lane of the warp, chosen by the hardware
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {  // without waiting
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// What a wait does after its first try, out of line: the code that runs once a chunk stays short
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t fail) {
+    for (uint32_t k = 0; k < kLPolls; ++k) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((k & 255u) == 255u) {
+            int f;
+            asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(f) : "r"(fail) : "memory");
+            if (f != 0) return false;
+        }
+    }
+    asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(fail) : "memory");
+    return false;
+}
+
 // kState: the first launch of cut prompts (what a piece adds to the state; no queries, no outputs)
 template <int DK, typename StT, bool kState>
 __global__ void __launch_bounds__(kLThreads, 1)
     gdn_linear_prefill_kernel(const LinearParams p, const __grid_constant__ LinearMaps maps, const int piece, float* ws) {
     constexpr int NP = std::is_same<StT, float>::value ? 3 : 2;  // parts of V'
-    using PL = LinearPlan<DK>;
+    using PL = LinearPlan<DK, NP>;
     const int ndv = (p.DV + kLDv - 1) / kLDv;
     const int item = blockIdx.x, tile = item % ndv, h = item / ndv % p.HV, b = item / (ndv * p.HV);
     const int dv0 = tile * kLDv, hk = h / (p.HV / p.HK);
-    const int tid = threadIdx.x, warp = tid >> 5, lt = tid & 127;
+    const int tid = threadIdx.x, warp = __reduce_min_sync(0xffffffffu, tid >> 5), lt = tid & 127;
+    const int hf = (warp >> 2) & 1, wl = warp & 3;  // half of a group, and the warp's quarter of the lanes
 
+    // everything that tells what to do is asked for at once
     const int slot = p.indices[b];
     const int out = p.out_indices != nullptr ? p.out_indices[b] : slot;
+    const int lo = p.cu_seqlens[b], hi = p.cu_seqlens[b + 1];
+    const bool init = p.has_init == nullptr || p.has_init[b] != 0;
+    const float ld = p.log_decay[h];
     const bool reporter = !kState && p.err != nullptr && tid == 0;
     if (slot == -1) return;
     if (slot < -1 || slot >= p.num_slots || out < -1 || out >= p.num_slots) {
         if (reporter) atomicOr(p.err, GDN_ERRBIT_INDEX);
         return;
     }
-    const int lo = p.cu_seqlens[b], hi = p.cu_seqlens[b + 1];
     if (lo < 0 || hi < lo || hi > p.N) {
         if (reporter) atomicOr(p.err, GDN_ERRBIT_SEQLEN);
         return;
@@ -102,7 +143,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const bool last = first + n == all, cut = n < all;
     if (kState && last) return;  // nothing starts behind it
     if (all == 0 && (out < 0 || out == slot)) return;
-    const bool init = p.has_init == nullptr || p.has_init[b] != 0;
     const int nch = (n + kLC - 1) / kLC;
     const int tok0 = lo + first;
 
@@ -115,16 +155,18 @@ __global__ void __launch_bounds__(kLThreads, 1)
     volatile int* fail = reinterpret_cast<volatile int*>(sm + PL::BAR_OFF + 8 * kNumLBars);
     volatile int* odd = fail + 1;  // [2]: c + 1 where V of chunk c (by its parity) holds an infinity or NaN
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + PL::BAR_OFF + 8 * kNumLBars + 16);
-    const float ld = p.log_decay[h];
 
     if (warp == 0) tmem_alloc(smem_u32(tmem_slot), kLCols);
     if (tid == 32) {
-        for (int i = 0; i < 2; ++i) mbar_init(bar(kFull + i), 1), mbar_init(bar(kEmpty + i), kState ? 1 : 1 + 128);
-        for (int i = kScFull; i < kPReady; ++i) mbar_init(bar(i), 1);       // arrivals of products
-        for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), 128);  // of a group of threads
+        for (int i = kQkFull; i < kPReady; ++i)
+            if (!(PL::OWN && !kState) || (i & ~1) != kEmptyV) mbar_init(bar(i), 1);         // arrivals of copies and products
+        if (PL::OWN && !kState)
+            for (int i = 0; i < 2; ++i) mbar_init(bar(kEmptyV + i), kLGroup);  // of the group that reads V last
+        for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), kLGroup);  // of a group of threads
         fence_mbar_init();
         fail[0] = odd[0] = odd[1] = 0;
     }
+    if (tid < 32) pw[tid - 32] = 0.f;
     if (tid < kLC + 1) pw[tid] = tid == 0 ? 1.f : (float)exp((double)tid * (double)ld);
     tc_fence_before();
     __syncthreads();
@@ -134,57 +176,189 @@ __global__ void __launch_bounds__(kLThreads, 1)
     auto stage = [&](int c) -> uint32_t { return (uint32_t)(c & 1) * PL::STAGE; };
     // bounded: a wait that runs out marks the CTA as failed, which ends every other wait of it
     auto wait = [&](int i, uint32_t parity) -> bool {
-        for (uint32_t k = 0; k < kLPolls; ++k) {
-            if (mbar_try_wait(bar(i), parity)) return true;
-            if ((k & 255u) == 255u && *fail != 0) return false;
-        }
-        *fail = 1;
-        return false;
+        return mbar_try_wait(bar(i), parity) || wait_more(bar(i), parity, smem_u32(const_cast<int*>(fail)));
     };
     auto warp_wait = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(i, parity)); };
 
-    if (warp < 4 && !kState) {
-        // ============ thread = row i of the chunk: P from the scores, o from the two products ============
+    if (warp < 8) {
+        // ============ thread = row i of the chunk: P from the scores ============
         float r[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) r[e] = pw[e];
+        for (int c = 0; c < (kState ? 0 : nch); ++c) {
+            if (!warp_wait(kScFull + (c & 1), (uint32_t)(c >> 1) & 1u)) break;
+            tc_fence_after();
+            const uint32_t sc = lane_base + kScCol + (uint32_t)(c & 1) * 128;
+            // 16 columns at a time of this half's 64; P lies over this half's scores that have been read
+#pragma unroll 1
+            for (int jb = 4 * hf; jb < 4 * hf + 4; ++jb) {
+                uint32_t w[8];
+                float x[16];
+                if (jb < 2 * wl + 2) {
+                    tmem_ld16(sc + 16 * jb, x);
+                    tmem_wait_ld();
+                }
+                if (jb < 2 * wl) {  // below the diagonal for every row of the warp
+                    const float f = pw[lt - (16 * jb + 15)];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 g2 = __fmul2_rn(make_float2(f, f), make_float2(r[15 - 2 * e], r[14 - 2 * e]));
+                        const float2 y = __fmul2_rn(g2, make_float2(x[2 * e], x[2 * e + 1]));
+                        w[e] = bf16x2_bits(y.x, y.y);
+                    }
+                } else if (jb < 2 * wl + 2) {
+                    const float* fp = pw + (lt - 16 * jb);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int d = lt - 16 * jb - 2 * e;  // i - j of the first of the two
+                        // the factors are read in any case (32 floats in front of g^0 are there to be): no branch, a select
+                        const float y0 = x[2 * e] * fp[-2 * e], y1 = x[2 * e + 1] * fp[-2 * e - 1];
+                        w[e] = bf16x2_bits(d >= 0 ? y0 : 0.f, d >= 1 ? y1 : 0.f);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = 0u;
+                }
+                tmem_st8(sc + 64 * hf + 8 * (jb & 3), w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(kPReady + (c & 1)));
+        }
+    } else if (warp < 16) {
+        // ============ thread = dk, half of the tile: the state ============
+        const bool mine = lt < DK;
+        const int dvh = dv0 + kLHalf * hf;                        // the thread's first value dimension
+        const int64_t row = ((int64_t)h * p.DV + dvh) * DK + lt;  // of [HV, DV, DK]: its row, column dk
+        const int64_t slot_elems = (int64_t)p.HV * p.DV * DK;
+        float2 S[kLHalf / 2];
+#pragma unroll
+        for (int e = 0; e < kLHalf / 2; ++e) S[e] = make_float2(0.f, 0.f);
+        float* wsp = ws != nullptr ? ws + (int64_t)item * gridDim.y * (kLDv * DK) + kLHalf * hf * DK + lt : nullptr;
+        // pieces after the first start from the states that the first launch left; it also kept the initial state of a cut
+        // prompt, whose slot the prompt's last piece may have overwritten
+        const bool from_ws = !kState && cut;
+        if (mine) {
+            if (from_ws) {
+                const int np = blockIdx.y == 0 ? 0 : 1;
+                const float gp = (float)exp((double)piece * (double)ld);
+                for (int s = np; s <= (int)blockIdx.y; ++s) {
+                    const float* src = wsp + (int64_t)s * (kLDv * DK);
+#pragma unroll
+                    for (int e = 0; e < kLHalf / 2; ++e) {
+                        const float2 u = make_float2(src[(2 * e) * DK], src[(2 * e + 1) * DK]);
+                        S[e] = s == np ? u : __ffma2_rn(make_float2(gp, gp), S[e], u);
+                    }
+                }
+            } else if (init && blockIdx.y == 0) {
+                const StT* src = static_cast<const StT*>(p.pool) + (int64_t)slot * slot_elems + row;
+#pragma unroll
+                for (int e = 0; e < kLHalf; ++e) {
+                    const float x = dvh + e < p.DV ? to_f32(src[(int64_t)e * DK]) : 0.f;
+                    if (e & 1) S[e / 2].y = x; else S[e / 2].x = x;
+                }
+            }
+            if (kState && blockIdx.y == 0) {
+#pragma unroll
+                for (int e = 0; e < kLHalf; ++e) wsp[e * DK] = (e & 1) ? S[e / 2].y : S[e / 2].x;
+            }
+        }
+        auto put_state = [&]() {  // S in bf16, rows dk
+            if (mine) {
+#pragma unroll
+                for (int c8 = 0; c8 < kLHalf / 8; ++c8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) w[u] = bf16x2_bits(S[4 * c8 + u].x, S[4 * c8 + u].y);
+                    *reinterpret_cast<uint4*>(sm + PL::SH_OFF + sw128(DK, lt, 4 * hf + c8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar(kSReady));
+        };
+        bool ok = true;
+        for (int c = 0; c < nch; ++c) {
+            if constexpr (!kState) {
+                ok = c == 0 || warp_wait(kIFull, (uint32_t)(c - 1) & 1u);  // the last inter product has read S
+                if (!ok) break;
+                put_state();
+            }
+            ok = warp_wait(kUFull, (uint32_t)c & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const float gm = pw[min(kLC, n - c * kLC)];
+#pragma unroll
+            for (int c0 = 0; c0 < kLHalf; c0 += 16) {
+                float u[16];
+                tmem_ld16(lane_base + kUCol + kLHalf * hf + c0, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    S[c0 / 2 + e] = __ffma2_rn(make_float2(gm, gm), S[c0 / 2 + e], make_float2(u[2 * e], u[2 * e + 1]));
+            }
+            tc_fence_before();
+            mbar_arrive(bar(kUFree));
+        }
+        if (ok && mine) {
+            if constexpr (kState) {
+                float* dst = wsp + (int64_t)(blockIdx.y + 1) * (kLDv * DK);
+#pragma unroll
+                for (int e = 0; e < kLHalf; ++e) dst[e * DK] = (e & 1) ? S[e / 2].y : S[e / 2].x;
+            } else if (last && out >= 0) {
+                StT* dst = static_cast<StT*>(p.pool) + (int64_t)out * slot_elems + row;
+#pragma unroll
+                for (int e = 0; e < kLHalf; ++e) {
+                    const float x = (e & 1) ? S[e / 2].y : S[e / 2].x;
+                    if (dvh + e < p.DV) {
+                        if constexpr (std::is_same<StT, float>::value)
+                            dst[(int64_t)e * DK] = x;
+                        else
+                            dst[(int64_t)e * DK] = __float2bfloat16_rn(x);
+                    }
+                }
+            }
+        }
+    } else if (warp < 24) {
+        // ============ thread = token, half of the tile: V'; thread = row i, half of the tile: o ============
         const float gi = pw[lt + 1];
-        auto write_o = [&](int c) -> bool {
-            if (!warp_wait(kOFull, (uint32_t)c & 1u)) return false;
+        auto write_o = [&](int c) -> bool {  // kOFull has been seen
             tc_fence_after();
             const int m = min(kLC, n - c * kLC);
             __nv_bfloat16* dst =
                 static_cast<__nv_bfloat16*>(p.o) + ((int64_t)(tok0 + c * kLC + lt) * p.HV + h) * p.DV + dv0;
-            const bool slow = odd[c & 1] == c + 1;
+            const bool slow = odd[c & 1] == c + 1;  // then V is read once more
+            // whole chunks go through shared memory and out by TMA: stored from here, 32 rows of 16 bytes an instruction, they took
+            // 2000 cycles
+            const bool staged = !slow && m == kLC;
+            unsigned char* ot = sm + (PL::OWN ? PL::O_OFF : stage(c) + PL::V_OFF);
+            if (PL::OWN) {
+                if (!slow) mbar_arrive(bar(kEmptyV + (c & 1)));
+                if (c > 0 && !warp_wait(kStFree, (uint32_t)(c - 1) & 1u)) return false;
+            }
 #pragma unroll 1
-            for (int c0 = 0; c0 < kLDv; c0 += 32) {
-                float a[32], x[32];
-#pragma unroll
-                for (int e = 0; e < 32; e += 16) {
-                    tmem_ld16(lane_base + kO1Col + c0 + e, a + e);
-                    tmem_ld16(lane_base + kO2Col + c0 + e, x + e);
-                }
+            for (int c0 = kLHalf * hf; c0 < kLHalf * hf + kLHalf; c0 += 16) {
+                float a[16], x[16];
+                tmem_ld16(lane_base + kO1Col + c0, a);
+                tmem_ld16(lane_base + kO2Col + c0, x);
                 tmem_wait_ld();
                 if (slow) {
                     // 0 times an infinity of a later token must not reach this row: its own tokens alone, one by one
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) a[e] = 0.f;
+                    for (int e = 0; e < 16; ++e) a[e] = 0.f;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < kLC; j0 += 32) {
-                        float pp[16];  // 32 weights, two a word
-                        tmem_ld16(lane_base + kScCol + (uint32_t)(c & 1) * 128 + j0 / 2, pp);
+                    for (int jw = 0; jw < kLC / 2; ++jw) {  // two weights a word of P
+                        uint32_t pp;
+                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                                     : "=r"(pp)
+                                     : "r"(lane_base + kScCol + (uint32_t)(c & 1) * 128 + (jw < 32 ? jw : jw + 32)));
                         tmem_wait_ld();
 #pragma unroll 1
-                        for (int jj = 0; jj < 32; ++jj) {
-                            float wj = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (e == jj / 2) wj = (jj & 1) ? bf16x2_to_float2(__float_as_uint(pp[e])).y
-                                                               : bf16x2_to_float2(__float_as_uint(pp[e])).x;
-                            const int j = j0 + jj;
+                        for (int jj = 0; jj < 2; ++jj) {
+                            const int j = 2 * jw + jj;
+                            const float wj = __uint_as_float(jj ? pp & 0xffff0000u : pp << 16);
                             if (j > lt || j >= m) continue;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
+                            for (int e = 0; e < 16; e += 8) {
                                 const uint4 q4 =
                                     *reinterpret_cast<const uint4*>(sm + stage(c) + PL::V_OFF + sw128(kLC, j, (c0 + e) / 8));
                                 const uint32_t vw[4] = {q4.x, q4.y, q4.z, q4.w};
@@ -196,10 +370,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
                                 }
                             }
                         }
+                        __syncwarp();
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < 16; e += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
@@ -209,316 +384,218 @@ __global__ void __launch_bounds__(kLThreads, 1)
                                        make_float2(a[e + 2 * u], a[e + 2 * u + 1])));
                         w[u] = bf16x2_bits(y.x, y.y);
                     }
-                    if (lt < m && dv0 + c0 + e < p.DV)
+                    if (staged)
+                        *reinterpret_cast<uint4*>(ot + sw128(kLC, lt, (c0 + e) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    else if (lt < m && dv0 + c0 + e < p.DV)
                         *reinterpret_cast<uint4*>(dst + c0 + e) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             tc_fence_before();
             mbar_arrive(bar(kOFree));
-            mbar_arrive(bar(kEmpty + (c & 1)));
+            if (PL::OWN && slow) mbar_arrive(bar(kEmptyV + (c & 1)));
+            fence_proxy_async_smem();
+            mbar_arrive(bar(kStaged));
             return true;
         };
+        // V' of a chunk and o of the one before, whichever is there first
         bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
-            if (c > 0 && !write_o(c - 1)) {
-                ok = false;
-                break;
-            }
-            if (!warp_wait(kScFull, (uint32_t)c & 1u)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t sc = lane_base + kScCol + (uint32_t)(c & 1) * 128;
-#pragma unroll 1
-            for (int jb = 0; jb < 8; ++jb) {  // 16 columns at a time; P lies over scores that have been read
-                uint32_t w[8];
-                if (jb < 2 * warp + 2) {
-                    float s[16];
-                    tmem_ld16(sc + 16 * jb, s);
-                    tmem_wait_ld();
-                    if (jb < 2 * warp) {  // below the diagonal for every row of the warp
-                        const float f = pw[lt - (16 * jb + 15)];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 g2 = __fmul2_rn(make_float2(f, f), make_float2(r[15 - 2 * e], r[14 - 2 * e]));
-                            const float2 y = __fmul2_rn(g2, make_float2(s[2 * e], s[2 * e + 1]));
-                            w[e] = bf16x2_bits(y.x, y.y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int d = lt - (16 * jb + 2 * e);  // i - j of the first of the two
-                            const float y0 = d >= 0 ? s[2 * e] * pw[max(d, 0)] : 0.f;
-                            const float y1 = d >= 1 ? s[2 * e + 1] * pw[max(d - 1, 0)] : 0.f;
-                            w[e] = bf16x2_bits(y0, y1);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = 0u;
-                }
-                tmem_st8(sc + 8 * jb, w);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar(kPReady));
-        }
-        if (ok && nch > 0) write_o(nch - 1);
-    } else if (warp >= 4 && warp < 8) {
-        // ============ thread = token of the chunk (V'), then dk (the state) ============
-        const bool mine = lt < DK;
-        const int64_t row = ((int64_t)h * p.DV + dv0) * DK + lt;  // of [HV, DV, DK]: dv0's row, column dk
-        const int64_t slot_elems = (int64_t)p.HV * p.DV * DK;
-        float2 S[kLDv / 2];
-#pragma unroll
-        for (int e = 0; e < kLDv / 2; ++e) S[e] = make_float2(0.f, 0.f);
-        float* wsp = ws != nullptr ? ws + (int64_t)item * gridDim.y * (kLDv * DK) + lt : nullptr;
-        // pieces after the first start from the states that the first launch left; it also kept the initial state of a cut
-        // prompt, whose slot the prompt's last piece may have overwritten
-        const bool from_ws = !kState && cut;
-        if (mine) {
-            if (from_ws) {
-                const int np = blockIdx.y == 0 ? 0 : 1;
-                const float gp = (float)exp((double)piece * (double)ld);
-                for (int s = np; s <= (int)blockIdx.y; ++s) {
-                    const float* src = wsp + (int64_t)s * (kLDv * DK);
-                    const float f = s == np ? 0.f : gp;
-#pragma unroll
-                    for (int e = 0; e < kLDv / 2; ++e) {
-                        const float2 u = make_float2(src[(2 * e) * DK], src[(2 * e + 1) * DK]);
-                        S[e] = s == np ? u : __ffma2_rn(make_float2(f, f), S[e], u);
-                    }
-                }
-            } else if (init && blockIdx.y == 0) {
-                const StT* src = static_cast<const StT*>(p.pool) + (int64_t)slot * slot_elems + row;
-#pragma unroll
-                for (int e = 0; e < kLDv; ++e) {
-                    const float x = dv0 + e < p.DV ? to_f32(src[(int64_t)e * DK]) : 0.f;
-                    if (e & 1) S[e / 2].y = x; else S[e / 2].x = x;
-                }
-            }
-            if (kState && blockIdx.y == 0) {
-#pragma unroll
-                for (int e = 0; e < kLDv; ++e) wsp[e * DK] = (e & 1) ? S[e / 2].y : S[e / 2].x;
-            }
-        }
-        auto put_state = [&]() {  // S as hi and lo, rows dk
-            if (mine) {
-#pragma unroll
-                for (int c8 = 0; c8 < 8; ++c8) {
-                    uint32_t hw[4], lw[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        float2 x = S[4 * c8 + u];
-                        hw[u] = take_bf16(x);
-                        lw[u] = bf16x2_bits(x.x, x.y);
-                    }
-                    const uint32_t at = sw128(DK, lt, c8);
-                    *reinterpret_cast<uint4*>(sm + PL::SH_OFF + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                    *reinterpret_cast<uint4*>(sm + PL::SH_OFF + PL::SPART + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            mbar_arrive(bar(kSReady));
-        };
-        bool ok = true;
-        if (!kState && nch > 0) put_state();
         for (int c = 0; c < nch; ++c) {
-            ok = warp_wait(kFull + (c & 1), (uint32_t)(c >> 1) & 1u);
-            if (!ok) break;
             const int m = min(kLC, n - c * kLC);
+            const uint32_t parity = (uint32_t)(c >> 1) & 1u;
+            bool o_left = !kState && c > 0;
+            for (uint32_t polls = 0; polls < kLPolls; ++polls) {  // what has not come by then is waited for below
+                // V' lies where the last chunk's was, which the update has read then; of a partial chunk K's rows are cleared too
+                const bool there = mbar_test(bar(kVFull + (c & 1)), parity) && (c == 0 || mbar_test(bar(kUFull), (uint32_t)(c - 1) & 1u)) &&
+                                   (m == kLC || mbar_test(bar(kQkFull + (c & 1)), parity));
+                if (__all_sync(0xffffffffu, there)) break;
+                if (o_left && __all_sync(0xffffffffu, mbar_test(bar(kOFull), (uint32_t)(c - 1) & 1u))) {
+                    ok = write_o(c - 1);
+                    o_left = false;
+                    break;
+                }
+                __nanosleep(20);
+                if (__any_sync(0xffffffffu, *fail != 0)) {
+                    ok = false;
+                    break;
+                }
+            }
+            ok = ok && warp_wait(kVFull + (c & 1), parity) && (c == 0 || warp_wait(kUFull, (uint32_t)(c - 1) & 1u)) &&
+                 (m == kLC || warp_wait(kQkFull + (c & 1), parity));
+            if (!ok) break;
             unsigned char* vt = sm + stage(c) + PL::V_OFF;
             const bool real = lt < m;
             const float f = real ? pw[m - 1 - lt] : 0.f;
-            float2 third[NP == 3 ? kLDv / 2 : 1];
             float2 probe = make_float2(0.f, 0.f);
             if (!real) {  // rows behind the prompt's last token belong to others, or to nobody
 #pragma unroll
-                for (int c8 = 0; c8 < DK / 8; ++c8)
+                for (int c8 = hf * DK / 16; c8 < (hf + 1) * DK / 16; ++c8)
                     *reinterpret_cast<uint4*>(sm + stage(c) + PL::K_OFF + sw128(kLC, lt, c8)) = make_uint4(0, 0, 0, 0);
-            }
 #pragma unroll
-            for (int c8 = 0; c8 < 8; ++c8) {
+                for (int c8 = 4 * hf; c8 < 4 * hf + 4; ++c8) *reinterpret_cast<uint4*>(vt + sw128(kLC, lt, c8)) = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll 2
+            for (int c8 = 4 * hf; c8 < 4 * hf + 4; ++c8) {
                 const uint32_t at = sw128(kLC, lt, c8);
-                uint4 v4 = make_uint4(0, 0, 0, 0);
-                if (real)
-                    v4 = *reinterpret_cast<const uint4*>(vt + at);
-                else
-                    *reinterpret_cast<uint4*>(vt + at) = v4;
+                const uint4 v4 = *reinterpret_cast<const uint4*>(vt + at);
                 const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
-                uint32_t hw[4], lw[4];
+                uint32_t w[NP][4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const float2 v2 = bf16x2_to_float2(vw[u]);
                     probe = __ffma2_rn(v2, make_float2(0.f, 0.f), probe);  // 0 unless one is not finite
                     float2 x = __fmul2_rn(make_float2(f, f), v2);
-                    hw[u] = take_bf16(x);
-                    lw[u] = bf16x2_bits(x.x, x.y);
-                    if constexpr (NP == 3) {
-                        (void)take_bf16(x);
-                        third[4 * c8 + u] = x;
-                    }
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) w[e][u] = take_bf16(x);
                 }
-                *reinterpret_cast<uint4*>(sm + PL::VP_OFF + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                *reinterpret_cast<uint4*>(sm + PL::VP_OFF + PL::BOX + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+#pragma unroll
+                for (int e = 0; e < NP; ++e)
+                    *reinterpret_cast<uint4*>(sm + PL::VP_OFF + e * PL::BOX + at) =
+                        make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
             }
             if (!(probe.x == 0.f && probe.y == 0.f)) odd[c & 1] = c + 1;
             fence_proxy_async_smem();
-            tc_fence_before();
             mbar_arrive(bar(kVReady));
-            if constexpr (NP == 3) {
-                if (!kState) {
-                    ok = warp_wait(kIFull, (uint32_t)c & 1u);
-                    if (!ok) break;
-                }
-#pragma unroll
-                for (int c8 = 0; c8 < 8; ++c8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) w[u] = bf16x2_bits(third[4 * c8 + u].x, third[4 * c8 + u].y);
-                    *reinterpret_cast<uint4*>(sm + PL::SH_OFF + sw128(kLC, lt, c8)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(bar(kLReady));
-            }
-            ok = warp_wait(kUFull, (uint32_t)c & 1u);
-            if (!ok) break;
-            tc_fence_after();
-            const float gm = pw[m];
-#pragma unroll
-            for (int c0 = 0; c0 < kLDv; c0 += 16) {
-                float u[16];
-                tmem_ld16(lane_base + kUCol + c0, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    S[c0 / 2 + e] = __ffma2_rn(make_float2(gm, gm), S[c0 / 2 + e], make_float2(u[2 * e], u[2 * e + 1]));
-            }
-            tc_fence_before();
-            if (!kState && c + 1 < nch) put_state();
-        }
-        if (ok && mine) {
-            if constexpr (kState) {
-                float* dst = wsp + (int64_t)(blockIdx.y + 1) * (kLDv * DK);
-#pragma unroll
-                for (int e = 0; e < kLDv; ++e) dst[e * DK] = (e & 1) ? S[e / 2].y : S[e / 2].x;
-            } else if (last && out >= 0) {
-                StT* dst = static_cast<StT*>(p.pool) + (int64_t)out * slot_elems + row;
-#pragma unroll
-                for (int e = 0; e < kLDv; ++e) {
-                    const float x = (e & 1) ? S[e / 2].y : S[e / 2].x;
-                    if (dv0 + e < p.DV) {
-                        if constexpr (std::is_same<StT, float>::value)
-                            dst[(int64_t)e * DK] = x;
-                        else
-                            dst[(int64_t)e * DK] = __float2bfloat16_rn(x);
-                    }
-                }
+            if (o_left) {
+                ok = warp_wait(kOFull, (uint32_t)(c - 1) & 1u) && write_o(c - 1);
+                if (!ok) break;
             }
         }
-    } else if (tid == 256) {
+        if (!kState && ok && nch > 0 && warp_wait(kOFull, (uint32_t)(nch - 1) & 1u)) write_o(nch - 1);
+    } else if (tid == 3 * kLGroup) {
         // ============ tiles by TMA ============
-        constexpr uint32_t bytes = (kState ? PL::QK : 2 * PL::QK) + PL::BOX;
-        int issued = 0;
+        constexpr uint32_t bytes = kState ? PL::QK : 2 * PL::QK;
+        int qk = 0, v = 0;  // chunks asked for
         for (int c = 0; c < nch; ++c) {
-            if (c >= 2 && !wait(kEmpty + (c & 1), (uint32_t)((c - 2) >> 1) & 1u)) break;
+            const uint32_t st = base + stage(c), parity = (uint32_t)((c - 2) >> 1) & 1u;
+            if (c >= 2 && !wait(kEmptyQk + (c & 1), parity)) break;
 #ifdef GDN_TEST_MISSING_COPY
             // test build: the first chunk of the first item is never loaded nor arrived on: its wait runs out
             if (item == 0 && blockIdx.y == 0 && c == 0) break;
 #endif
-            const uint32_t full = bar(kFull + (c & 1)), st = base + stage(c);
-            mbar_arrive_expect_tx(full, bytes);
+            mbar_arrive_expect_tx(bar(kQkFull + (c & 1)), bytes);
 #pragma unroll
             for (int j = 0; j < DK / 64; ++j) {
-                tma_load_3d(st + PL::K_OFF + j * PL::BOX, &maps.k, 64 * j, hk, tok0 + c * kLC, full);
-                if (!kState) tma_load_3d(st + PL::Q_OFF + j * PL::BOX, &maps.q, 64 * j, hk, tok0 + c * kLC, full);
+                tma_load_3d(st + PL::K_OFF + j * PL::BOX, &maps.k, 64 * j, hk, tok0 + c * kLC, bar(kQkFull + (c & 1)));
+                if (!kState) tma_load_3d(st + PL::Q_OFF + j * PL::BOX, &maps.q, 64 * j, hk, tok0 + c * kLC, bar(kQkFull + (c & 1)));
             }
-            tma_load_3d(st + PL::V_OFF, &maps.v, dv0, h, tok0 + c * kLC, full);
-            issued = c + 1;
+            qk = c + 1;
+            if (c >= 2 && !wait(kEmptyV + (c & 1), parity)) break;
+            mbar_arrive_expect_tx(bar(kVFull + (c & 1)), PL::BOX);
+            tma_load_3d(st + PL::V_OFF, &maps.v, dv0, h, tok0 + c * kLC, bar(kVFull + (c & 1)));
+            v = c + 1;
         }
-        for (int c = max(0, issued - 2); c < issued; ++c)  // copies in flight land before the CTA leaves
-            mbar_wait_bounded(bar(kFull + (c & 1)), (uint32_t)(c >> 1) & 1u, kLPolls);
-    } else if (tid == 288) {
+        // copies in flight land before the CTA leaves
+        for (int c = max(0, qk - 2); c < qk; ++c) mbar_wait_bounded(bar(kQkFull + (c & 1)), (uint32_t)(c >> 1) & 1u, kLPolls);
+        for (int c = max(0, v - 2); c < v; ++c) mbar_wait_bounded(bar(kVFull + (c & 1)), (uint32_t)(c >> 1) & 1u, kLPolls);
+    } else if (warp == 25) {
         // ============ products ============
-        bool any = false;
-        auto scores = [&](int c) -> bool {
-            if (!wait(kFull + (c & 1), (uint32_t)(c >> 1) & 1u)) return false;
-            // the rows behind the last token are cleared first
-            if (n - c * kLC < kLC && !wait(kVReady, (uint32_t)c & 1u)) return false;
-            tc_fence_after();
-            const uint32_t st = base + stage(c);
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
-                const uint32_t off = (uint32_t)(ks >> 2) * PL::BOX + (uint32_t)(ks & 3) * 32u;
-                umma_bf16(tmem + kScCol + (uint32_t)(c & 1) * 128, umma_desc_sw128(st + PL::Q_OFF + off),
-                          umma_desc_sw128(st + PL::K_OFF + off), umma_idesc_bf16(kLC, kLC), ks > 0 ? 1u : 0u);
-            }
-            umma_commit(bar(kScFull));
-            any = true;
-            return true;
-        };
+        // The whole warp runs this code, so that descriptors stay in registers of the warp (from code of a single thread a product
+        // took 100 cycles to issue, where it runs 32 to 64), and waits for up to three barriers at once, a lane for each.
+        bool any = false, ok = true;
+        const bool lead = elect_one();
+        const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
         constexpr uint32_t kBn = 1u << 16, kAm = 1u << 15;  // B N-major, A M-major
         constexpr uint32_t id64 = umma_idesc_bf16(128, kLDv);
-        bool ok = true;
-        if (!kState && nch > 0) ok = scores(0);
-        for (int c = 0; c < nch && ok; ++c) {
-            const uint32_t st = base + stage(c);
-            if constexpr (!kState) {
-                ok = wait(kSReady, (uint32_t)c & 1u) && (c == 0 || wait(kOFree, (uint32_t)(c - 1) & 1u));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int ks = 0; ks < DK / 16; ++ks) {
-                        const uint32_t off = (uint32_t)(ks >> 2) * PL::BOX + (uint32_t)(ks & 3) * 32u;
-                        umma_bf16(tmem + kO2Col, umma_desc_sw128(st + PL::Q_OFF + off),
-                                  umma_desc_sw128_mn(base + PL::SH_OFF + part * PL::SPART + ks * 2048u, PL::BOX), id64 | kBn,
-                                  part + ks > 0 ? 1u : 0u);
-                    }
-                umma_commit(bar(kIFull));
-            }
-            if (!wait(kVReady, (uint32_t)c & 1u) || (kState && !wait(kFull + (c & 1), (uint32_t)(c >> 1) & 1u))) {
-                ok = false;
-                break;
-            }
+        const int ln = tid & 31;
+        auto all_over = [&](int b0, int c0, int b1, int c1, int b2, int c2) -> bool {  // phase c of barrier b, c < 0: none
+            const int b = ln == 0 ? b0 : ln == 1 ? b1 : b2, c = ln == 0 ? c0 : ln == 1 ? c1 : c2;
+            return __all_sync(0xffffffffu, c < 0 || wait(b, (uint32_t)c & 1u));
+        };
+        auto scores = [&](int c) {
             tc_fence_after();
-#pragma unroll
-            for (int part = 0; part < NP; ++part) {
-                if (part == 2) {
-                    ok = wait(kLReady, (uint32_t)c & 1u);
-                    if (!ok) break;
+            const uint32_t st = base + stage(c);
+            if (lead) {
+#pragma unroll 2
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    const uint32_t off = (uint32_t)(ks >> 2) * PL::BOX + (uint32_t)(ks & 3) * 32u;
+                    umma_bf16(tm + kScCol + (uint32_t)(c & 1) * 128, umma_desc_sw128(st + PL::Q_OFF + off),
+                              umma_desc_sw128(st + PL::K_OFF + off), umma_idesc_bf16(kLC, kLC), ks > 0 ? 1u : 0u);
                 }
-                const uint32_t vp = base + (part < 2 ? PL::VP_OFF + part * PL::BOX : PL::SH_OFF);
-#pragma unroll
-                for (int ks = 0; ks < kLC / 16; ++ks)
-                    umma_bf16(tmem + kUCol, umma_desc_sw128_mn(st + PL::K_OFF + ks * 2048u, PL::BOX),
-                              umma_desc_sw128_mn(vp + ks * 2048u, PL::BOX), id64 | kBn | kAm, part + ks > 0 ? 1u : 0u);
+                umma_commit(bar(kScFull + (c & 1)));
             }
             any = true;
+        };
+        // a last, partial chunk's scores wait for its rows to be cleared
+        auto whole = [&](int c) { return n - c * kLC >= kLC; };
+        if (!kState && nch > 0) {
+            ok = all_over(kQkFull, 0, kVReady, whole(0) ? -1 : 0, 0, -1);
+            if (ok) scores(0);
+        }
+        for (int c = 0; c < nch && ok; ++c) {
+            const uint32_t st = base + stage(c);
+            // U: K^T V'.  The state waits for it alone.
+            ok = all_over(kVReady, c, kUFree, c - 1, kQkFull + (c & 1), c >> 1);
             if (!ok) break;
-            umma_commit(bar(kUFull));
-            if constexpr (kState) {
-                umma_commit(bar(kEmpty + (c & 1)));
-            } else {
-                ok = wait(kPReady, (uint32_t)c & 1u);
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+                for (int part = 0; part < NP; ++part)
+#pragma unroll 2
+                    for (int ks = 0; ks < kLC / 16; ++ks)
+                        umma_bf16(tm + kUCol, umma_desc_sw128_mn(st + PL::K_OFF + ks * 2048u, PL::BOX),
+                                  umma_desc_sw128_mn(base + PL::VP_OFF + part * PL::BOX + ks * 2048u, PL::BOX),
+                                  id64 | kBn | kAm, part + ks > 0 ? 1u : 0u);
+                umma_commit(bar(kUFull));
+                if (kState) {
+                    umma_commit(bar(kEmptyQk + (c & 1)));
+                    umma_commit(bar(kEmptyV + (c & 1)));
+                }
+            }
+            any = true;
+            if constexpr (!kState) {
+                ok = all_over(kSReady, c, kOFree, c - 1, 0, -1);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < kLC / 16; ++ks)
-                    umma_bf16_ta(tmem + kO1Col, tmem + kScCol + (uint32_t)(c & 1) * 128 + 8 * ks,
-                                 umma_desc_sw128_mn(st + PL::V_OFF + ks * 2048u, PL::BOX), id64 | kBn, ks > 0 ? 1u : 0u);
-                umma_commit(bar(kOFull));
-                umma_commit(bar(kEmpty + (c & 1)));
-                if (c + 1 < nch) ok = scores(c + 1);
+                if (lead) {
+#pragma unroll 2
+                    for (int ks = 0; ks < DK / 16; ++ks) {
+                        const uint32_t off = (uint32_t)(ks >> 2) * PL::BOX + (uint32_t)(ks & 3) * 32u;
+                        umma_bf16(tm + kO2Col, umma_desc_sw128(st + PL::Q_OFF + off),
+                                  umma_desc_sw128_mn(base + PL::SH_OFF + ks * 2048u, PL::BOX), id64 | kBn, ks > 0 ? 1u : 0u);
+                    }
+                    umma_commit(bar(kIFull));
+                    umma_commit(bar(kEmptyQk + (c & 1)));  // scores, update and inter products have read K and Q
+                }
+                // the next scores go over the P that the last chunk's intra product has read; they come first where their
+                // tiles are there, else the intra product does not wait for them
+                const int nx = c + 1;
+                bool late = nx < nch;
+                if (late && whole(nx) && __all_sync(0xffffffffu, mbar_test(bar(kQkFull + (nx & 1)), (uint32_t)(nx >> 1) & 1u))) {
+                    scores(nx);
+                    late = false;
+                }
+                ok = all_over(kPReady + (c & 1), c >> 1, 0, -1, 0, -1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll 2
+                    for (int ks = 0; ks < kLC / 16; ++ks)
+                        umma_bf16_ta(tm + kO1Col, tm + kScCol + (uint32_t)(c & 1) * 128 + (ks < 4 ? 8 * ks : 32 + 8 * ks),
+                                     umma_desc_sw128_mn(st + PL::V_OFF + ks * 2048u, PL::BOX), id64 | kBn, ks > 0 ? 1u : 0u);
+                    umma_commit(bar(kOFull));
+                }
+                if (late) {
+                    ok = all_over(kQkFull + (nx & 1), nx >> 1, kVReady, whole(nx) ? -1 : nx, 0, -1);
+                    if (ok) scores(nx);
+                }
             }
         }
         if (any) {  // every product is complete before the tensor memory is released
-            umma_commit(bar(kDrain));
+            if (lead) umma_commit(bar(kDrain));
             mbar_wait_bounded(bar(kDrain), 0u, kLPolls);
         }
+    } else if (tid == 3 * kLGroup + 64 && !kState) {
+        // ============ o out ============
+        for (int c = 0; c < nch; ++c) {
+            if (!wait(kStaged, (uint32_t)c & 1u)) break;
+            if (n - c * kLC >= kLC && odd[c & 1] != c + 1) {
+                tma_store_3d(&maps.o, dv0, h, tok0 + c * kLC, base + (PL::OWN ? PL::O_OFF : stage(c) + PL::V_OFF));
+                bulk_commit_group();
+                bulk_wait_read_all();
+            }
+            mbar_arrive(bar(PL::OWN ? kStFree : kEmptyV + (c & 1)));
+        }
+        bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -563,7 +640,7 @@ bool encode_rows(CUtensorMap* map, const void* ptr, int cols, int heads, int n) 
 
 template <int DK, typename StT, bool kState>
 cudaError_t launch_one(const LinearParams& p, const LinearMaps& m, int piece, int pieces, float* ws, cudaStream_t s) {
-    using PL = LinearPlan<DK>;
+    using PL = LinearPlan<DK, std::is_same<StT, float>::value ? 3 : 2>;
     auto kernel = gdn_linear_prefill_kernel<DK, StT, kState>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -607,7 +684,7 @@ bool launch_linear_prefill(const LinearParams& p, bool qkv_bf16, bool state_bf16
     LinearMaps m;
     std::memset(&m, 0, sizeof m);
     if (!encode_rows(&m.q, p.q, p.DK, p.HK, p.N) || !encode_rows(&m.k, p.k, p.DK, p.HK, p.N) ||
-        !encode_rows(&m.v, p.v, p.DV, p.HV, p.N))
+        !encode_rows(&m.v, p.v, p.DV, p.HV, p.N) || !encode_rows(&m.o, p.o, p.DV, p.HV, p.N))
         return false;
     if (p.DK == 64)
         err = state_bf16 ? launch_dk<64, __nv_bfloat16>(p, m, ws, s) : launch_dk<64, float>(p, m, ws, s);
