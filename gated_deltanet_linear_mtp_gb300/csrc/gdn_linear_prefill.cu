@@ -18,7 +18,7 @@
 //
 // Three groups of eight warps: the first forms P from the scores (thread = row i and a half of the columns), the second keeps the
 // state (thread = dk and 32 dv), the third forms V' from V (thread = token and 32 dv) and takes o from the products (thread = row i and 32 dv); warp 24
-// brings the tiles by TMA (two stages), 25 issues the products, 26 stores o by TMA from where V was.  A group's work on a chunk is a few hundred dependent
+// brings the tiles by TMA (two stages), 25 issues the products, 26 stores o by TMA, 27 says when V has been read.  A group's work on a chunk is a few hundred dependent
 // instructions, at which one warp issues every sixth cycle or so: eight warps a group take half the time of four.  For the same
 // reason code is kept short (unrolled to 95 KB, the warps waited for instructions).  The only serial chain between chunks is
 // state -> inter -> state and V' -> update -> state; the scores of the next chunk and the intra product fill the tensor cores.
@@ -38,13 +38,13 @@ namespace {
 constexpr int kLC = 128;   // tokens of a chunk
 constexpr int kLDv = 64;   // value dimensions of a CTA
 constexpr int kLGroup = 256;                 // threads of a group
-constexpr int kLThreads = 3 * kLGroup + 96;
+constexpr int kLThreads = 3 * kLGroup + 128;
 constexpr int kLHalf = kLDv / 2;              // value dimensions of a thread
 constexpr uint32_t kLPolls = GDN_WAIT_POLLS;
 
 // barriers (the first ones: one for each of two stages or score buffers); a stage's K and Q are free before its V
-enum { kQkFull = 0, kVFull = 2, kEmptyQk = 4, kEmptyV = 6, kScFull = 8, kIFull = 10, kUFull, kOFull, kStFree, kDrain, kPReady, kVReady = kPReady + 2, kUFree, kSReady, kOFree,
-       kStaged, kNumLBars };
+enum { kQkFull = 0, kVFull = 2, kEmptyQk = 4, kEmptyV = 6, kScFull = 8, kIFull = 10, kUFull, kOFull, kStFree, kDrain, kPReady, kVReady = kPReady + 2, kStaged = kVReady + 2, kUFree = kStaged + 2,
+       kSReady, kOFree, kNumLBars };
 // tensor memory: scores (P over them) of two chunks, intra, inter, update
 constexpr uint32_t kScCol = 0, kO1Col = 256, kO2Col = 320, kUCol = 384, kLCols = 512;
 
@@ -158,16 +158,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
 
     if (warp == 0) tmem_alloc(smem_u32(tmem_slot), kLCols);
     if (tid == 32) {
-        for (int i = kQkFull; i < kPReady; ++i)
-            if (!(PL::OWN && !kState) || (i & ~1) != kEmptyV) mbar_init(bar(i), 1);         // arrivals of copies and products
-        if (PL::OWN && !kState)
-            for (int i = 0; i < 2; ++i) mbar_init(bar(kEmptyV + i), kLGroup);  // of the group that reads V last
+        for (int i = kQkFull; i < kPReady; ++i) mbar_init(bar(i), PL::OWN && !kState && (i & ~1) == kEmptyV ? 2 : 1);         // arrivals of copies and products
         for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), kLGroup);  // of a group of threads
         fence_mbar_init();
         fail[0] = odd[0] = odd[1] = 0;
     }
     if (tid < 32) pw[tid - 32] = 0.f;
-    if (tid < kLC + 1) pw[tid] = tid == 0 ? 1.f : (float)exp((double)tid * (double)ld);
+    if (tid < kLC + 1) pw[tid] = tid == 0 ? 1.f : expf((float)tid * ld);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -241,7 +238,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (mine) {
             if (from_ws) {
                 const int np = blockIdx.y == 0 ? 0 : 1;
-                const float gp = (float)exp((double)piece * (double)ld);
+                const float gp = expf((float)piece * ld);
                 for (int s = np; s <= (int)blockIdx.y; ++s) {
                     const float* src = wsp + (int64_t)s * (kLDv * DK);
 #pragma unroll
@@ -331,10 +328,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             // 2000 cycles
             const bool staged = !slow && m == kLC;
             unsigned char* ot = sm + (PL::OWN ? PL::O_OFF : stage(c) + PL::V_OFF);
-            if (PL::OWN) {
-                if (!slow) mbar_arrive(bar(kEmptyV + (c & 1)));
-                if (c > 0 && !warp_wait(kStFree, (uint32_t)(c - 1) & 1u)) return false;
-            }
+            if (PL::OWN && c > 0 && !warp_wait(kStFree, (uint32_t)(c - 1) & 1u)) return false;
 #pragma unroll 1
             for (int c0 = kLHalf * hf; c0 < kLHalf * hf + kLHalf; c0 += 16) {
                 float a[16], x[16];
@@ -392,9 +386,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
             }
             tc_fence_before();
             mbar_arrive(bar(kOFree));
-            if (PL::OWN && slow) mbar_arrive(bar(kEmptyV + (c & 1)));
             fence_proxy_async_smem();
-            mbar_arrive(bar(kStaged));
+            mbar_arrive(bar(kStaged + (c & 1)));
             return true;
         };
         // V' of a chunk and o of the one before, whichever is there first
@@ -454,7 +447,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             }
             if (!(probe.x == 0.f && probe.y == 0.f)) odd[c & 1] = c + 1;
             fence_proxy_async_smem();
-            mbar_arrive(bar(kVReady));
+            mbar_arrive(bar(kVReady + (c & 1)));
             if (o_left) {
                 ok = warp_wait(kOFull, (uint32_t)(c - 1) & 1u) && write_o(c - 1);
                 if (!ok) break;
@@ -524,7 +517,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         for (int c = 0; c < nch && ok; ++c) {
             const uint32_t st = base + stage(c);
             // U: K^T V'.  The state waits for it alone.
-            ok = all_over(kVReady, c, kUFree, c - 1, kQkFull + (c & 1), c >> 1);
+            ok = all_over(kVReady + (c & 1), c >> 1, kUFree, c - 1, kQkFull + (c & 1), c >> 1);
             if (!ok) break;
             tc_fence_after();
             if (lead) {
@@ -556,11 +549,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     umma_commit(bar(kIFull));
                     umma_commit(bar(kEmptyQk + (c & 1)));  // scores, update and inter products have read K and Q
                 }
-                // the next scores go over the P that the last chunk's intra product has read; they come first where their
-                // tiles are there, else the intra product does not wait for them
+                // The intra product and the next scores, which go over the P that the last chunk's intra product has read: in
+                // this order where P is there (V is free for the next load earlier), else the scores first if their tiles are
                 const int nx = c + 1;
                 bool late = nx < nch;
-                if (late && whole(nx) && __all_sync(0xffffffffu, mbar_test(bar(kQkFull + (nx & 1)), (uint32_t)(nx >> 1) & 1u))) {
+                if (late && whole(nx) && !__all_sync(0xffffffffu, mbar_test(bar(kPReady + (c & 1)), (uint32_t)(c >> 1) & 1u)) &&
+                    __all_sync(0xffffffffu, mbar_test(bar(kQkFull + (nx & 1)), (uint32_t)(nx >> 1) & 1u))) {
                     scores(nx);
                     late = false;
                 }
@@ -573,9 +567,10 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         umma_bf16_ta(tm + kO1Col, tm + kScCol + (uint32_t)(c & 1) * 128 + (ks < 4 ? 8 * ks : 32 + 8 * ks),
                                      umma_desc_sw128_mn(st + PL::V_OFF + ks * 2048u, PL::BOX), id64 | kBn, ks > 0 ? 1u : 0u);
                     umma_commit(bar(kOFull));
+                    if (PL::OWN) umma_commit(bar(kEmptyV + (c & 1)));
                 }
                 if (late) {
-                    ok = all_over(kQkFull + (nx & 1), nx >> 1, kVReady, whole(nx) ? -1 : nx, 0, -1);
+                    ok = all_over(kQkFull + (nx & 1), nx >> 1, kVReady + (nx & 1), whole(nx) ? -1 : nx >> 1, 0, -1);
                     if (ok) scores(nx);
                 }
             }
@@ -587,7 +582,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     } else if (tid == 3 * kLGroup + 64 && !kState) {
         // ============ o out ============
         for (int c = 0; c < nch; ++c) {
-            if (!wait(kStaged, (uint32_t)c & 1u)) break;
+            if (!wait(kStaged + (c & 1), (uint32_t)(c >> 1) & 1u)) break;
             if (n - c * kLC >= kLC && odd[c & 1] != c + 1) {
                 tma_store_3d(&maps.o, dv0, h, tok0 + c * kLC, base + (PL::OWN ? PL::O_OFF : stage(c) + PL::V_OFF));
                 bulk_commit_group();
@@ -596,6 +591,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
             mbar_arrive(bar(PL::OWN ? kStFree : kEmptyV + (c & 1)));
         }
         bulk_wait_all();
+    } else if (tid == 3 * kLGroup + 96 && PL::OWN && !kState) {
+        // ============ V read: by V' and the intra product (which arrives by itself), and where it is not finite once more ============
+        for (int c = 0; c < nch; ++c) {
+            const uint32_t parity = (uint32_t)(c >> 1) & 1u;
+            if (!wait(kVReady + (c & 1), parity) || (odd[c & 1] == c + 1 && !wait(kStaged + (c & 1), parity))) break;
+            mbar_arrive(bar(kEmptyV + (c & 1)));
+        }
     }
     tc_fence_before();
     __syncthreads();
