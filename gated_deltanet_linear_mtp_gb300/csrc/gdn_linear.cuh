@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(Split<DK>::THREADS, Split<DK>::MIN_CTAS_PER_SM
     };
 
     bool unpacked = false;
-    for (int c0 = 0; c0 < n; c0 += CT) {
-        const int m = min(CT, n - c0);
+    for (unsigned c0 = 0; c0 < (unsigned)n; c0 += CT) {  // unsigned: n may be near 2^31
+        const int m = min(CT, n - (int)c0);
         if (c0 > 0) __syncthreads();  // the last chunk's tokens are no longer read
         // tokens into shared memory: P threads a q or k row
         for (int j = tid / P; j < m; j += NT / P) {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(Split<DK>::THREADS, Split<DK>::MIN_CTAS_PER_SM
                     store_o(c0 + t, x);
                 }
             }
-            if (out >= 0 || c0 + CT < n) {
+            if (out >= 0 || c0 + CT < (unsigned)n) {
                 const float gm = pw[m];
 #pragma unroll
                 for (int i = 0; i < RL; ++i)

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const bool last = first + n == all, cut = n < all;
     if (kState && last) return;  // nothing starts behind it
     if (all == 0 && (out < 0 || out == slot)) return;
-    const int nch = (n + kLC - 1) / kLC;
+    const int nch = n / kLC + (n % kLC != 0);
     const int tok0 = lo + first;
 
     extern __shared__ unsigned char smem_raw[];
@@ -622,9 +622,9 @@ int linear_split(int B, int N, int HV, int DV) {
     if (items == 0 || N == 0) return 0;
     const int64_t times = linear_sms() / items;  // pieces that fill the GPU once
     if (times < 2) return 0;
-    const int64_t chunks = ((int64_t)N / B + kLC - 1) / kLC;
+    const int64_t chunks = (N / B + (int64_t)kLC - 1) / kLC;
     const int64_t per = (chunks + times - 1) / times > 4 ? (chunks + times - 1) / times : 4;
-    if (2 * per > chunks) return 0;
+    if (3 * per > 2 * chunks) return 0;  // prompts of less than a piece and a half on average
     return (int)(per * kLC);
 }
 
@@ -661,7 +661,7 @@ cudaError_t launch_one(const LinearParams& p, const LinearMaps& m, int piece, in
 template <int DK, typename StT>
 cudaError_t launch_dk(const LinearParams& p, const LinearMaps& m, float* ws, cudaStream_t s) {
     const int piece = linear_split(p.B, p.N, p.HV, p.DV);
-    const int pieces = piece > 0 ? (p.N + piece - 1) / piece : 1;
+    const int pieces = piece > 0 ? (int)(((int64_t)p.N + piece - 1) / piece) : 1;
     if (pieces > 1) {
         const cudaError_t e = launch_one<DK, StT, true>(p, m, piece, pieces, ws, s);
         if (e != cudaSuccess) return e;
@@ -675,7 +675,7 @@ int64_t linear_prefill_workspace(int B, int N, int HV, int DK, int DV) {
     if (DK != 64 && DK != 128) return 0;
     const int piece = linear_split(B, N, HV, DV);
     if (piece == 0) return 0;
-    return (int64_t)((N + piece - 1) / piece) * B * HV * ((DV + kLDv - 1) / kLDv) * kLDv * DK * 4;
+    return ((int64_t)N + piece - 1) / piece * B * HV * ((DV + kLDv - 1) / kLDv) * kLDv * DK * 4;
 }
 
 bool launch_linear_prefill(const LinearParams& p, bool qkv_bf16, bool state_bf16, float* ws, cudaStream_t s, cudaError_t& err) {
