@@ -36,21 +36,21 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
     return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
 
-// r = max(p - q, 0) of one token as an exact pair; values that are not finite count as nothing
-__device__ __forceinline__ float2 residual(float p, float q, bool& bad) {
-    if (!(fabsf(p) <= FLT_MAX) || !(fabsf(q) <= FLT_MAX)) {
-        bad = true;
-        return make_float2(0.f, 0.f);
-    }
-    return p > q ? two_sum(p, -q) : make_float2(0.f, 0.f);
+// r = max(p - q, 0) of one token as an exact pair.  kChecked: values that are not finite count as nothing.
+template <bool kChecked>
+__device__ __forceinline__ float2 residual(float p, float q) {
+    if (kChecked && (!(fabsf(p) <= FLT_MAX) || !(fabsf(q) <= FLT_MAX))) return make_float2(0.f, 0.f);
+    const float s = p - q;
+    const float2 r = make_float2(s, (p - s) - q);  // exact, since |p| >= |q|
+    return p > q ? r : make_float2(0.f, 0.f);
 }
 
 struct RowPair {
     const float* p;
     const float* q;  // nullptr: q is 1 at `certain` and 0 elsewhere
     int certain;     // -1: nowhere
-    __device__ __forceinline__ float2 at(int v, bool& bad) const {
-        return residual(p[v], q != nullptr ? q[v] : (v == certain ? 1.f : 0.f), bad);
+    __device__ __forceinline__ float2 at(int v) const {
+        return residual<true>(p[v], q != nullptr ? q[v] : (v == certain ? 1.f : 0.f));
     }
 };
 
@@ -131,21 +131,46 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
     const int tiles = (V + tile - 1) / tile, first = rank * per, mine = max(0, min(per, tiles - first));
     bool bad = false;
     double before = 0., total = 0., own = 0.;  // sums of the CTAs before this one, of all, of this one
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int k = warp; k < mine; k += kAcceptWarps) {
-            float2 acc = make_float2(0.f, 0.f);
-            const int end = min(V, (first + k + 1) * tile);
-            for (int v0 = (first + k) * tile; v0 < end; v0 += kAcceptBlock) {
-                float pv[8], qv[8];  // all loads before any arithmetic
+    // tile k's sum; false where a value is not finite (kChecked: never)
+    auto tile_sum = [&](auto checked, int k, float2& acc) -> bool {
+        constexpr bool kChecked = sizeof(checked) > 1;
+        acc = make_float2(0.f, 0.f);
+        float2 probe = make_float2(0.f, 0.f);
+        const int end = min(V, (first + k + 1) * tile);
+        float pv[8], qv[8];  // the next block's loads are in flight meanwhile
+        auto load = [&](int v0, float (&pb)[8], float (&qb)[8]) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int v = v0 + 32 * i + lane;
-                    pv[i] = v < end ? r.p[v] : 0.f;
-                    qv[i] = r.q != nullptr && v < end ? r.q[v] : 0.f;
-                }
+            for (int i = 0; i < 8; ++i) {
+                const int v = v0 + 32 * i + lane;
+                pb[i] = v < end ? r.p[v] : 0.f;
+                qb[i] = r.q != nullptr && v < end ? r.q[v] : 0.f;
+            }
+        };
+        int v0 = (first + k) * tile;
+        load(v0, pv, qv);
+        for (; v0 < end; v0 += kAcceptBlock) {
+            float pc[8], qc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pc[i] = pv[i], qc[i] = qv[i];
+            if (v0 + kAcceptBlock < end) load(v0 + kAcceptBlock, pv, qv);
+            if (r.certain >= v0 && r.certain < v0 + kAcceptBlock)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    add_pair(acc, residual(pv[i], v0 + 32 * i + lane == r.certain ? 1.f : qv[i], bad));
+                    if (v0 + 32 * i + lane == r.certain) qc[i] = 1.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!kChecked) probe = __ffma2_rn(make_float2(pc[i], qc[i]), make_float2(0.f, 0.f), probe);
+                add_pair(acc, residual<kChecked>(pc[i], qc[i]));
+            }
+        }
+        return kChecked || (probe.x == 0.f && probe.y == 0.f);
+    };
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int k = warp; k < mine; k += kAcceptWarps) {
+            float2 acc;
+            if (!__all_sync(0xffffffffu, tile_sum(char{}, k, acc))) {
+                bad = true;
+                tile_sum(int{}, k, acc);
             }
 #pragma unroll
             for (int m = 16; m >= 1; m >>= 1)
@@ -219,14 +244,13 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
         }
         if (found < 0) past = true;
         const int k = first + (past ? last : found), end = min(V, (k + 1) * tile);
-        bool dummy = false;
         for (int v0 = k * tile; v0 < end; v0 += kAcceptBlock) {  // 8 neighbours a lane
             float2 x[8];
             double s = 0.;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int v = v0 + 8 * lane + i;
-                x[i] = v < end ? r.at(v, dummy) : make_float2(0.f, 0.f);
+                x[i] = v < end ? r.at(v) : make_float2(0.f, 0.f);
                 s += (double)x[i].x + (double)x[i].y;
             }
             double upto = before + scan(s, lane) - s;
@@ -259,12 +283,14 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
 }  // namespace
 
 cudaError_t launch_draft_accept(const DraftAcceptParams& p, cudaStream_t s) {
-    // CTAs a lane: at least 4 blocks a warp while there are lanes enough, fewer where there are not
+    // CTAs a lane: parts of up to 65536 tokens where lanes fill the GPU (256 lanes of 131072: 2 CTAs 62 us, 4 66, 8 78, 1 100; a CTA's start
+    // and the search cost some microseconds), of 2048 where they do not (one lane of 131072: 8 CTAs 15 us, 4 19, 2 27)
     int ncta = 1;
-    while (ncta < kAcceptMaxCluster &&
-           (int64_t)p.V > (int64_t)ncta * kAcceptBlock * kAcceptWarps * ((int64_t)p.B * ncta < 608 ? 1 : 4))
-        ncta *= 2;
+    while (ncta < kAcceptMaxCluster && ((int64_t)p.V > (int64_t)ncta * 65536 || ((int64_t)p.B * ncta < 456 && p.V > ncta * 2048))) ncta *= 2;
+    // tiles of two blocks where a warp has at least four of them: the warp's sum is formed once a tile (512 against 256: 62 and 69 us,
+    // 15 and 17 for the one lane), of one where it has fewer (one lane of 50001: 13 against 15)
     int tile = kAcceptBlock;
+    if ((int64_t)p.V > (int64_t)tile * kAcceptWarps * ncta * 4) tile *= 2;
     while ((int64_t)tile * kAcceptTiles * ncta < p.V) tile *= 2;
     const int tiles = (p.V + tile - 1) / tile, per = (tiles + ncta - 1) / ncta;
     cudaLaunchConfig_t cfg = {};
