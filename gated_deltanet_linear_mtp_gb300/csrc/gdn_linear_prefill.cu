@@ -43,8 +43,8 @@ constexpr int kLHalf = kLDv / 2;              // value dimensions of a thread
 constexpr uint32_t kLPolls = GDN_WAIT_POLLS;
 
 // barriers (the first ones: one for each of two stages or score buffers); a stage's K and Q are free before its V
-enum { kQkFull = 0, kVFull = 2, kEmptyQk = 4, kEmptyV = 6, kScFull = 8, kIFull = 10, kUFull, kOFull, kStFree, kDrain, kPReady, kVReady = kPReady + 2, kStaged = kVReady + 2, kUFree = kStaged + 2,
-       kSReady, kOFree, kNumLBars };
+enum { kQkFull = 0, kVFull = 2, kEmptyQk = 4, kEmptyV = 6, kScFull = 8, kIFull = 10, kUFull, kOFull = kUFull + 2, kStFree, kDrain, kPReady, kVReady = kPReady + 2, kStaged = kVReady + 2, kUFree = kStaged + 2,
+       kSReady = kUFree + 2, kOFree, kNumLBars };
 // tensor memory: scores (P over them) of two chunks, intra, inter, update
 constexpr uint32_t kScCol = 0, kO1Col = 256, kO2Col = 320, kUCol = 384, kLCols = 512;
 
@@ -63,6 +63,11 @@ struct LinearPlan {
     static constexpr uint32_t END = BAR_OFF + 8 * kNumLBars + 32;
     static constexpr uint32_t BYTES = END + 1024;          // the base is aligned to 1024
     static_assert(BYTES <= 232448, "fits one SM");
+    // The first launch of cut prompts has no queries and no o: the parts of V' of odd chunks lie there, so that one chunk's V' is formed
+    // beside the last one's update.
+    static constexpr __host__ __device__ uint32_t vp(bool odd, int e) {
+        return !odd ? VP_OFF + e * BOX : DK == 128 ? (e < 2 ? Q_OFF + e * BOX : STAGE + Q_OFF) : e < 2 ? Q_OFF + e * STAGE : O_OFF;
+    }
 };
 
 struct LinearMaps {
@@ -156,12 +161,33 @@ __global__ void __launch_bounds__(kLThreads, 1)
     volatile int* odd = fail + 1;  // [2]: c + 1 where V of chunk c (by its parity) holds an infinity or NaN
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + PL::BAR_OFF + 8 * kNumLBars + 16);
 
+    auto stage = [&](int c) -> uint32_t { return (uint32_t)(c & 1) * PL::STAGE; };
+    auto load_qk = [&](int c) {
+        const uint32_t st = base + stage(c), full = bar(kQkFull + (c & 1));
+        mbar_arrive_expect_tx(full, kState ? PL::QK : 2 * PL::QK);
+#pragma unroll
+        for (int j = 0; j < DK / 64; ++j) {
+            tma_load_3d(st + PL::K_OFF + j * PL::BOX, &maps.k, 64 * j, hk, tok0 + c * kLC, full);
+            if (!kState) tma_load_3d(st + PL::Q_OFF + j * PL::BOX, &maps.q, 64 * j, hk, tok0 + c * kLC, full);
+        }
+    };
+    auto load_v = [&](int c) {
+        mbar_arrive_expect_tx(bar(kVFull + (c & 1)), PL::BOX);
+        tma_load_3d(base + stage(c) + PL::V_OFF, &maps.v, dv0, h, tok0 + c * kLC, bar(kVFull + (c & 1)));
+    };
     if (warp == 0) tmem_alloc(smem_u32(tmem_slot), kLCols);
-    if (tid == 32) {
-        for (int i = kQkFull; i < kPReady; ++i) mbar_init(bar(i), PL::OWN && !kState && (i & ~1) == kEmptyV ? 2 : 1);         // arrivals of copies and products
-        for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), kLGroup);  // of a group of threads
+    if (tid == 3 * kLGroup) {
+        // V is read by the intra product and by V'
+        for (int i = kQkFull; i < kPReady; ++i) mbar_init(bar(i), PL::OWN && !kState && (i & ~1) == kEmptyV ? 2 : 1);  // of copies and products
+        for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), kLGroup);                                         // of a group of threads
         fence_mbar_init();
+        fence_proxy_async_smem();
         fail[0] = odd[0] = odd[1] = 0;
+#ifdef GDN_TEST_MISSING_COPY
+        // test build: the first chunks of the first item are never loaded nor arrived on: their waits run out
+        if (item > 0 || blockIdx.y > 0)
+#endif
+            for (int c = 0; c < min(nch, 2); ++c) load_qk(c), load_v(c);  // before anything else is set up
     }
     if (tid < 32) pw[tid - 32] = 0.f;
     if (tid < kLC + 1) pw[tid] = tid == 0 ? 1.f : expf((float)tid * ld);
@@ -170,7 +196,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    auto stage = [&](int c) -> uint32_t { return (uint32_t)(c & 1) * PL::STAGE; };
+    auto u_col = [&](int c) -> uint32_t { return kState && (c & 1) ? kScCol : kUCol; };
     // bounded: a wait that runs out marks the CTA as failed, which ends every other wait of it
     auto wait = [&](int i, uint32_t parity) -> bool {
         return mbar_try_wait(bar(i), parity) || wait_more(bar(i), parity, smem_u32(const_cast<int*>(fail)));
@@ -280,21 +306,21 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 if (!ok) break;
                 put_state();
             }
-            ok = warp_wait(kUFull, (uint32_t)c & 1u);
+            ok = warp_wait(kUFull + (c & 1), (uint32_t)(c >> 1) & 1u);
             if (!ok) break;
             tc_fence_after();
             const float gm = pw[min(kLC, n - c * kLC)];
 #pragma unroll
             for (int c0 = 0; c0 < kLHalf; c0 += 16) {
                 float u[16];
-                tmem_ld16(lane_base + kUCol + kLHalf * hf + c0, u);
+                tmem_ld16(lane_base + u_col(c) + kLHalf * hf + c0, u);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     S[c0 / 2 + e] = __ffma2_rn(make_float2(gm, gm), S[c0 / 2 + e], make_float2(u[2 * e], u[2 * e + 1]));
             }
             tc_fence_before();
-            mbar_arrive(bar(kUFree));
+            mbar_arrive(bar(kUFree + (c & 1)));
         }
         if (ok && mine) {
             if constexpr (kState) {
@@ -396,9 +422,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
             const int m = min(kLC, n - c * kLC);
             const uint32_t parity = (uint32_t)(c >> 1) & 1u;
             bool o_left = !kState && c > 0;
+            const int before = kState ? c - 2 : c - 1;  // the chunk whose V' was where this one's goes
             for (uint32_t polls = 0; polls < kLPolls; ++polls) {  // what has not come by then is waited for below
-                // V' lies where the last chunk's was, which the update has read then; of a partial chunk K's rows are cleared too
-                const bool there = mbar_test(bar(kVFull + (c & 1)), parity) && (c == 0 || mbar_test(bar(kUFull), (uint32_t)(c - 1) & 1u)) &&
+                // V' goes over another chunk's, which the update has read then; of a partial chunk K's rows are cleared too
+                const bool there = mbar_test(bar(kVFull + (c & 1)), parity) &&
+                                   (before < 0 || mbar_test(bar(kUFull + (before & 1)), (uint32_t)(before >> 1) & 1u)) &&
                                    (m == kLC || mbar_test(bar(kQkFull + (c & 1)), parity));
                 if (__all_sync(0xffffffffu, there)) break;
                 if (o_left && __all_sync(0xffffffffu, mbar_test(bar(kOFull), (uint32_t)(c - 1) & 1u))) {
@@ -412,7 +440,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     break;
                 }
             }
-            ok = ok && warp_wait(kVFull + (c & 1), parity) && (c == 0 || warp_wait(kUFull, (uint32_t)(c - 1) & 1u)) &&
+            ok = ok && warp_wait(kVFull + (c & 1), parity) &&
+                 (before < 0 || warp_wait(kUFull + (before & 1), (uint32_t)(before >> 1) & 1u)) &&
                  (m == kLC || warp_wait(kQkFull + (c & 1), parity));
             if (!ok) break;
             unsigned char* vt = sm + stage(c) + PL::V_OFF;
@@ -442,7 +471,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < NP; ++e)
-                    *reinterpret_cast<uint4*>(sm + PL::VP_OFF + e * PL::BOX + at) =
+                    *reinterpret_cast<uint4*>(sm + PL::vp(kState && (c & 1), e) + at) =
                         make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
             }
             if (!(probe.x == 0.f && probe.y == 0.f)) odd[c & 1] = c + 1;
@@ -456,25 +485,18 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (!kState && ok && nch > 0 && warp_wait(kOFull, (uint32_t)(nch - 1) & 1u)) write_o(nch - 1);
     } else if (tid == 3 * kLGroup) {
         // ============ tiles by TMA ============
-        constexpr uint32_t bytes = kState ? PL::QK : 2 * PL::QK;
-        int qk = 0, v = 0;  // chunks asked for
-        for (int c = 0; c < nch; ++c) {
-            const uint32_t st = base + stage(c), parity = (uint32_t)((c - 2) >> 1) & 1u;
-            if (c >= 2 && !wait(kEmptyQk + (c & 1), parity)) break;
 #ifdef GDN_TEST_MISSING_COPY
-            // test build: the first chunk of the first item is never loaded nor arrived on: its wait runs out
-            if (item == 0 && blockIdx.y == 0 && c == 0) break;
+        int qk = item > 0 || blockIdx.y > 0 ? min(nch, 2) : 0, v = qk;
+#else
+        int qk = min(nch, 2), v = qk;  // chunks asked for
 #endif
-            mbar_arrive_expect_tx(bar(kQkFull + (c & 1)), bytes);
-#pragma unroll
-            for (int j = 0; j < DK / 64; ++j) {
-                tma_load_3d(st + PL::K_OFF + j * PL::BOX, &maps.k, 64 * j, hk, tok0 + c * kLC, bar(kQkFull + (c & 1)));
-                if (!kState) tma_load_3d(st + PL::Q_OFF + j * PL::BOX, &maps.q, 64 * j, hk, tok0 + c * kLC, bar(kQkFull + (c & 1)));
-            }
+        for (int c = qk; c < nch && qk > 0; ++c) {
+            const uint32_t parity = (uint32_t)((c - 2) >> 1) & 1u;
+            if (!wait(kEmptyQk + (c & 1), parity)) break;
+            load_qk(c);
             qk = c + 1;
-            if (c >= 2 && !wait(kEmptyV + (c & 1), parity)) break;
-            mbar_arrive_expect_tx(bar(kVFull + (c & 1)), PL::BOX);
-            tma_load_3d(st + PL::V_OFF, &maps.v, dv0, h, tok0 + c * kLC, bar(kVFull + (c & 1)));
+            if (!wait(kEmptyV + (c & 1), parity)) break;
+            load_v(c);
             v = c + 1;
         }
         // copies in flight land before the CTA leaves
@@ -517,7 +539,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
         for (int c = 0; c < nch && ok; ++c) {
             const uint32_t st = base + stage(c);
             // U: K^T V'.  The state waits for it alone.
-            ok = all_over(kVReady + (c & 1), c >> 1, kUFree, c - 1, kQkFull + (c & 1), c >> 1);
+            const int before = kState ? c - 2 : c - 1;
+            ok = all_over(kVReady + (c & 1), c >> 1, kUFree + (before & 1), before >> 1, kQkFull + (c & 1), c >> 1);
             if (!ok) break;
             tc_fence_after();
             if (lead) {
@@ -525,10 +548,10 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 for (int part = 0; part < NP; ++part)
 #pragma unroll 2
                     for (int ks = 0; ks < kLC / 16; ++ks)
-                        umma_bf16(tm + kUCol, umma_desc_sw128_mn(st + PL::K_OFF + ks * 2048u, PL::BOX),
-                                  umma_desc_sw128_mn(base + PL::VP_OFF + part * PL::BOX + ks * 2048u, PL::BOX),
+                        umma_bf16(tm + u_col(c), umma_desc_sw128_mn(st + PL::K_OFF + ks * 2048u, PL::BOX),
+                                  umma_desc_sw128_mn(base + PL::vp(kState && (c & 1), part) + ks * 2048u, PL::BOX),
                                   id64 | kBn | kAm, part + ks > 0 ? 1u : 0u);
-                umma_commit(bar(kUFull));
+                umma_commit(bar(kUFull + (c & 1)));
                 if (kState) {
                     umma_commit(bar(kEmptyQk + (c & 1)));
                     umma_commit(bar(kEmptyV + (c & 1)));
