@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
     };
     if (warp == 0) tmem_alloc(smem_u32(tmem_slot), kLCols);
     if (tid == 3 * kLGroup) {
-        // V is read by the intra product and by V'
-        for (int i = kQkFull; i < kPReady; ++i) mbar_init(bar(i), PL::OWN && !kState && (i & ~1) == kEmptyV ? 2 : 1);  // of copies and products
+        for (int i = kQkFull; i < kPReady; ++i)  // of copies and products; V is read by the intra product and by V' (kState: by V' alone)
+            mbar_init(bar(i), (i & ~1) != kEmptyV ? 1 : kState ? kLGroup : PL::OWN ? 2 : 1);
         for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), kLGroup);                                         // of a group of threads
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             if (!(probe.x == 0.f && probe.y == 0.f)) odd[c & 1] = c + 1;
             fence_proxy_async_smem();
             mbar_arrive(bar(kVReady + (c & 1)));
+            if (kState) mbar_arrive(bar(kEmptyV + (c & 1)));
             if (o_left) {
                 ok = warp_wait(kOFull, (uint32_t)(c - 1) & 1u) && write_o(c - 1);
                 if (!ok) break;
@@ -492,12 +493,19 @@ __global__ void __launch_bounds__(kLThreads, 1)
 #endif
         for (int c = qk; c < nch && qk > 0; ++c) {
             const uint32_t parity = (uint32_t)((c - 2) >> 1) & 1u;
+            if (kState) {  // V is free first, else K and Q are
+                if (!wait(kEmptyV + (c & 1), parity)) break;
+                load_v(c);
+                v = c + 1;
+            }
             if (!wait(kEmptyQk + (c & 1), parity)) break;
             load_qk(c);
             qk = c + 1;
-            if (!wait(kEmptyV + (c & 1), parity)) break;
-            load_v(c);
-            v = c + 1;
+            if (!kState) {
+                if (!wait(kEmptyV + (c & 1), parity)) break;
+                load_v(c);
+                v = c + 1;
+            }
         }
         // copies in flight land before the CTA leaves
         for (int c = max(0, qk - 2); c < qk; ++c) mbar_wait_bounded(bar(kQkFull + (c & 1)), (uint32_t)(c >> 1) & 1u, kLPolls);
@@ -554,7 +562,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 umma_commit(bar(kUFull + (c & 1)));
                 if (kState) {
                     umma_commit(bar(kEmptyQk + (c & 1)));
-                    umma_commit(bar(kEmptyV + (c & 1)));
                 }
             }
             any = true;
