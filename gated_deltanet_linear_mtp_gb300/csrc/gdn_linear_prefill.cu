@@ -8,23 +8,29 @@
 //
 // One CTA holds a tile of 64 value dimensions of one (prompt, head) and walks its chunks; all four products run on tcgen05:
 //     scores  [128 i x 128 j]   Q K^T                  both K-major, as TMA brings them (128-byte swizzle)
-//     inter   [128 i x 64 dv]   Q S^T                  S as bf16 hi + lo in shared memory, rows dk
+//     inter   [128 i x 64 dv]   Q S^T                  S as bf16 in shared memory, rows dk
 //     update  [DK dk x 64 dv]   K^T V'                 K read M-major, V' = g^{m-1-j} v_j as 2 or 3 bf16 parts
 //     intra   [128 i x 64 dv]   P V                    P bf16 in tensor memory (over the scores), V N-major as it came
-// The state itself stays in fp32 registers (thread = dk, 64 dv) and never passes through fewer bits: an update adds the
-// product to it, and what is rounded are operands.  hi + lo is 16 bits of S in o, which is bf16.  v g^e is rounded to
-// 2^-17 of each term for a bf16 pool and, in three parts, to 2^-25 for an fp32 pool, whose states keep fp32's digits.  P is
-// rounded to bf16 as o is: its rounding errors are those of single terms of a sum.
+// The state itself stays in fp32 registers (thread = dk, 32 dv) and never passes through fewer bits: an update adds the product
+// to it, and what is rounded are operands.  S is rounded to bf16 on its way into o, as o is, and so is P: the errors are those of
+// single terms of a sum.  v g^e, which the pool keeps, is good to 2^-16 of each term in two bf16 parts for a bf16 pool and to 2^-24
+// in three for an fp32 pool, whose states keep fp32's digits.
 //
 // Three groups of eight warps: the first forms P from the scores (thread = row i and a half of the columns), the second keeps the
-// state (thread = dk and 32 dv), the third forms V' from V (thread = token and 32 dv) and takes o from the products (thread = row i and 32 dv); warp 24
-// brings the tiles by TMA (two stages), 25 issues the products, 26 stores o by TMA, 27 says when V has been read.  A group's work on a chunk is a few hundred dependent
-// instructions, at which one warp issues every sixth cycle or so: eight warps a group take half the time of four.  For the same
-// reason code is kept short (unrolled to 95 KB, the warps waited for instructions).  The only serial chain between chunks is
-// state -> inter -> state and V' -> update -> state; the scores of the next chunk and the intra product fill the tensor cores.
+// state (thread = dk and 32 dv), the third forms V' from V (thread = token and 32 dv) and takes o from the products (thread = row
+// i and 32 dv).  Warp 24 brings the tiles by TMA (two stages), 25 issues the products, 26 stores o by TMA, 27 says when V has been
+// read.  A group's work on a chunk is a few hundred dependent instructions, at which one warp issues every sixth cycle or so: eight
+// warps a group take half the time of four.  For the same reason code is kept short (unrolled to 95 KB, the warps waited for
+// instructions).  The only serial chains between chunks are state -> inter -> state and V' -> update -> state; the scores of the
+// next chunk and the intra product fill the tensor cores meanwhile.
+//
+// Measured (D 128): 8 prompts of 8192, HK 16, HV 32, bf16 pool 401 us (4.0 TB/s, 342 TFLOP/s of the recurrence's 4 DK DV a token); a step
+// of one chunk and 64 dv takes about 3950 cycles, of which the products run 2000 and their issue takes 2770, and a CTA's start and end 9 us.
+// Two warps issuing two products each measured the same (400).
 //
 // Few prompts and heads leave SMs without work: then prompts are cut into pieces (linear_split), a first launch forms what
-// each piece adds to the state (K and V only), and the second starts every piece from the sum of those before it.
+// each piece adds to the state (K and V only), and the second starts every piece from the sum of those before it (one prompt of
+// 16384, fp32 pool, HV 16: 136 us on 128 CTAs; whole, with 76 heads on 152 CTAs, 337).
 #include <atomic>
 #include <cstring>
 #include <type_traits>

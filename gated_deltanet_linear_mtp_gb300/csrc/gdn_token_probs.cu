@@ -5,7 +5,8 @@
 // -inf logits (forbidden tokens) get 0; a row of nothing else gets zeros.  A NaN or +inf logit, or a temperature that is
 // negative or not finite, makes the row zeros and sets GDN_ERRBIT_NONFINITE.
 //
-// Bytes bound it: a row is read once from DRAM and written once.  A thread-block cluster takes a row, each CTA a run of it:
+// Bytes bound it: a row is read once from DRAM and written once (512 rows of 131072 bf16: 90 us, 4.5 TB/s; one row of 50001 fp32:
+// 7 us a call).  A thread-block cluster takes a row, each CTA a run of it:
 // a first pass with the running maximum and sum, 8 or 16 numbers at a time, one exchange of (maximum, sum, index) within the
 // cluster, and a second pass that reads the run again (from L1 or L2, where it still is) and writes.
 //
@@ -90,6 +91,8 @@ __device__ __forceinline__ uint32_t shared_of(const void* p, uint32_t rank) {  /
     return r;
 }
 
+// Tried for rows of 131072: the run kept in registers between the passes (one exp an element, 64 registers and fewer threads in
+// flight: 158 us), and the maximum first and the sum after it.
 template <typename InT>
 __global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const TokenProbsParams p, const int run) {
     constexpr int EPC = 16 / sizeof(InT);  // elements of a 16-byte piece
@@ -257,7 +260,7 @@ cudaError_t launch_t(const TokenProbsParams& p, cudaStream_t s) {
     int ncta = 1;
     while (ncta < kProbMaxCluster && ((int64_t)p.V > (int64_t)ncta * 32768 || (rows * ncta < 152 && p.V > ncta * 4096))) ncta *= 2;
     const int run = (int)(((int64_t)p.V + ncta * 64 - 1) / (ncta * 64) * 64);
-    const unsigned gy = (unsigned)(rows < 32768 ? rows : 32768);
+    const unsigned gy = (unsigned)(rows < 65535 ? rows : 65535);  // rows < 2^31: z stays below 2^16
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ncta, gy, (unsigned)((rows + gy - 1) / gy));
     cfg.blockDim = dim3(kProbThreads);

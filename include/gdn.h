@@ -502,7 +502,8 @@ GDN_API gdn_status gdn_linear_prefill(const gdn_dims* dims, const int32_t* cu_se
 GDN_API int64_t gdn_linear_prefill_workspace(int32_t B, int32_t N, int32_t HV, int32_t DK, int32_t DV);
 
 /*
- * The sampling that ends a speculative step: the logits of its rows become probabilities (gdn_token_probs), drafts are accepted
+ * The sampling that ends a speculative step (the CTAs of a row or lane run as one thread-block cluster and meet at its hardware
+ * barrier): the logits of its rows become probabilities (gdn_token_probs), drafts are accepted
  * against them and one more token is drawn (gdn_draft_accept), and accept_len goes to the commits above.  T is the step's: the
  * last token and T - 1 drafts; T = 1 is a decode step without drafts.
  */

@@ -255,3 +255,63 @@ def test_a_speculative_step(captured):
         assert int(n[b]) == want and tokens[b].tolist() == tk
         _, s, _, sa = linear_ref.steps(start[index[b]].cpu(), q[b, :want].cpu(), k[b, :want].cpu(), v[b, :want].cpu(), ld.cpu(), 1.0)
         assert bool(((pool[index[b]].double().cpu() - s[-1]).abs() <= 2.0 ** -15 * sa[-1]).all())
+
+
+def test_clusters_captured_replayed_and_on_another_stream():
+    """Rows that several CTAs share, in a graph and on a side stream."""
+    x, te = 3 * torch.randn((3, 2, 60001), device="cuda"), torch.tensor([0.7, 0.0, 1.1], device="cuda")
+    y = torch.zeros_like(x)
+    lanes = Lanes(3, 3, 60001, True, 4)
+    gdn.gdn_token_probs(x, te, y)
+    lanes.check()
+    want, n, tokens = y.clone(), lanes.len.clone(), lanes.tokens.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_token_probs(x, te, y)
+        lanes.call()
+    for side in (None, torch.cuda.Stream()):
+        y.zero_()
+        lanes.len.zero_()
+        lanes.tokens.zero_()
+        torch.cuda.synchronize()
+        if side is None:
+            graph.replay()
+            graph.replay()
+        else:
+            gdn.gdn_token_probs(x, te, y, stream=side)
+            lanes.call(stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(lanes.len, n) and torch.equal(lanes.tokens, tokens)
+
+
+def test_from_other_threads():
+    """As a thread's first CUDA call, and from two at once."""
+    import threading
+
+    from test_gpu_threads import in_thread
+
+    lanes = [Lanes(4, 3, 30011, True, s) for s in range(2)]
+    xs = [torch.randn((2, 2, 9000 + s), device="cuda") for s in range(2)]
+    ys, te = [torch.zeros_like(x) for x in xs], torch.ones(2, device="cuda")
+    q, k, v = (torch.randn((300, 1, 64), device="cuda").bfloat16() for _ in range(3))
+    ld, pools, cu = torch.tensor([-0.1], device="cuda"), [torch.zeros((1, 1, 64, 64), device="cuda") for _ in range(3)], torch.tensor([0, 300], **I32)
+    os_ = [torch.zeros_like(v) for _ in range(3)]
+    index = torch.zeros(1, **I32)
+
+    def work(i):
+        ws = gdn.linear_prefill_workspace(300, 1, 1, 64, 64)
+        gdn.gdn_linear_prefill(q, k, v, ld, pools[i], index, cu, os_[i], ws)
+        gdn.gdn_token_probs(xs[i % 2], te, ys[i % 2])
+        lanes[i % 2].call()
+
+    in_thread(lambda: work(2))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(os_[i], os_[2]) and torch.equal(pools[i], pools[2]) and bool(os_[i].any())
+        check_probs(xs[i], te)
+        lanes[i].check()
