@@ -89,28 +89,27 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
     __shared__ bool sh_refused;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.T, V = p.V;
     const int ncta = gridDim.x, rank = blockIdx.x, b = blockIdx.y;
-    if (p.indices != nullptr) {
-        const int slot = p.indices[b];
-        if (slot < 0) {  // the whole cluster leaves
-            if (slot < -1 && tid == 0 && rank == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
-            return;
-        }
+    const int32_t* drafts = p.drafts + (int64_t)b * (T - 1);
+    const int slot = p.indices != nullptr ? p.indices[b] : 0;
+    const int x = warp == 0 && lane < T - 1 ? drafts[lane] : -1;  // asked for together with the slot
+    const float u = warp == 0 && lane < T ? p.uniform[(int64_t)b * T + lane] : 0.f;
+    if (slot < 0) {  // the whole cluster leaves
+        if (slot < -1 && tid == 0 && rank == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
+        return;
     }
     // shared memory of another CTA is there once that CTA runs: arrived at here, waited for before the first exchange
     if (ncta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    const int32_t* drafts = p.drafts + (int64_t)b * (T - 1);
     const float* target = p.target + (int64_t)b * T * p.target_stride;
     const float* draft = p.draft != nullptr ? p.draft + (int64_t)b * (T - 1) * p.draft_stride : nullptr;
     if (warp == 0) {  // lane i: draft i
         bool good = false, real = false;
         if (lane < T - 1) {
-            const int x = drafts[lane];
             real = x >= 0 && x < V;
             if ((x < -1 || x >= V) && rank == 0 && p.err != nullptr) atomicOr(p.err, GDN_ERRBIT_INDEX);
             if (real) {
                 const float px = target[lane * p.target_stride + x];
                 const float qx = draft != nullptr ? draft[lane * p.draft_stride + x] : 1.f;
-                good = (double)p.uniform[(int64_t)b * T + lane] * (double)qx < (double)px;
+                good = (double)u * (double)qx < (double)px;
             }
         }
         const unsigned goods = __ballot_sync(0xffffffffu, good), reals = __ballot_sync(0xffffffffu, real);
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
 
     // The CTA whose part the threshold falls into draws the token: the first v whose running sum passes it.  Where rounding
     // leaves none, the last v with r_v > 0, which is in the last CTA with a sum.
-    const double threshold = (double)p.uniform[(int64_t)b * T + T - 1] * total;
+    const double threshold = (double)__shfl_sync(0xffffffffu, u, T - 1) * total;
     bool writer = rank == 0, past = false;
     if (total > 0.) {
         int winner = 0;
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
         atomicOr(p.err, GDN_ERRBIT_NONFINITE);
     }
     if (lane == 0) p.accept_len[b] = n + 1;
-    if (lane < T) p.tokens[(int64_t)b * T + lane] = lane < n ? drafts[lane] : lane == n ? token : -1;
+    if (lane < T) p.tokens[(int64_t)b * T + lane] = lane < n ? x : lane == n ? token : -1;
 }
 
 }  // namespace
