@@ -901,80 +901,83 @@ def gdn_kv4_attention(q, cache, block_tables, kv_lens, o, workspace, *, cu_seqle
 
 
 # ---- linear attention with a fixed decay for each head ----------------------------------------------
+# A call on one token takes 3 us on the GPU, so its marshalling is kept as short as its checks allow.
 def _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, lead, scale):
-    """GPU, gdn_dims and pointers of k, v, log_decay, state_pool and the slots of a linear-attention call whose tokens have
-    the leading shape `lead` ([B, T], or [N] packed)."""
+    """GPU, gdn_dims (o's type that of k), and the pointers of k, v, log_decay, state_pool, state_indices, out_indices of a
+    linear-attention call whose tokens have the leading shape `lead` ([B, T], or [N] packed)."""
     import torch
 
     dev = _gpu(k, "k")
-    if k.dim() != len(lead) + 2 or v.dim() != len(lead) + 2 or state_pool.dim() != 4:
+    if len(lead) + 2 != k.dim() or state_pool.dim() != 4:
         raise ValueError("q, k, v and o are [B,T,heads,dim] (prefill: [N,heads,dim]), state_pool is [num_slots,HV,DV,DK]")
     HK, DK = k.shape[-2:]
-    num_slots, HV, DV, _ = state_pool.shape
-    B, f32, i32, code = state_indices.shape[0], torch.float32, torch.int32, _code(k, "k")
-    sd = _code(state_pool, "state_pool")
-    d = GdnDims(B, lead[-1], HK, HV, DK, DV, num_slots, code, sd, code, float(scale), 0.0)
-    ptrs = dict(k=_ptr(k, "k", k.dtype, (*lead, HK, DK), dev), v=_ptr(v, "v", k.dtype, (*lead, HV, DV), dev),
-                log_decay=_ptr(log_decay, "log_decay", f32, (HV,), dev),
-                pool=_ptr(state_pool, "state_pool", state_pool.dtype, (num_slots, HV, DV, DK), dev),
-                idx=_ptr(state_indices, "state_indices", i32, (B,), dev),
-                out=_ptr(out_indices, "out_indices", i32, (B,), dev))
-    return dev, d, ptrs
+    pool_shape = state_pool.shape
+    num_slots, HV, DV, pool_dk = pool_shape
+    if pool_dk != DK:
+        raise ValueError(f"state_pool: shape {tuple(pool_shape)}, expected {(num_slots, HV, DV, DK)}")
+    lanes, i32, dt, pool_dt = state_indices.shape, torch.int32, k.dtype, state_pool.dtype
+    code = _code(k, "k")
+    d = GdnDims(lanes[0], lead[-1], HK, HV, DK, DV, num_slots, code, code if pool_dt is dt else _code(state_pool, "state_pool"),
+                code, scale, 0.0)
+    return (dev, d, _ptr(k, "k", dt, k.shape, dev), _ptr(v, "v", dt, lead + (HV, DV), dev),
+            _ptr(log_decay, "log_decay", torch.float32, (HV,), dev), _ptr(state_pool, "state_pool", pool_dt, pool_shape, dev),
+            _ptr(state_indices, "state_indices", i32, lanes, dev), _ptr(out_indices, "out_indices", i32, lanes, dev))
 
 
 def _linear_io(q, k, o, d, dev):
     """Pointers of q (k's type and shape) and o (fp32 or bf16, [.., HV, DV]); o's type goes into the dims."""
-    d.out_dtype = _code(o, "o")
-    return (_ptr(q, "q", k.dtype, k.shape, dev), _ptr(o, "o", o.dtype, (*k.shape[:-2], d.HV, d.DV), dev))
+    if o.dtype is not k.dtype:
+        d.out_dtype = _code(o, "o")
+    return (_ptr(q, "q", k.dtype, k.shape, dev), _ptr(o, "o", o.dtype, k.shape[:-2] + (d.HV, d.DV), dev))
 
 
 def _lanes(k, state_indices):
     if k.dim() != 4 or state_indices.dim() != 1 or k.shape[0] != state_indices.shape[0]:
         raise ValueError("q, k, v and o are [B,T,heads,dim], state_indices [B]")
-    return tuple(k.shape[:2])
+    return k.shape[:2]
+
+
+def _err(err_word, dev: int):
+    import torch
+
+    return None if err_word is None else _ptr(err_word, "err_word", torch.int32, (1,), dev)
 
 
 def gdn_linear_decode(q, k, v, log_decay, state_pool, state_indices, o, err_word=None, *, out_indices=None, scale=1.0,
                       stream=None) -> None:
     """T tokens (normally 1) of ``S = exp(log_decay) S + v k^T``, ``o = scale S q`` from ``state_pool[state_indices[b]]``; the
     final state goes into slot ``out_indices[b]`` (the same slot if not given; -1 writes none)."""
-    import torch
-
     L = lib()
-    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, _lanes(k, state_indices), scale)
+    dev, d, kp, vp, ld, pool, idx, out = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices,
+                                                      _lanes(k, state_indices), scale)
     qp, op = _linear_io(q, k, o, d, dev)
-    _run(dev, stream, L.gdn_linear_decode,
-         (ctypes.byref(d), qp, a["k"], a["v"], a["log_decay"], a["pool"], a["idx"], a["out"], op,
-          _ptr(err_word, "err_word", torch.int32, (1,), dev)), "gdn_linear_decode")
+    _run(dev, stream, L.gdn_linear_decode, (ctypes.byref(d), qp, kp, vp, ld, pool, idx, out, op, _err(err_word, dev)),
+         "gdn_linear_decode")
 
 
 def gdn_linear_verify(q, k, v, log_decay, state_pool, state_indices, o, intermediate_states=None, err_word=None, *, scale=1.0,
                       stream=None) -> None:
     """The same for T draft tokens from states that are only read; ``intermediate_states`` ``[B,T,HV,DV,DK]`` (state_pool's
     type) receives the state after every token, for ``gdn_commit``."""
-    import torch
-
     L = lib()
     lead = _lanes(k, state_indices)
-    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, None, lead, scale)
+    dev, d, kp, vp, ld, pool, idx, _ = _linear_args(k, v, log_decay, state_pool, state_indices, None, lead, scale)
     qp, op = _linear_io(q, k, o, d, dev)
     _run(dev, stream, L.gdn_linear_verify,
-         (ctypes.byref(d), qp, a["k"], a["v"], a["log_decay"], a["pool"], a["idx"], op,
-          _ptr(intermediate_states, "intermediate_states", state_pool.dtype, (*lead, d.HV, d.DV, d.DK), dev),
-          _ptr(err_word, "err_word", torch.int32, (1,), dev)), "gdn_linear_verify")
+         (ctypes.byref(d), qp, kp, vp, ld, pool, idx, op,
+          _ptr(intermediate_states, "intermediate_states", state_pool.dtype, lead + (d.HV, d.DV, d.DK), dev), _err(err_word, dev)),
+         "gdn_linear_verify")
 
 
 def gdn_linear_commit(k, v, log_decay, state_pool, state_indices, accept_len, err_word=None, *, out_indices=None,
                       stream=None) -> None:
     """The state after the first ``accept_len[b]`` of a verify's tokens, into the lane's slot (or ``out_indices[b]``)."""
-    import torch
-
     L = lib()
-    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, _lanes(k, state_indices), 1.0)
+    dev, d, kp, vp, ld, pool, idx, out = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices,
+                                                      _lanes(k, state_indices), 1.0)
     _run(dev, stream, L.gdn_linear_commit,
-         (ctypes.byref(d), a["k"], a["v"], a["log_decay"], a["pool"], a["idx"], a["out"],
-          _ptr(accept_len, "accept_len", torch.int32, (d.B,), dev), _ptr(err_word, "err_word", torch.int32, (1,), dev)),
-         "gdn_linear_commit")
+         (ctypes.byref(d), kp, vp, ld, pool, idx, out, _ptr(accept_len, "accept_len", state_indices.dtype, (d.B,), dev),
+          _err(err_word, dev)), "gdn_linear_commit")
 
 
 def linear_prefill_workspace(N, B, HV, DK, DV, device=None):
@@ -999,14 +1002,14 @@ def gdn_linear_prefill(q, k, v, log_decay, state_pool, state_indices, cu_seqlens
     L = lib()
     if k.dim() != 3 or state_indices.dim() != 1:
         raise ValueError("q, k [N,HK,DK], v, o [N,HV,DV], state_indices [B]")
-    dev, d, a = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, (k.shape[0],), scale)
+    dev, d, kp, vp, ld, pool, idx, out = _linear_args(k, v, log_decay, state_pool, state_indices, out_indices, k.shape[:1], scale)
     qp, op = _linear_io(q, k, o, d, dev)
     i32 = torch.int32
     _run(dev, stream, L.gdn_linear_prefill,
-         (ctypes.byref(d), _ptr(cu_seqlens, "cu_seqlens", i32, (d.B + 1,), dev), qp, a["k"], a["v"], a["log_decay"], a["pool"],
-          a["idx"], a["out"], _ptr(has_initial_state, "has_initial_state", i32, (d.B,), dev), op,
-          _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel(),
-          _ptr(err_word, "err_word", i32, (1,), dev)), "gdn_linear_prefill")
+         (ctypes.byref(d), _ptr(cu_seqlens, "cu_seqlens", i32, (d.B + 1,), dev), qp, kp, vp, ld, pool, idx, out,
+          _ptr(has_initial_state, "has_initial_state", i32, (d.B,), dev), op,
+          _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel(), _err(err_word, dev)),
+         "gdn_linear_prefill")
 
 
 # ---- the sampling that ends a speculative step ---------------------------------------------------------
