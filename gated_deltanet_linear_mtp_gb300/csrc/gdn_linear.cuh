@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(Split<DK>::THREADS, Split<DK>::MIN_CTAS_PER_SM
 //   * A token's q as the product's column for S q is, register by register, its row for q . k.
 // A value that is not finite would reach earlier tokens as 0 times it: then the sum over j is formed term by term.
 // Measured (HK 16, HV 32, D 128): decode of 64 lanes with fp32 states 47.5 us (5.7 TB/s; the lane layout above: 63), verify of 128 x 4 with
-// states kept 110 (6.2 TB/s; 137), of 256 x 8 without 74 (3.9; 295), its commit 103 (4.8; 152).  The last two wait for loads; two
-// blocks of rows a warp measured the same or slower (75 and 110: fewer warps).
+// states kept 110 (6.2 TB/s; 137).  Verify and commit of many lanes wait for loads here and are the streaming kernel's
+// (gdn_linear_stream.cuh); two blocks of rows a warp measured the same or slower (fewer warps).
 enum { kLinVerify, kLinDecode, kLinKept, kLinCommit };
 constexpr int kLinWarps = 4;
 
@@ -581,10 +581,18 @@ cudaError_t launch_linear_mma(const LinearParams& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+}  // namespace gdn
+
+#include "gdn_linear_stream.cuh"
+
+namespace gdn {
+
 template <int DK, typename InT, typename StT>
 cudaError_t launch_linear_dk(const LinearParams& p, cudaStream_t s) {
     // bf16 tokens of a step, where a warp's 16 rows fit its registers
     if constexpr (std::is_same<InT, __nv_bfloat16>::value && DK >= 32 && DK * sizeof(StT) <= 512) {
+        cudaError_t e;
+        if (p.cu_seqlens == nullptr && try_linear_stream<DK, StT>(p, s, e)) return e;
         if (p.cu_seqlens == nullptr) return p.T <= 8 ? launch_linear_mma<DK, StT, 1>(p, s) : launch_linear_mma<DK, StT, 2>(p, s);
     }
     using SP = Split<DK>;

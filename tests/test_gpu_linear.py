@@ -364,6 +364,154 @@ def test_a_tile_that_never_lands(timeout_lib, monkeypatch, lens, in_pieces):  # 
     assert int(c.err) == 0 and torch.equal(c.o, good)
 
 
+STREAMED = [  # B, T, HK, HV, DK, DV, state: enough lanes for the streaming kernel
+    (90, 8, 4, 8, 128, 128, "bf16"), (200, 1, 2, 6, 128, 72, "bf16"), (100, 3, 7, 7, 64, 136, "bf16"), (170, 5, 1, 4, 256, 48, "bf16"),
+    (90, 7, 8, 8, 128, 128, "f32"), (156, 2, 2, 4, 64, 200, "f32"), (1000, 8, 1, 1, 64, 80, "bf16"), (40, 4, 16, 32, 128, 128, "bf16")]
+
+
+def lanes_in_64_bits(c, S, T):
+    """States and o's after 0 .. T tokens of all lanes at once, with the sums of absolute values."""
+    rep = c.HV // c.HK
+    q, k = c.q.double().repeat_interleave(rep, 2), c.k.double().repeat_interleave(rep, 2)
+    v, g = c.v.double(), torch.exp(c.ld.double())[None, :, None, None]
+    S, A = S.double(), S.double().abs()
+    states, o = [(S, A)], []
+    for t in range(T):
+        S = g * S + v[:, t, :, :, None] * k[:, t, :, None, :]
+        A = g * A + v[:, t, :, :, None].abs() * k[:, t, :, None, :].abs()
+        states.append((S, A))
+        o.append((c.scale * torch.einsum("bhij,bhj->bhi", S, q[:, t]), c.scale * torch.einsum("bhij,bhj->bhi", A, q[:, t].abs())))
+    return states, [torch.stack(x, 1) for x in zip(*o)]
+
+
+@pytest.mark.parametrize("B,T,HK,HV,DK,DV,state", STREAMED)
+def test_steps_of_many_lanes(B, T, HK, HV, DK, DV, state):
+    c = Case((B, T), B, HK, HV, DK, DV, "bf16", state, seed=B)
+    g = torch.Generator().manual_seed(B)
+    padded = (torch.rand(B, generator=g) < 0.2).cuda()
+    padded[1], padded[-1] = True, False
+    read, write = c.read.clone(), c.write.clone()
+    read[padded] = -1
+    before, live = c.pool.clone(), ~padded
+    states, (o, oa) = lanes_in_64_bits(c, before[c.read.long()], T)
+    gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, read, c.o, None, c.err, scale=c.scale)
+    assert torch.equal(c.pool, before) and bool((c.o[padded] == CANARY).all())
+    near(c.o[live], o[live], oa[live], 0, "o")
+    # decode into other slots, some lanes into none
+    write[::7] = -1
+    o2 = torch.full_like(c.o, CANARY)
+    gdn.gdn_linear_decode(c.q, c.k, c.v, c.ld, c.pool, read, o2, c.err, out_indices=write, scale=c.scale)
+    near(o2[live], o[live], oa[live], 0, "decode o")
+    to = live & (write >= 0)
+    touched = torch.zeros(c.slots, dtype=torch.bool, device="cuda")
+    touched[write[to].long()] = True
+    near(c.pool[write[to].long()], states[T][0][to], states[T][1][to], 0, "decode state")
+    assert torch.equal(c.pool[~touched], before[~touched]) and bool((o2[padded] == CANARY).all())
+    # commit of 0 .. T tokens in place
+    c.pool.copy_(before)
+    n = torch.randint(0, T + 1, (B,), generator=g).to(**I32)
+    n[0], n[-1] = 0, T
+    gdn.gdn_linear_commit(c.k, c.v, c.ld, c.pool, read, n, c.err)
+    S = torch.stack([x[0] for x in states])[n.long(), torch.arange(B, device="cuda")]
+    A = torch.stack([x[1] for x in states])[n.long(), torch.arange(B, device="cuda")]
+    near(c.pool[c.read[live].long()], S[live], A[live], 0, "commit")
+    still = torch.ones(c.slots, dtype=torch.bool, device="cuda")
+    still[read[live & (n > 0)].long()] = False
+    assert torch.equal(c.pool[still], before[still])
+    # of none into other slots: copies
+    c.pool.copy_(before)
+    gdn.gdn_linear_commit(c.k, c.v, c.ld, c.pool, read, torch.zeros(B, **I32), c.err, out_indices=c.write)
+    assert torch.equal(c.pool[c.write[live].long()], before[c.read[live].long()])
+    assert int(c.err) == 0
+
+
+def test_many_lanes_with_bad_indices_lengths_and_values():
+    """Bad lanes are skipped and counted, good ones beside them get their results; what is not finite stays in its own rows and
+    tokens, and behind a lane's accepted tokens it is not read."""
+    B, T, HK, HV, DK, DV = 90, 6, 4, 8, 128, 128
+    c = Case((B, T), B, HK, HV, DK, DV, seed=5)
+    before = c.pool.clone()
+    n = torch.full((B,), 3, **I32)
+    c.k[7, 3:], c.v[7, 4:] = float("nan"), float("inf")  # behind the accepted tokens
+    c.v[8, 2, 1, 5] = float("inf")
+    c.k[9, 1, 0, 3] = float("-inf")
+    states, (o, oa) = lanes_in_64_bits(c, before[c.read.long()], T)
+    read = c.read.clone()
+    read[3], read[4], n[5], n[6] = -2, c.slots, T + 1, -1
+    gdn.gdn_linear_commit(c.k, c.v, c.ld, c.pool, read, n, c.err)
+    assert int(c.err) == gdn.ERRBIT_INDEX | gdn.ERRBIT_ACCEPT_LEN
+    got, (S, A) = c.pool[c.read.long()], states[3]
+    for b in range(B):
+        if b in (3, 4, 5, 6):
+            assert torch.equal(got[b], before[c.read[b].long()])
+        elif b in (8, 9):
+            fine = torch.isfinite(S[b])
+            assert torch.equal(torch.isfinite(got[b]), fine) and torch.equal(got[b][~fine].isnan(), S[b][~fine].isnan())
+            assert torch.equal(got[b][~fine & ~S[b].isnan()].double(), S[b][~fine & ~S[b].isnan()])
+            near(got[b][fine], S[b][fine], A[b][fine], 0, "beside what is not finite")
+        else:
+            near(got[b], S[b], A[b], 0, "commit")
+    # verify: tokens before the one with an infinity are not touched by it, nor are the other rows
+    c.err.zero_()
+    c.pool.copy_(before)
+    gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, read, c.o, None, c.err, scale=c.scale)
+    assert int(c.err) == gdn.ERRBIT_INDEX and bool((c.o[3:5] == CANARY).all())
+    keep = torch.isfinite(o)
+    keep[3:5] = False
+    keep[[7, 9]] = False
+    near(c.o[keep], o[keep], oa[keep], 0, "o")
+    near(c.o[7, :3], o[7, :3], oa[7, :3], 0, "o in front of what is not finite")
+    near(c.o[9, :1], o[9, :1], oa[9, :1], 0, "o in front of an infinite k")
+    assert not bool(torch.isfinite(c.o[8, 2:, 1, 5]).any())
+
+
+def test_many_lanes_twice_at_once_and_replayed():
+    """Two streams at once, and a captured call whose pool changes between replays."""
+    cases = [Case((128, 4), 128, 4, 8, 128, 128, seed=s) for s in (1, 2)]
+    alone = []
+    for c in cases:
+        gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, c.read, c.o, None, c.err, scale=c.scale)
+        alone.append(c.o.clone())
+        c.o.fill_(CANARY)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, c.read, c.o, None, c.err, scale=c.scale, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(c.o, a) for c, a in zip(cases, alone))
+    c = cases[0]
+    start = c.pool.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_linear_decode(c.q, c.k, c.v, c.ld, c.pool, c.read, c.o, c.err, scale=c.scale)
+    c.pool.copy_(start)
+    for _ in range(3):
+        graph.replay()
+    replayed, o = c.pool.clone(), c.o.clone()
+    c.pool.copy_(start)
+    for _ in range(3):
+        gdn.gdn_linear_decode(c.q, c.k, c.v, c.ld, c.pool, c.read, c.o, c.err, scale=c.scale)
+    assert torch.equal(replayed, c.pool) and torch.equal(o, c.o) and int(c.err) == 0
+
+
+def test_a_state_that_never_lands(timeout_lib, monkeypatch):  # noqa: F811
+    c = Case((128, 4), 128, 4, 8, 128, 128, seed=3)
+
+    def call():
+        gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, c.read, c.o, None, c.err, scale=c.scale)
+        torch.cuda.synchronize()
+
+    call()
+    assert int(c.err) == 0
+    good = c.o.clone()
+    run_with(timeout_lib, monkeypatch, call)
+    assert int(c.err) & gdn.ERRBIT_TIMEOUT
+    c.err.zero_()
+    call()
+    assert int(c.err) == 0 and torch.equal(c.o, good)
+
+
 def test_tensors_that_the_binding_refuses():
     c = Case((2, 2), 2, 1, 2, 64, 32)
     ok = (c.q, c.k, c.v, c.ld, c.pool, c.read, c.o)
