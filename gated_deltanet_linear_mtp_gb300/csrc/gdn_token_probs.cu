@@ -5,8 +5,8 @@
 // -inf logits (forbidden tokens) get 0; a row of nothing else gets zeros.  A NaN or +inf logit, or a temperature that is
 // negative or not finite, makes the row zeros and sets GDN_ERRBIT_NONFINITE.
 //
-// Bytes bound it: a row is read once from DRAM and written once (512 rows of 131072 bf16: 90 us, 4.5 TB/s; one row of 50001 fp32:
-// 7 us a call).  A thread-block cluster takes a row, each CTA a run of it:
+// Bytes bound it: a row is read once from DRAM and written once (512 rows of 131072 bf16: 73 us, 5.5 TB/s; one row of 50001 fp32:
+// 6.5 us a call).  A thread-block cluster takes a row, each CTA a run of it:
 // a first pass with the running maximum and sum, 8 or 16 numbers at a time, one exchange of (maximum, sum, index) within the
 // cluster, and a second pass that reads the run again (from L1 or L2, where it still is) and writes.
 //
@@ -19,6 +19,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "gdn.h"
 #include "gdn_internal.h"
@@ -47,6 +48,15 @@ __device__ __forceinline__ void unpack16(const uint4& r, float (&f)[8]) {  // bf
     }
 }
 
+// four logits
+template <typename InT>
+using Four = typename std::conditional<sizeof(InT) == 2, uint2, float4>::type;
+__device__ __forceinline__ float4 as_f32(const float4& r) { return r; }
+__device__ __forceinline__ float4 as_f32(const uint2& r) {
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -72,16 +82,23 @@ struct Weights {
     __device__ __forceinline__ float ratio(float o, float o2) const {  // of the weights against o to those against o2 >= o
         return kFar ? (*this)(o, o2) : ex2(o - o2);
     }
-    // a part joined with another: the sums against the larger maximum
-    __device__ __forceinline__ void join(Part& a, const Part& b) const {
-        const float m = fmaxf(a.m, b.m);
-        if (m > -INFINITY) {
-            const float o = offset(m);
-            a.s = (a.m > -INFINITY ? a.s * ratio(offset(a.m), o) : 0.f) + (b.m > -INFINITY ? b.s * ratio(offset(b.m), o) : 0.f);
-        }
-        a.at = b.m > a.m || (b.m == a.m && b.at < a.at) ? b.at : a.at;
-        a.m = m;
-        a.bad |= b.bad;
+    // the parts of N neighbouring lanes as one: the largest first, then every sum against it (o: the offset of a's)
+    template <int N>
+    __device__ __forceinline__ Part joined(Part a, float o) const {
+        float m = a.m;
+#pragma unroll
+        for (int k = N / 2; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        float s = a.m > -INFINITY ? a.s * ratio(o, offset(m)) : 0.f;
+        int at = a.m == m ? a.at : INT32_MAX;
+#pragma unroll
+        for (int k = N / 2; k >= 1; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+        return Part{m, s, __reduce_min_sync(0xffffffffu, at), __any_sync(0xffffffffu, a.bad)};
+    }
+    // the parts of a cluster as one, in every thread
+    __device__ __forceinline__ Part of_cluster(const Part* parts, int n) const {
+        const int i = threadIdx.x & 7;
+        const Part a = i < n ? parts[i] : Part{-INFINITY, 0.f, INT32_MAX, 0};
+        return joined<8>(a, offset(a.m));
     }
 };
 
@@ -91,15 +108,96 @@ __device__ __forceinline__ uint32_t shared_of(const void* p, uint32_t rank) {  /
     return r;
 }
 
-// Tried for rows of 131072: the run kept in registers between the passes (one exp an element, 64 registers and fewer threads in
-// flight: 158 us), and the maximum first and the sum after it.
+// one thread's part of a row
+template <bool kFar>
+struct Sum {
+    const Weights<kFar> w;
+    float m = -INFINITY, o = 0.f, s = 0.f;
+    int at = INT32_MAX;
+    bool bad = false;
+    __device__ __forceinline__ void raise(float top) {  // a new maximum
+        const float o2 = w.offset(top);
+        s = m > -INFINITY ? s * w.ratio(o, o2) : 0.f;
+        m = top;
+        o = o2;
+    }
+    template <int E>
+    __device__ __forceinline__ void take(const float (&f)[E], int v, bool greedy) {  // logits v .. v + E - 1
+        float top = f[0];
+#pragma unroll
+        for (int i = 1; i < E; ++i) top = fmaxf(top, f[i]);
+        if (top > m) {
+            raise(top);
+            if (greedy)
+#pragma unroll
+                for (int i = E - 1; i >= 0; --i)
+                    if (f[i] == top) at = v + i;
+        }
+        if (kFar)
+#pragma unroll
+            for (int i = 0; i < E; ++i) bad |= !(f[i] <= FLT_MAX);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            s0 += w(f[i], o);
+            s1 += w(f[i + 1], o);
+        }
+        s += s0 + s1;
+    }
+    __device__ __forceinline__ void take_one(float f, int v) {
+        if (f == m) at = min(at, v);
+        if (f > m) {
+            raise(f);
+            at = v;
+        }
+        bad |= kFar && !(f <= FLT_MAX);
+        s += w(f, o);
+    }
+    // the CTA's part, in every thread
+    __device__ __forceinline__ Part of_cta(Part* warps) const {
+        const int lane = threadIdx.x & 31;
+        const Part all = w.template joined<32>(Part{m, s, at, bad}, o);
+        if (lane == 0) warps[threadIdx.x >> 5] = all;
+        __syncthreads();
+        const Part mine = warps[lane % kProbWarps];
+        return w.template joined<kProbWarps>(mine, w.offset(mine.m));
+    }
+};
+
+__device__ __forceinline__ void put_part(uint32_t to, const Part& a) {  // into a CTA of the cluster
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(__float_as_uint(a.m)), "r"(__float_as_uint(a.s)),
+                 "r"(a.at), "r"(a.bad)
+                 : "memory");
+}
+
+// A CTA's run of a row: elements lo .. hi - 1, of them whole 16-byte pieces a .. b - 1 (by their addresses)
 template <typename InT>
-__global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const TokenProbsParams p, const int run) {
+struct RunOf {
+    static constexpr int EPC = 16 / sizeof(InT);
+    int lo, hi, a, b;
+    __device__ __forceinline__ RunOf(const InT* x, int V, int rank, int run) {
+        lo = (int)min((int64_t)rank * run, (int64_t)V);
+        hi = (int)min((int64_t)lo + run, (int64_t)V);
+        const int off = (int)((reinterpret_cast<uintptr_t>(x + lo) & 15u) / sizeof(InT));
+        a = min(hi, lo + (off == 0 ? 0 : EPC - off));
+        b = a + (hi - a) / EPC * EPC;
+    }
+    __device__ __forceinline__ int pieces() const { return (b - a) / EPC; }
+    __device__ __forceinline__ int edge() const { return (a - lo) + (hi - b); }  // elements in no piece
+    __device__ __forceinline__ int edge_at(int i) const { return i < a - lo ? lo + i : b + i - (a - lo); }
+};
+
+// Pieces in flight a thread and CTAs an SM: two and four for bf16, four and three for fp32 (us the other way about: 512 rows of 65536 bf16 42.7
+// against 39.8, 256 of 131072 fp32 61.5 against 58.3; CTAs of 256 and 1024 threads were slower).
+// Tried for rows of 131072: the run kept in registers between the passes (one exp an element, fewer threads in flight: 158 us then), the
+// maximum first and the sum after it, and a persistent cluster whose next run lands in shared memory meanwhile (104 us).
+template <typename InT>
+__global__ void __launch_bounds__(kProbThreads, sizeof(InT) == 2 ? 4 : 3) gdn_token_probs_kernel(const TokenProbsParams p, const int run) {
     constexpr int EPC = 16 / sizeof(InT);  // elements of a 16-byte piece
-    constexpr int U = 4;                   // pieces in flight a thread
+    constexpr int U = 16 / EPC;            // pieces in flight a thread
     __shared__ Part warps[2][kProbWarps];  // of the first pass, and of its repetition
     __shared__ Part parts[2][kProbMaxCluster];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int ncta = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
     const int64_t row = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (row >= (int64_t)p.B * p.T) return;  // the whole cluster leaves
@@ -110,27 +208,14 @@ __global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const 
     const float T = p.temperature[row / p.T];
     const bool greedy = T >= 0.f && T < FLT_MIN;
     const float c = 1.44269504f / (greedy ? 1.f : T);
-    // this CTA's elements lo .. hi - 1, of them whole pieces a .. b - 1
-    const int lo = (int)min((int64_t)rank * run, (int64_t)p.V), hi = (int)min((int64_t)lo + run, (int64_t)p.V);
-    const int off = (int)((reinterpret_cast<uintptr_t>(x + lo) & 15u) / sizeof(InT));
-    const int a = min(hi, lo + (off == 0 ? 0 : EPC - off)), b = a + (hi - a) / EPC * EPC;
+    const RunOf<InT> r(x, p.V, rank, run);
+    const int lo = r.lo, hi = r.hi, a = r.a, pieces = r.pieces(), edge = r.edge();
     const uint4* xv = reinterpret_cast<const uint4*>(x + a);
-    const int pieces = (b - a) / EPC;
-    const int edge = (a - lo) + (hi - b);  // elements in no piece
-    auto edge_at = [&](int i) { return i < a - lo ? lo + i : b + i - (a - lo); };
 
     auto first_pass = [&](auto wf) -> Part {
         constexpr bool kFar = sizeof(wf) != sizeof(float);
         const Weights<kFar> w{c};
-        float m = -INFINITY, o = 0.f, s = 0.f;
-        int at = INT32_MAX;
-        bool bad = false;
-        auto raise = [&](float top) {  // a new maximum
-            const float o2 = w.offset(top);
-            s = m > -INFINITY ? s * w.ratio(o, o2) : 0.f;
-            m = top;
-            o = o2;
-        };
+        Sum<kFar> sum{w};
         for (int c0 = tid; c0 < pieces; c0 += U * kProbThreads) {
             uint4 raw[U];
 #pragma unroll
@@ -141,62 +226,16 @@ __global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const 
                 if (c0 + u * kProbThreads >= pieces) break;
                 float f[EPC];
                 unpack16(raw[u], f);
-                float top = f[0];
-#pragma unroll
-                for (int i = 1; i < EPC; ++i) top = fmaxf(top, f[i]);
-                if (top > m) {
-                    raise(top);
-                    if (greedy)
-#pragma unroll
-                        for (int i = EPC - 1; i >= 0; --i)
-                            if (f[i] == top) at = a + (c0 + u * kProbThreads) * EPC + i;
-                }
-                if (kFar)
-#pragma unroll
-                    for (int i = 0; i < EPC; ++i) bad |= !(f[i] <= FLT_MAX);
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int i = 0; i < EPC; i += 2) {
-                    s0 += w(f[i], o);
-                    s1 += w(f[i + 1], o);
-                }
-                s += s0 + s1;
+                sum.take(f, a + (c0 + u * kProbThreads) * EPC, greedy);
             }
         }
-        if (tid < edge) {  // the ends, one element a thread
-            const int v = edge_at(tid);
-            const float f = as_f32(x[v]);
-            if (f == m) at = min(at, v);
-            if (f > m) {
-                raise(f);
-                at = v;
-            }
-            bad |= kFar && !(f <= FLT_MAX);
-            s += w(f, o);
-        }
-        Part all{m, s, at, bad};
-#pragma unroll
-        for (int k = 16; k >= 1; k >>= 1)
-            w.join(all, Part{__shfl_xor_sync(0xffffffffu, all.m, k), __shfl_xor_sync(0xffffffffu, all.s, k),
-                             __shfl_xor_sync(0xffffffffu, all.at, k), __shfl_xor_sync(0xffffffffu, all.bad, k)});
-        if (lane == 0) warps[kFar][warp] = all;
-        __syncthreads();
-        all = warps[kFar][lane % kProbWarps];
-#pragma unroll
-        for (int k = kProbWarps / 2; k >= 1; k >>= 1)
-            w.join(all, Part{__shfl_xor_sync(0xffffffffu, all.m, k), __shfl_xor_sync(0xffffffffu, all.s, k),
-                             __shfl_xor_sync(0xffffffffu, all.at, k), __shfl_xor_sync(0xffffffffu, all.bad, k)});
+        if (tid < edge) sum.take_one(as_f32(x[r.edge_at(tid)]), r.edge_at(tid));
+        Part all = sum.of_cta(warps[kFar]);
         if (ncta > 1) {  // every CTA puts its part into every other's shared memory
             if (!kFar) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-            if (tid < ncta) {
-                const uint32_t to = shared_of(&parts[kFar][rank], (uint32_t)tid);
-                asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(__float_as_uint(all.m)),
-                             "r"(__float_as_uint(all.s)), "r"(all.at), "r"(all.bad)
-                             : "memory");
-            }
+            if (tid < ncta) put_part(shared_of(&parts[kFar][rank], (uint32_t)tid), all);
             asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-            all = parts[kFar][0];
-            for (int r = 1; r < ncta; ++r) w.join(all, parts[kFar][r]);
+            all = w.of_cluster(parts[kFar], ncta);
         }
         return all;
     };
@@ -215,24 +254,24 @@ __global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const 
         const Weights<sizeof(wf) != sizeof(float)> w{c};
         const float o = w.offset(all.m), f = 1.f / all.s;
         if ((reinterpret_cast<uintptr_t>(y + a) & 15u) == 0) {
-            for (int c0 = tid; c0 < pieces; c0 += U * kProbThreads) {
-                uint4 raw[U];
+            // four numbers a thread and store: a warp writes whole lines (eight as two stores leave half sectors: 98 us against 75)
+            const Four<InT>* x4 = reinterpret_cast<const Four<InT>*>(x + a);
+            const int fours = pieces * (EPC / 4);
+            constexpr int U4 = U * EPC / 4;
+            for (int c0 = tid; c0 < fours; c0 += U4 * kProbThreads) {
+                Four<InT> raw[U4];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + u * kProbThreads < pieces) raw[u] = xv[c0 + u * kProbThreads];
+                for (int u = 0; u < U4; ++u)
+                    if (c0 + u * kProbThreads < fours) raw[u] = x4[c0 + u * kProbThreads];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (c0 + u * kProbThreads >= pieces) break;
-                    float e[EPC];
-                    unpack16(raw[u], e);
-                    float4* dst = reinterpret_cast<float4*>(y + a + (c0 + u * kProbThreads) * EPC);
-#pragma unroll
-                    for (int i = 0; i < EPC; i += 4)
-                        __stcs(dst + i / 4, make_float4(w(e[i], o) * f, w(e[i + 1], o) * f, w(e[i + 2], o) * f,
-                                                        w(e[i + 3], o) * f));
+                for (int u = 0; u < U4; ++u) {
+                    if (c0 + u * kProbThreads >= fours) break;
+                    const float4 e = as_f32(raw[u]);
+                    __stcs(reinterpret_cast<float4*>(y + a) + c0 + u * kProbThreads,
+                           make_float4(w(e.x, o) * f, w(e.y, o) * f, w(e.z, o) * f, w(e.w, o) * f));
                 }
             }
-            if (tid < edge) y[edge_at(tid)] = w(as_f32(x[edge_at(tid)]), o) * f;
+            if (tid < edge) y[r.edge_at(tid)] = w(as_f32(x[r.edge_at(tid)]), o) * f;
         } else {  // the places of x and y differ: neighbours a warp
             for (int v0 = lo + tid; v0 < hi; v0 += 8 * kProbThreads) {
                 InT raw[8];
@@ -254,9 +293,9 @@ __global__ void __launch_bounds__(kProbThreads, 3) gdn_token_probs_kernel(const 
 template <typename InT>
 cudaError_t launch_t(const TokenProbsParams& p, cudaStream_t s) {
     const int64_t rows = (int64_t)p.B * p.T;
-    // CTAs a row.  Runs of up to 32768 elements where rows fill the GPU (512 rows of 131072 bf16: 4 CTAs 96 us, 2 98, 8 122; of 32768:
-    // 1 CTA 25 us, 2 30, 4 41: a CTA's start and the exchange cost some microseconds), of 4096 where they do not (one row of 131072:
-    // 8 CTAs 9.0 us, 4 12.7, 1 27.6)
+    // CTAs a row.  Runs of up to 32768 elements where rows fill the GPU (512 rows of 131072 bf16: 4 CTAs 75 us, 2 81, 8 87; of 32768:
+    // 1 CTA 19 us, 2 23, 4 30: a CTA's start and the exchange cost some microseconds), of 4096 where they do not (one row of 131072:
+    // 8 CTAs 6.7 us, 4 8.7, 1 20.5)
     int ncta = 1;
     while (ncta < kProbMaxCluster && ((int64_t)p.V > (int64_t)ncta * 32768 || (rows * ncta < 152 && p.V > ncta * 4096))) ncta *= 2;
     const int run = (int)(((int64_t)p.V + ncta * 64 - 1) / (ncta * 64) * 64);
