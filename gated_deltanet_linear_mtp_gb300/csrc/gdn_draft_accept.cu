@@ -131,51 +131,68 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
     const int tiles = (V + tile - 1) / tile, first = rank * per, mine = max(0, min(per, tiles - first));
     bool bad = false;
     double before = 0., total = 0., own = 0.;  // sums of the CTAs before this one, of all, of this one
-    // tile k's sum; false where a value is not finite (kChecked: never)
-    auto tile_sum = [&](auto checked, int k, float2& acc) -> bool {
-        constexpr bool kChecked = sizeof(checked) > 1;
-        acc = make_float2(0.f, 0.f);
-        float2 probe = make_float2(0.f, 0.f);
-        const int end = min(V, (first + k + 1) * tile);
-        float pv[8], qv[8];  // the next block's loads are in flight meanwhile
-        auto load = [&](int v0, float (&pb)[8], float (&qb)[8]) {
+    auto load = [&](int v0, int end, float (&pb)[8], float (&qb)[8]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int v = v0 + 32 * i + lane;
-                pb[i] = v < end ? r.p[v] : 0.f;
-                qb[i] = r.q != nullptr && v < end ? r.q[v] : 0.f;
-            }
-        };
-        int v0 = (first + k) * tile;
-        load(v0, pv, qv);
-        for (; v0 < end; v0 += kAcceptBlock) {
+        for (int i = 0; i < 8; ++i) {
+            const int v = v0 + 32 * i + lane;
+            pb[i] = v < end ? r.p[v] : 0.f;
+            qb[i] = r.q != nullptr && v < end ? r.q[v] : 0.f;
+        }
+    };
+    // a block's sum goes to acc; probe stays 0 while values are finite (kChecked: those that are not count as nothing)
+    auto add_block = [&](auto checked, int v0, const float (&pc)[8], float (&qc)[8], float2& acc, float2& probe) {
+        constexpr bool kChecked = sizeof(checked) > 1;
+        if (r.certain >= v0 && r.certain < v0 + kAcceptBlock)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (v0 + 32 * i + lane == r.certain) qc[i] = 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!kChecked) probe = __ffma2_rn(make_float2(pc[i], qc[i]), make_float2(0.f, 0.f), probe);
+            add_pair(acc, residual<kChecked>(pc[i], qc[i]));
+        }
+    };
+    for (int pass = 0; pass < 2; ++pass) {
+        // the warp's tiles, a block at a time, with the next block's loads in flight, be it of the same tile or of the next one
+        int k = warp, v0 = 0, end = 0;
+        float pv[8], qv[8];
+        if (k < mine) {
+            v0 = (first + k) * tile;
+            end = V - v0 > tile ? v0 + tile : V;
+            load(v0, end, pv, qv);
+        }
+        float2 acc = make_float2(0.f, 0.f), probe = acc;
+        while (k < mine) {
             float pc[8], qc[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) pc[i] = pv[i], qc[i] = qv[i];
-            if (v0 + kAcceptBlock < end) load(v0 + kAcceptBlock, pv, qv);
-            if (r.certain >= v0 && r.certain < v0 + kAcceptBlock)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (v0 + 32 * i + lane == r.certain) qc[i] = 1.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!kChecked) probe = __ffma2_rn(make_float2(pc[i], qc[i]), make_float2(0.f, 0.f), probe);
-                add_pair(acc, residual<kChecked>(pc[i], qc[i]));
+            int k2 = k, v2 = v0, end2 = end;
+            if (end - v0 > kAcceptBlock) {
+                v2 += kAcceptBlock;
+            } else if ((k2 += kAcceptWarps) < mine) {
+                v2 = (first + k2) * tile;
+                end2 = V - v2 > tile ? v2 + tile : V;
             }
-        }
-        return kChecked || (probe.x == 0.f && probe.y == 0.f);
-    };
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int k = warp; k < mine; k += kAcceptWarps) {
-            float2 acc;
-            if (!__all_sync(0xffffffffu, tile_sum(char{}, k, acc))) {
-                bad = true;
-                tile_sum(int{}, k, acc);
-            }
+            if (k2 < mine) load(v2, end2, pv, qv);
+            add_block(char{}, v0, pc, qc, acc, probe);
+            if (k2 != k) {
+                if (!__all_sync(0xffffffffu, probe.x == 0.f && probe.y == 0.f)) {  // the tile again, with checks
+                    bad = true;
+                    acc = make_float2(0.f, 0.f);
+                    for (int v = (first + k) * tile; v < end; v += min(kAcceptBlock, end - v)) {
+                        load(v, end, pc, qc);
+                        add_block(int{}, v, pc, qc, acc, probe);
+                    }
+                }
 #pragma unroll
-            for (int m = 16; m >= 1; m >>= 1)
-                add_pair(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, m), __shfl_xor_sync(0xffffffffu, acc.y, m)));
-            if (lane == 0) sums[k] = acc;
+                for (int m = 16; m >= 1; m >>= 1)
+                    add_pair(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, m), __shfl_xor_sync(0xffffffffu, acc.y, m)));
+                if (lane == 0) sums[k] = acc;
+                acc = probe = make_float2(0.f, 0.f);
+            }
+            k = k2;
+            v0 = v2;
+            end = end2;
         }
         __syncthreads();
         // every warp forms the same sums, in the same order
@@ -290,7 +307,7 @@ cudaError_t launch_draft_accept(const DraftAcceptParams& p, cudaStream_t s) {
     // tiles of two blocks where a warp has at least four of them: the warp's sum is formed once a tile (512 against 256: 62 and 69 us,
     // 15 and 17 for the one lane), of one where it has fewer (one lane of 50001: 13 against 15)
     int tile = kAcceptBlock;
-    if ((int64_t)p.V > (int64_t)tile * kAcceptWarps * ncta * 4) tile *= 2;
+    if ((int64_t)p.V > (int64_t)tile * kAcceptWarps * ncta * 8) tile *= 2;
     while ((int64_t)tile * kAcceptTiles * ncta < p.V) tile *= 2;
     const int tiles = (p.V + tile - 1) / tile, per = (tiles + ncta - 1) / ncta;
     cudaLaunchConfig_t cfg = {};
