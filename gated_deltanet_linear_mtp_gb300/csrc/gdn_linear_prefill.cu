@@ -124,16 +124,34 @@ __global__ void __launch_bounds__(kLThreads, 1)
     constexpr int NP = std::is_same<StT, float>::value ? 3 : 2;  // parts of V'
     using PL = LinearPlan<DK, NP>;
     const int ndv = (p.DV + kLDv - 1) / kLDv;
-    const int item = blockIdx.x, tile = item % ndv, h = item / ndv % p.HV, b = item / (ndv * p.HV);
+    const int item = blockIdx.x, tile = item % ndv, h = item / ndv % p.HV, turn = item / (ndv * p.HV);
     const int dv0 = tile * kLDv, hk = h / (p.HV / p.HK);
     const int tid = threadIdx.x, warp = __reduce_min_sync(0xffffffffu, tid >> 5), lt = tid & 127;
     const int hf = (warp >> 2) & 1, wl = warp & 3;  // half of a group, and the warp's quarter of the lanes
 
-    // everything that tells what to do is asked for at once
-    const int slot = p.indices[b];
-    const int out = p.out_indices != nullptr ? p.out_indices[b] : slot;
-    const int lo = p.cu_seqlens[b], hi = p.cu_seqlens[b + 1];
-    const bool init = p.has_init == nullptr || p.has_init[b] != 0;
+    // Everything that tells what to do is asked for at once.  Of up to 32 whole prompts a lane asks for one each, and the longest is
+    // taken first, so that no long one is left for the end.  (HV 32, D 64: 32 prompts of 17 to 2048 131 us against 141 in the order of the
+    // lanes, 8 of 17 to 8192 138 against 154; 32 of 1024 each 156 against 150, for the longer start.)
+    const bool sorted = piece == 0 && p.B > 1 && p.B <= 32;
+    int b = sorted ? min(tid & 31, p.B - 1) : turn;
+    int slot = p.indices[b];
+    int out = p.out_indices != nullptr ? p.out_indices[b] : slot;
+    int lo = p.cu_seqlens[b], hi = p.cu_seqlens[b + 1];
+    int has = p.has_init == nullptr ? 1 : p.has_init[b];
+    if (sorted) {
+        const uint32_t key = ((uint32_t)min(max(hi - lo, 0), (1 << 26) - 1) << 5) | (31u - (tid & 31));
+        b = turn;
+        if (!__all_sync(0xffffffffu, (key >> 5) == __shfl_sync(0xffffffffu, key >> 5, 0))) {
+            int before = 0;
+            for (int i = 0; i < p.B; ++i) before += __shfl_sync(0xffffffffu, key, i) > key;
+            b = __ffs(__ballot_sync(0xffffffffu, (tid & 31) < p.B && before == turn)) - 1;
+        }
+    }
+    const auto of_b = [&](int x) {  // the value of lane b where lanes have their own (a uniform register in either case)
+        return __reduce_max_sync(0xffffffffu, !sorted || (tid & 31) == b ? x : INT32_MIN);
+    };
+    slot = of_b(slot), out = of_b(out), lo = of_b(lo), hi = of_b(hi), has = of_b(has);
+    const bool init = has != 0;
     const float ld = p.log_decay[h];
     const bool reporter = !kState && p.err != nullptr && tid == 0;
     if (slot == -1) return;

@@ -527,3 +527,50 @@ def test_tensors_that_the_binding_refuses():
         gdn.gdn_linear_decode(*ok, out_indices=c.read[:1])
     with pytest.raises(gdn.GdnError):
         gdn.gdn_linear_decode(*ok, scale=math.inf)
+
+
+@pytest.mark.parametrize("B", [2, 31, 32, 33])
+def test_prompts_of_many_lengths(B):
+    """Up to 32 prompts are taken from the longest to the shortest: each is served once, equal and empty ones among them."""
+    lens = [(b * 37) % 150 for b in range(B - 1)] + [260]
+    if B > 4:
+        lens[3] = lens[2] = 0
+        lens[-2] = lens[0] = lens[1]
+    prompts(lens, 1, 2, 64, 72, "bf16", "f32", seed=B)
+    prompts([130] * B, 1, 1, 128, 64, "bf16", "bf16", seed=B)
+
+
+def test_bad_prompts_between_good_ones_of_many_lengths():
+    """Padded lanes and bad bounds keep their place in the order: the prompts beside them get their results."""
+    lens = [100, 5, 300, 40, 129]
+    c = Case((sum(lens),), 5, 1, 2, 64, 64, seed=9)
+    cu = torch.zeros(6, dtype=torch.int64)
+    cu[1:] = torch.cumsum(torch.tensor(lens), 0)
+    ws = gdn.linear_prefill_workspace(sum(lens), 5, 2, 64, 64)
+    before = c.pool.clone()
+    c.read[1], c.read[3] = -1, c.slots
+    gdn.gdn_linear_prefill(c.q, c.k, c.v, c.ld, c.pool, c.read, cu.to(**I32), c.o, ws, None, c.err, out_indices=c.write, scale=c.scale)
+    assert int(c.err) == gdn.ERRBIT_INDEX
+    for b in range(5):
+        at = slice(int(cu[b]), int(cu[b + 1]))
+        if b in (1, 3):
+            assert bool((c.o[at] == CANARY).all()) and torch.equal(c.pool[c.write[b]], before[c.write[b]])
+            continue
+        o, s, oa, sa = c.ref(before[c.read[b]], at)
+        near(c.o[at], o, oa, 2.0 ** -8, "o")
+        near(c.pool[c.write[b]], s[-1], sa[-1], 2.0 ** -16, "state")
+    # a bound beyond the tokens, and one that goes back
+    c.err.zero_()
+    c.read[1], c.read[3] = 0, 1
+    cu[5], cu[1] = sum(lens) + 7, 200
+    before = c.pool.clone()
+    gdn.gdn_linear_prefill(c.q, c.k, c.v, c.ld, c.pool, torch.arange(5, **I32), cu.to(**I32), c.o, ws, None, c.err,
+                           out_indices=torch.arange(5, 10, **I32), scale=c.scale)
+    assert int(c.err) == gdn.ERRBIT_SEQLEN
+    for b in (2, 3):
+        o, s, oa, sa = c.ref(before[b], slice(int(cu[b]), int(cu[b + 1])))
+        alone = max(0, 200 - int(cu[b]))  # by these bounds the first prompt has tokens 0 .. 199 too, so o there is of either
+        near(c.o[int(cu[b]) + alone:int(cu[b + 1])], o[alone:], oa[alone:], 2.0 ** -8, "o")
+        near(c.pool[5 + b], s[-1], sa[-1], 2.0 ** -16, "state")
+    for b in (1, 4):
+        assert torch.equal(c.pool[5 + b], before[5 + b])
