@@ -37,10 +37,9 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
     return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
 
-// r = max(p - q, 0) of one token as an exact pair.  kChecked: values that are not finite count as nothing.
-template <bool kChecked>
+// r = max(p - q, 0) of one token as an exact pair; values that are not finite count as nothing
 __device__ __forceinline__ float2 residual(float p, float q) {
-    if (kChecked && (!(fabsf(p) <= FLT_MAX) || !(fabsf(q) <= FLT_MAX))) return make_float2(0.f, 0.f);
+    if (!(fabsf(p) <= FLT_MAX) || !(fabsf(q) <= FLT_MAX)) return make_float2(0.f, 0.f);
     const float s = p - q;
     const float2 r = make_float2(s, (p - s) - q);  // exact, since |p| >= |q|
     return p > q ? r : make_float2(0.f, 0.f);
@@ -51,7 +50,7 @@ struct RowPair {
     const float* q;  // nullptr: q is 1 at `certain` and 0 elsewhere
     int certain;     // -1: nowhere
     __device__ __forceinline__ float2 at(int v) const {
-        return residual<true>(p[v], q != nullptr ? q[v] : (v == certain ? 1.f : 0.f));
+        return residual(p[v], q != nullptr ? q[v] : (v == certain ? 1.f : 0.f));
     }
 };
 
@@ -69,6 +68,24 @@ __device__ __forceinline__ void add_pair(float2& a, float2 b) {
     const float2 s = two_sum(a.x, b.x);
     a = make_float2(s.x, s.y + (a.y + b.y));
 }
+
+// Two sums of max(p - q, 0) beside each other, each a pair of floats, with packed instructions (two tokens' share of each).
+struct TwoSums {
+    float2 hi = make_float2(0.f, 0.f), lo = make_float2(0.f, 0.f);
+    __device__ __forceinline__ static float2 minus(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }  // rounded once
+    __device__ __forceinline__ void add(float2 p, float2 q) {
+        q = make_float2(fminf(p.x, q.x), fminf(p.y, q.y));  // nothing where q is the larger
+        const float2 s = minus(p, q), e = minus(minus(p, s), q);  // exact, since |p| >= |q|
+        const float2 t = __fadd2_rn(hi, s), u = minus(t, hi);
+        lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(minus(hi, minus(t, u)), minus(s, u)), e));
+        hi = t;
+    }
+    __device__ __forceinline__ float2 both() const {
+        float2 a = make_float2(hi.x, lo.x);
+        add_pair(a, make_float2(hi.y, lo.y));
+        return a;
+    }
+};
 
 __device__ __forceinline__ uint32_t shared_of(const void* p, uint32_t rank) {  // the same variable in another CTA of the cluster
     uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
@@ -132,25 +149,25 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
     bool bad = false;
     double before = 0., total = 0., own = 0.;  // sums of the CTAs before this one, of all, of this one
     auto load = [&](int v0, int end, float (&pb)[8], float (&qb)[8]) {
+        const float* pp = r.p + v0 + lane;
+        const float* qq = r.q + v0 + lane;
+        if (end - v0 >= kAcceptBlock) {  // a whole block: no bounds a number
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int v = v0 + 32 * i + lane;
-            pb[i] = v < end ? r.p[v] : 0.f;
-            qb[i] = r.q != nullptr && v < end ? r.q[v] : 0.f;
+            for (int i = 0; i < 8; ++i) pb[i] = pp[32 * i];
+            if (r.q != nullptr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) qb[i] = qq[32 * i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = v0 + 32 * i + lane < end;
+                pb[i] = in ? pp[32 * i] : 0.f;
+                qb[i] = in && r.q != nullptr ? qq[32 * i] : 0.f;
+            }
         }
-    };
-    // a block's sum goes to acc; probe stays 0 while values are finite (kChecked: those that are not count as nothing)
-    auto add_block = [&](auto checked, int v0, const float (&pc)[8], float (&qc)[8], float2& acc, float2& probe) {
-        constexpr bool kChecked = sizeof(checked) > 1;
-        if (r.certain >= v0 && r.certain < v0 + kAcceptBlock)
+        if (r.q == nullptr)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (v0 + 32 * i + lane == r.certain) qc[i] = 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (!kChecked) probe = __ffma2_rn(make_float2(pc[i], qc[i]), make_float2(0.f, 0.f), probe);
-            add_pair(acc, residual<kChecked>(pc[i], qc[i]));
-        }
+            for (int i = 0; i < 8; ++i) qb[i] = v0 + 32 * i + lane == r.certain ? 1.f : 0.f;
     };
     for (int pass = 0; pass < 2; ++pass) {
         // the warp's tiles, a block at a time, with the next block's loads in flight, be it of the same tile or of the next one
@@ -161,7 +178,8 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
             end = V - v0 > tile ? v0 + tile : V;
             load(v0, end, pv, qv);
         }
-        float2 acc = make_float2(0.f, 0.f), probe = acc;
+        TwoSums acc;
+        float2 probe = make_float2(0.f, 0.f);  // stays 0 while values are finite
         while (k < mine) {
             float pc[8], qc[8];
 #pragma unroll
@@ -174,21 +192,29 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
                 end2 = V - v2 > tile ? v2 + tile : V;
             }
             if (k2 < mine) load(v2, end2, pv, qv);
-            add_block(char{}, v0, pc, qc, acc, probe);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 p2 = make_float2(pc[i], pc[i + 1]), q2 = make_float2(qc[i], qc[i + 1]);
+                probe = __ffma2_rn(q2, make_float2(0.f, 0.f), __ffma2_rn(p2, make_float2(0.f, 0.f), probe));
+                acc.add(p2, q2);
+            }
             if (k2 != k) {
-                if (!__all_sync(0xffffffffu, probe.x == 0.f && probe.y == 0.f)) {  // the tile again, with checks
+                float2 sum = acc.both();
+                if (!__all_sync(0xffffffffu, probe.x == 0.f && probe.y == 0.f)) {  // again, where a value that is not finite counts as nothing
                     bad = true;
-                    acc = make_float2(0.f, 0.f);
+                    sum = make_float2(0.f, 0.f);
                     for (int v = (first + k) * tile; v < end; v += min(kAcceptBlock, end - v)) {
                         load(v, end, pc, qc);
-                        add_block(int{}, v, pc, qc, acc, probe);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) add_pair(sum, residual(pc[i], qc[i]));
                     }
                 }
 #pragma unroll
                 for (int m = 16; m >= 1; m >>= 1)
-                    add_pair(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, m), __shfl_xor_sync(0xffffffffu, acc.y, m)));
-                if (lane == 0) sums[k] = acc;
-                acc = probe = make_float2(0.f, 0.f);
+                    add_pair(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, m), __shfl_xor_sync(0xffffffffu, sum.y, m)));
+                if (lane == 0) sums[k] = sum;
+                acc = TwoSums();
+                probe = make_float2(0.f, 0.f);
             }
             k = k2;
             v0 = v2;
