@@ -11,8 +11,8 @@
 //
 // Bytes bound it: of all the rows a lane reads T - 1 numbers of p and of q, and then one row of each.  A cluster takes a lane:
 // its CTAs' warps sum tiles of the row, the CTAs put their sums into each other's shared memory, and a warp of the one that the
-// threshold falls into finds the tile and reads that tile again.  256 lanes (a tenth padded) of 131072 with draft probabilities: 61 us,
-// 4.0 TB/s; one lane 12 us a call.
+// threshold falls into finds the tile and reads that tile again.  256 lanes (a tenth padded) of 131072 with draft probabilities: 55 us,
+// 4.4 TB/s; one lane 12 us a call.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -25,8 +25,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kAcceptThreads = 256;
-constexpr int kAcceptWarps = kAcceptThreads / 32;
+constexpr int kAcceptThreads = 256;  // of a CTA at most
 constexpr int kAcceptBlock = 256;     // elements that a warp sums at a time: 8 a lane
 constexpr int kAcceptTiles = 1024;    // tiles of a CTA's part of a row at most
 constexpr int kAcceptMaxCluster = 8;
@@ -104,7 +103,7 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
     __shared__ double part[2][kAcceptMaxCluster];  // the CTAs' sums, of either pass
     __shared__ int sh_n;
     __shared__ bool sh_refused;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.T, V = p.V;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, T = p.T, V = p.V;
     const int ncta = gridDim.x, rank = blockIdx.x, b = blockIdx.y;
     const int32_t* drafts = p.drafts + (int64_t)b * (T - 1);
     const int slot = p.indices != nullptr ? p.indices[b] : 0;
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
             int k2 = k, v2 = v0, end2 = end;
             if (end - v0 > kAcceptBlock) {
                 v2 += kAcceptBlock;
-            } else if ((k2 += kAcceptWarps) < mine) {
+            } else if ((k2 += warps) < mine) {
                 v2 = (first + k2) * tile;
                 end2 = V - v2 > tile ? v2 + tile : V;
             }
@@ -326,19 +325,25 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
 }  // namespace
 
 cudaError_t launch_draft_accept(const DraftAcceptParams& p, cudaStream_t s) {
-    // CTAs a lane: parts of up to 65536 tokens where lanes fill the GPU (256 lanes of 131072: 2 CTAs 62 us, 4 66, 8 78, 1 100; a CTA's start
-    // and the search cost some microseconds), of 2048 where they do not (one lane of 131072: 8 CTAs 15 us, 4 19, 2 27)
+    // Lanes that fill the GPU: CTAs of 128 threads, up to four a lane (two where lanes alone are 512), of which eight share an SM and some
+    // read while others start, exchange and search.  Fewer lanes: 256 threads, as many CTAs as fill the GPU.  us in graph replays with draft
+    // probabilities, the second form / the first: 128 lanes of 131072 32.4 / 38.3, 160 47.6 / 42.1, 256 54.6 / 50.6; 256 of 5000 12.1 / 9.5;
+    // 512 of 32000 with four CTAs a lane 31.4 / 34.4.  (One lane of 131072: 8 CTAs 15 us a call, 4 19, 2 27.)
+    const bool many = p.B >= 152;
+    const int warps = many ? 4 : 8;
     int ncta = 1;
-    while (ncta < kAcceptMaxCluster && ((int64_t)p.V > (int64_t)ncta * 65536 || ((int64_t)p.B * ncta < 456 && p.V > ncta * 2048))) ncta *= 2;
-    // tiles of two blocks where a warp has at least four of them: the warp's sum is formed once a tile (512 against 256: 62 and 69 us,
-    // 15 and 17 for the one lane), of one where it has fewer (one lane of 50001: 13 against 15)
+    if (many)
+        while (ncta < 4 && p.V > ncta * 8192 && (int64_t)p.B * ncta < 1024) ncta *= 2;
+    else
+        while (ncta < kAcceptMaxCluster && ((int64_t)p.V > (int64_t)ncta * 65536 || ((int64_t)p.B * ncta < 456 && p.V > ncta * 2048))) ncta *= 2;
+    // tiles of two blocks where a warp has more than eight blocks: its sum is formed once a tile (256 lanes of 131072: 59 us against 63)
     int tile = kAcceptBlock;
-    if ((int64_t)p.V > (int64_t)tile * kAcceptWarps * ncta * 8) tile *= 2;
+    if ((int64_t)p.V > (int64_t)tile * warps * ncta * 8) tile *= 2;
     while ((int64_t)tile * kAcceptTiles * ncta < p.V) tile *= 2;
     const int tiles = (p.V + tile - 1) / tile, per = (tiles + ncta - 1) / ncta;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ncta, (unsigned)p.B);
-    cfg.blockDim = dim3(kAcceptThreads);
+    cfg.blockDim = dim3(32u * (unsigned)warps);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

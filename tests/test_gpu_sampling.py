@@ -137,6 +137,13 @@ def test_accept(B, T, V, probs):
         x.check()
 
 
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("B,T,V", [(151, 2, 9001), (160, 3, 40000), (512, 2, 20001), (1100, 1, 9000)])
+def test_accept_of_many_lanes(B, T, V, probs):
+    """Lanes that fill the GPU: smaller CTAs, one, two or four a lane."""
+    test_accept(B, T, V, probs)
+
+
 def test_accept_flat_and_peaked():
     """Flat probabilities put every threshold next to a border; a row of one token has one."""
     for seed in range(4):
