@@ -13,7 +13,8 @@
 // exp((x - m) / T) = 2^(c x - o), c = log2(e) / T and o = c m rounded: one multiply-add that rounds its result alone, and a
 // common error of o that the division by the sum takes out again.  ex2.approx.ftz adds 2^-22 and takes what is below 2^-126 as 0.
 // That needs |o| <= 2^20 (o's error stays below 1/16): a row whose largest logit lies beyond, one with NaN or +inf, and one
-// whose largest entries are the type's lowest value go through the first pass again with differences x - m, and checks.
+// whose largest entries are the type's lowest value go through the first pass again with differences x - m, and checks.  NaN is no
+// maximum, so the sum alone carries it: also that of a thread, warp or CTA which has met nothing but NaN and -inf.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -88,7 +89,7 @@ struct Weights {
         float m = a.m;
 #pragma unroll
         for (int k = N / 2; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-        float s = a.m > -INFINITY ? a.s * ratio(o, offset(m)) : 0.f;
+        float s = a.m > -INFINITY ? a.s * ratio(o, offset(m)) : a.s;  // without a maximum: 0, or NaN, which stays
         int at = a.m == m ? a.at : INT32_MAX;
 #pragma unroll
         for (int k = N / 2; k >= 1; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
@@ -117,7 +118,7 @@ struct Sum {
     bool bad = false;
     __device__ __forceinline__ void raise(float top) {  // a new maximum
         const float o2 = w.offset(top);
-        s = m > -INFINITY ? s * w.ratio(o, o2) : 0.f;
+        s = m > -INFINITY ? s * w.ratio(o, o2) : s;  // 0 before the first logit above -inf, or NaN, which stays
         m = top;
         o = o2;
     }
