@@ -103,7 +103,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {  // w
         : "memory");
     return done != 0;
 }
-// What a wait does after its first try, out of line: the code that runs once a chunk stays short
+// What a wait of one thread does after its first try, out of line: the code that runs once a chunk stays short
 __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t fail) {
     for (uint32_t k = 0; k < kLPolls; ++k) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -111,6 +111,20 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t f
             int f;
             asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(f) : "r"(fail) : "memory");
             if (f != 0) return false;
+        }
+    }
+    asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(fail) : "memory");
+    return false;
+}
+// The same of a whole warp, each lane for its barrier.  Every branch goes by a vote: products, commits and tensor memory's loads and stores
+// are instructions of the warp, and a warp whose lanes left a wait one after the other would issue them once for each part of it.
+__device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, uint32_t fail) {
+    for (uint32_t k = 0; k < kLPolls; ++k) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((k & 255u) == 255u) {
+            int f;
+            asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(f) : "r"(fail) : "memory");
+            if (__any_sync(0xffffffffu, f != 0)) return false;
         }
     }
     asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(fail) : "memory");
@@ -222,10 +236,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     auto u_col = [&](int c) -> uint32_t { return kState && (c & 1) ? kScCol : kUCol; };
     // bounded: a wait that runs out marks the CTA as failed, which ends every other wait of it
-    auto wait = [&](int i, uint32_t parity) -> bool {
+    auto wait = [&](int i, uint32_t parity) -> bool {  // of one thread
         return mbar_try_wait(bar(i), parity) || wait_more(bar(i), parity, smem_u32(const_cast<int*>(fail)));
     };
-    auto warp_wait = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(i, parity)); };
+    auto warp_wait = [&](int i, uint32_t parity) -> bool {  // of a whole warp
+        return __all_sync(0xffffffffu, mbar_try_wait(bar(i), parity)) ||
+               warp_wait_more(bar(i), parity, smem_u32(const_cast<int*>(fail)));
+    };
 
     if (warp < 8) {
         // ============ thread = row i of the chunk: P from the scores ============
@@ -449,9 +466,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
             const int before = kState ? c - 2 : c - 1;  // the chunk whose V' was where this one's goes
             for (uint32_t polls = 0; polls < kLPolls; ++polls) {  // what has not come by then is waited for below
                 // V' goes over another chunk's, which the update has read then; of a partial chunk K's rows are cleared too
-                const bool there = mbar_test(bar(kVFull + (c & 1)), parity) &&
-                                   (before < 0 || mbar_test(bar(kUFull + (before & 1)), (uint32_t)(before >> 1) & 1u)) &&
-                                   (m == kLC || mbar_test(bar(kQkFull + (c & 1)), parity));
+                bool there = mbar_test(bar(kVFull + (c & 1)), parity);
+                if (before >= 0) there &= mbar_test(bar(kUFull + (before & 1)), (uint32_t)(before >> 1) & 1u);
+                if (m < kLC) there &= mbar_test(bar(kQkFull + (c & 1)), parity);
                 if (__all_sync(0xffffffffu, there)) break;
                 if (o_left && __all_sync(0xffffffffu, mbar_test(bar(kOFull), (uint32_t)(c - 1) & 1u))) {
                     ok = write_o(c - 1);
@@ -544,9 +561,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
         constexpr uint32_t kBn = 1u << 16, kAm = 1u << 15;  // B N-major, A M-major
         constexpr uint32_t id64 = umma_idesc_bf16(128, kLDv);
         const int ln = tid & 31;
-        auto all_over = [&](int b0, int c0, int b1, int c1, int b2, int c2) -> bool {  // phase c of barrier b, c < 0: none
-            const int b = ln == 0 ? b0 : ln == 1 ? b1 : b2, c = ln == 0 ? c0 : ln == 1 ? c1 : c2;
-            return __all_sync(0xffffffffu, c < 0 || wait(b, (uint32_t)c & 1u));
+        auto all_over = [&](int b0, int c0, int b1, int c1, int b2, int c2) -> bool {  // phase c of barrier b, c1 and c2 < 0: none
+            const bool one = ln == 1 && c1 >= 0, two = ln == 2 && c2 >= 0;
+            return warp_wait(one ? b1 : two ? b2 : b0, (uint32_t)(one ? c1 : two ? c2 : c0) & 1u);
         };
         auto scores = [&](int c) {
             tc_fence_after();
@@ -631,7 +648,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
         if (any) {  // every product is complete before the tensor memory is released
             if (lead) umma_commit(bar(kDrain));
-            mbar_wait_bounded(bar(kDrain), 0u, kLPolls);
+            for (uint32_t k = 0; k < kLPolls && !__all_sync(0xffffffffu, mbar_try_wait(bar(kDrain), 0u)); ++k) {}  // whatever has failed
         }
     } else if (tid == 3 * kLGroup + 64 && !kState) {
         // ============ o out ============

@@ -1,0 +1,61 @@
+"""Linear attention where tokens or states are not finite, against the recurrence in 64 bits.  Tolerances are those of test_gpu_linear."""
+import math
+
+import pytest
+import torch
+
+import gated_deltanet_linear_mtp_gb300 as gdn
+import linear_ref
+from test_gpu_linear import I32, Case, near
+
+pytestmark = pytest.mark.gpu
+INF = math.inf
+
+
+def where_finite(x, ref, A, extra, what):
+    """x is finite where the recurrence's result is, and near it there."""
+    fine = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(x), fine), what
+    near(x[fine], ref[fine], A[fine], extra, what)
+
+
+def recurrence(c, S0, tokens):
+    """linear_ref.steps for some of the tokens, on the GPU (hundreds of steps take minutes on a host)."""
+    return linear_ref.steps(S0, c.q[tokens], c.k[tokens], c.v[tokens], c.ld, c.scale)
+
+
+def run_prompts(c, cu, has=None):
+    ws = gdn.linear_prefill_workspace(c.q.shape[0], c.B, c.HV, c.DK, c.DV)
+    ws.fill_(255)
+    gdn.gdn_linear_prefill(c.q, c.k, c.v, c.ld, c.pool, c.read, torch.tensor(cu).to(**I32), c.o, ws, has, c.err, out_indices=c.write, scale=c.scale)
+    assert int(c.err) == 0
+    return ws
+
+
+@pytest.mark.parametrize("DK,state", [(128, "bf16"), (128, "f32"), (64, "f32")])
+@pytest.mark.parametrize("lens", [[200], [384], [946], [140, 300]])
+def test_products_that_wait_long_for_the_chunk_before(DK, state, lens):
+    """A chunk whose V is not finite takes a hundred microseconds for o, so that the products of the next wait beyond their first try: they and
+    their arrivals are issued once all the same, and the call ends by itself, not by its waits' limit of some seconds."""
+    N = sum(lens)
+    cu = [sum(lens[:b]) for b in range(len(lens) + 1)]
+    c = Case((N,), len(lens), 1, 2, DK, 64, "bf16", state, seed=N, log_decay=[-0.02, -0.3])
+    before = c.pool.clone()
+    for b in range(len(lens)):
+        for first in range(cu[b], cu[b + 1], 256):  # every other chunk
+            c.v[first + 5, :, (first - cu[b]) // 128] = INF
+    run_prompts(c, cu)
+    times = []
+    for _ in range(3):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        c.pool.copy_(before)
+        start.record()
+        run_prompts(c, cu)
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end))
+    assert max(times) < 500, times  # ms; the limit of one wait alone is about 16 s
+    for b in range(len(lens)):
+        o, s, oa, sa = recurrence(c, before[c.read[b]], slice(cu[b], cu[b + 1]))
+        where_finite(c.o[cu[b]:cu[b + 1]], o, oa, 2.0 ** -8, f"o of prompt {b}")
+        where_finite(c.pool[c.write[b]], s[-1], sa[-1], 2.0 ** -16 if state == "bf16" else 2.0 ** -24, f"state {b}")
