@@ -196,8 +196,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
     auto bar = [&](int i) -> uint32_t { return base + PL::BAR_OFF + 8u * (uint32_t)i; };
     float* pw = reinterpret_cast<float*>(sm + PL::PW_OFF);
     volatile int* fail = reinterpret_cast<volatile int*>(sm + PL::BAR_OFF + 8 * kNumLBars);
-    volatile int* odd = fail + 1;  // [2]: c + 1 where V of chunk c (by its parity) holds an infinity or NaN
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + PL::BAR_OFF + 8 * kNumLBars + 16);
+    // [4]: c + 1 where V of chunk c (c mod 4) holds an infinity or NaN.  V' of chunk c + 4 is formed after o of chunk c + 2, which waits for the
+    // storing warp to be past c + 1, and V of c + 4 is asked for when the releasing warp is past c + 2: a mark is read before it is written
+    // over.  (With two, the storing warp could read that of c + 2 for c's.)
+    volatile int* odd = fail + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + PL::BAR_OFF + 8 * kNumLBars + 24);
 
     auto stage = [&](int c) -> uint32_t { return (uint32_t)(c & 1) * PL::STAGE; };
     auto load_qk = [&](int c) {
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         for (int i = kPReady; i < kNumLBars; ++i) mbar_init(bar(i), kLGroup);                                         // of a group of threads
         fence_mbar_init();
         fence_proxy_async_smem();
-        fail[0] = odd[0] = odd[1] = 0;
+        fail[0] = odd[0] = odd[1] = odd[2] = odd[3] = 0;
 #ifdef GDN_TEST_MISSING_COPY
         // test build: the first chunks of the first item are never loaded nor arrived on: their waits run out
         if (item > 0 || blockIdx.y > 0)
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             const int m = min(kLC, n - c * kLC);
             __nv_bfloat16* dst =
                 static_cast<__nv_bfloat16*>(p.o) + ((int64_t)(tok0 + c * kLC + lt) * p.HV + h) * p.DV + dv0;
-            const bool slow = odd[c & 1] == c + 1;  // then V is read once more
+            const bool slow = odd[c & 3] == c + 1;  // then V is read once more
             // whole chunks go through shared memory and out by TMA: stored from here, 32 rows of 16 bytes an instruction, they took
             // 2000 cycles
             const bool staged = !slow && m == kLC;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     *reinterpret_cast<uint4*>(sm + PL::vp(kState && (c & 1), e) + at) =
                         make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
             }
-            if (!(probe.x == 0.f && probe.y == 0.f)) odd[c & 1] = c + 1;
+            if (!(probe.x == 0.f && probe.y == 0.f)) odd[c & 3] = c + 1;
             fence_proxy_async_smem();
             mbar_arrive(bar(kVReady + (c & 1)));
             if (kState) mbar_arrive(bar(kEmptyV + (c & 1)));
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         // ============ o out ============
         for (int c = 0; c < nch; ++c) {
             if (!wait(kStaged + (c & 1), (uint32_t)(c >> 1) & 1u)) break;
-            if (n - c * kLC >= kLC && odd[c & 1] != c + 1) {
+            if (n - c * kLC >= kLC && odd[c & 3] != c + 1) {
                 tma_store_3d(&maps.o, dv0, h, tok0 + c * kLC, base + (PL::OWN ? PL::O_OFF : stage(c) + PL::V_OFF));
                 bulk_commit_group();
                 bulk_wait_read_all();
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         // ============ V read: by V' and the intra product (which arrives by itself), and where it is not finite once more ============
         for (int c = 0; c < nch; ++c) {
             const uint32_t parity = (uint32_t)(c >> 1) & 1u;
-            if (!wait(kVReady + (c & 1), parity) || (odd[c & 1] == c + 1 && !wait(kStaged + (c & 1), parity))) break;
+            if (!wait(kVReady + (c & 1), parity) || (odd[c & 3] == c + 1 && !wait(kStaged + (c & 1), parity))) break;
             mbar_arrive(bar(kEmptyV + (c & 1)));
         }
     }

@@ -59,3 +59,20 @@ def test_products_that_wait_long_for_the_chunk_before(DK, state, lens):
         o, s, oa, sa = recurrence(c, before[c.read[b]], slice(cu[b], cu[b + 1]))
         where_finite(c.o[cu[b]:cu[b + 1]], o, oa, 2.0 ** -8, f"o of prompt {b}")
         where_finite(c.pool[c.write[b]], s[-1], sa[-1], 2.0 ** -16 if state == "bf16" else 2.0 ** -24, f"state {b}")
+
+
+@pytest.mark.parametrize("DK,state", [(128, "bf16"), (128, "f32"), (64, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("chunks", [(0, 1, 2, 3, 4, 5, 6), (0, 2, 4, 6), (1, 2, 4, 5), (0, 3, 4)])
+def test_infinite_values_in_chunk_after_chunk(DK, state, chunks):
+    """Each of these chunks has an infinity in a value dimension of its own: o of the others is served, of whole chunks by the copy out of shared
+    memory, of these by the sum over their tokens."""
+    L = 7 * 128 + 50
+    for seed in range(2):
+        c = Case((L,), 1, 1, 2, DK, 64, "bf16", state, seed=seed, log_decay=[-0.02, -0.3])
+        before = c.pool.clone()
+        for n in chunks:
+            c.v[128 * n + 37 * (seed + 1), :, n] = INF
+        run_prompts(c, [0, L])
+        o, s, oa, sa = recurrence(c, before[c.read[0]], slice(0, L))
+        where_finite(c.o, o, oa, 2.0 ** -8, "o")
+        where_finite(c.pool[c.write[0]], s[-1], sa[-1], 2.0 ** -16 if state == "bf16" else 2.0 ** -24, "state")
