@@ -299,6 +299,12 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// g^e (e >= 0) of a decay g = exp(log_decay): 1 for e = 0, for g = 0 too; of another g it is never 0 (the smallest fp32 number, 2^-149, is added:
+// at most a unit in the last place, and that below 2^-124 alone), so that an infinity in a state stays one while it decays.
+__device__ __forceinline__ float decay_power(float log_decay, int e) {
+    return e == 0 ? 1.f : expf((float)e * log_decay) + (log_decay > -INFINITY ? 1.4012984643e-45f : 0.f);
+}
+
 // Bounded wait for the phase with the given parity: false if it did not complete within `limit` polls.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, uint32_t limit) {
     for (uint32_t i = 0; i < limit; ++i)

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(Split<DK>::THREADS, Split<DK>::MIN_CTAS_PER_SM
         if (init && row0 + lr.row[i] < p.DV) Slice8<StT>::load_global(src + (int64_t)lr.row[i] * DK + 8 * pc, raw[i]);
     }
     const float ld = p.log_decay[h];
-    if (tid <= CT) pw[tid] = tid == 0 ? 1.f : expf((float)tid * ld);
+    if (tid <= CT) pw[tid] = decay_power(ld, tid);
     float2 S[RL][4];
     const InT* qp = static_cast<const InT*>(p.q);
     const InT* kp = static_cast<const InT*>(p.k);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(32 * kLinWarps, (sizeof(StT) * DK > 256 ? 4 : 
     } else {
         __syncwarp();
     }
-    const float pw = lane == 0 ? 1.f : expf((float)lane * ld);  // lane e: g^e (up to 16)
+    const float pw = decay_power(ld, lane);  // lane e: g^e (up to 16)
     auto power = [&](int e) { return __shfl_sync(0xffffffffu, pw, e & 31); };
 
     if constexpr (kOut) {

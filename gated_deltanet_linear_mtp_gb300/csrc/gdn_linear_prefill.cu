@@ -32,6 +32,7 @@
 // each piece adds to the state (K and V only), and the second starts every piece from the sum of those before it (one prompt of
 // 16384, fp32 pool, HV 16: 136 us on 128 CTAs; whole, with 76 heads on 152 CTAs, 337).
 #include <atomic>
+#include <cfloat>
 #include <cstring>
 #include <type_traits>
 
@@ -66,7 +67,7 @@ struct LinearPlan {
     static constexpr uint32_t O_OFF = SH_OFF + DK * 128;
     static constexpr uint32_t PW_OFF = O_OFF + (OWN ? BOX : 0) + 128;  // g^0 .. g^128, behind 32 floats that are read and not used
     static constexpr uint32_t BAR_OFF = PW_OFF + 132 * 4;
-    static constexpr uint32_t END = BAR_OFF + 8 * kNumLBars + 32;
+    static constexpr uint32_t END = BAR_OFF + 8 * kNumLBars + 48;
     static constexpr uint32_t BYTES = END + 1024;          // the base is aligned to 1024
     static_assert(BYTES <= 232448, "fits one SM");
     // The first launch of cut prompts has no queries and no o: the parts of V' of odd chunks lie there, so that one chunk's V' is formed
@@ -131,10 +132,53 @@ __device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, uint3
     return false;
 }
 
+// Where a CTA's tokens are, in shared memory for add_tokens
+struct Place {
+    int tok0, h, hk, dv0;
+};
+// What the m tokens of chunk c give to a thread's 32 columns of the state, which lie in tensor memory: column e += sum_j g^(m-1-j) v_j[e] k_j,
+// token by token in fp32.  For chunks that hold what is not finite; out of line, since the state's threads have no registers for it.
+template <int DK>
+__device__ __noinline__ void add_tokens(const LinearParams& p, const volatile Place* at, const float* pw, uint32_t columns, int c, int m) {
+    const int64_t tok = at->tok0 + c * kLC;
+    const int first = at->dv0 + kLHalf * ((threadIdx.x >> 7) & 1), dv = p.DV - first, kstep = p.HK * DK;
+    const int64_t vstep = (int64_t)p.HV * p.DV;
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + (tok * p.HK + at->hk) * DK + (threadIdx.x & 127);
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (tok * p.HV + at->h) * p.DV + first;
+#pragma unroll 1
+    for (int c0 = 0; c0 < kLHalf; c0 += 16) {
+        float x[16];
+        tmem_ld16(columns + c0, x);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int j = 0; j < m; ++j) {
+            const float k1 = __bfloat162float(k[(int64_t)j * kstep]), f = pw[m - 1 - j];
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+                if (c0 + e >= dv) break;  // DV is a multiple of 8
+                const uint4 v4 = *reinterpret_cast<const uint4*>(v + j * vstep + c0 + e);
+                const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {  // v k first: where it is not finite it stays so, whatever f is
+                    const float2 v2 = bf16x2_to_float2(vw[u]);
+                    x[e + 2 * u] = fmaf(f, v2.x * k1, x[e + 2 * u]);
+                    x[e + 2 * u + 1] = fmaf(f, v2.y * k1, x[e + 2 * u + 1]);
+                }
+            }
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(x[e]);
+        tmem_st8(columns + c0, w);
+        tmem_st8(columns + c0 + 8, w + 8);
+    }
+    tmem_wait_st();
+}
+
 // kState: the first launch of cut prompts (what a piece adds to the state; no queries, no outputs)
 template <int DK, typename StT, bool kState>
 __global__ void __launch_bounds__(kLThreads, 1)
-    gdn_linear_prefill_kernel(const LinearParams p, const __grid_constant__ LinearMaps maps, const int piece, float* ws) {
+    gdn_linear_prefill_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ LinearMaps maps, const int piece, float* ws) {
     constexpr int NP = std::is_same<StT, float>::value ? 3 : 2;  // parts of V'
     using PL = LinearPlan<DK, NP>;
     const int ndv = (p.DV + kLDv - 1) / kLDv;
@@ -200,6 +244,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     // storing warp to be past c + 1, and V of c + 4 is asked for when the releasing warp is past c + 2: a mark is read before it is written
     // over.  (With two, the storing warp could read that of c + 2 for c's.)
     volatile int* odd = fail + 1;
+    volatile Place* const place = reinterpret_cast<volatile Place*>(sm + PL::BAR_OFF + 8 * kNumLBars + 32);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + PL::BAR_OFF + 8 * kNumLBars + 24);
 
     auto stage = [&](int c) -> uint32_t { return (uint32_t)(c & 1) * PL::STAGE; };
@@ -224,6 +269,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         fence_mbar_init();
         fence_proxy_async_smem();
         fail[0] = odd[0] = odd[1] = odd[2] = odd[3] = 0;
+        place->tok0 = tok0, place->h = h, place->hk = hk, place->dv0 = dv0;
 #ifdef GDN_TEST_MISSING_COPY
         // test build: the first chunks of the first item are never loaded nor arrived on: their waits run out
         if (item > 0 || blockIdx.y > 0)
@@ -231,7 +277,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             for (int c = 0; c < min(nch, 2); ++c) load_qk(c), load_v(c);  // before anything else is set up
     }
     if (tid < 32) pw[tid - 32] = 0.f;
-    if (tid < kLC + 1) pw[tid] = tid == 0 ? 1.f : expf((float)tid * ld);
+    if (tid < kLC + 1) pw[tid] = decay_power(ld, tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -294,7 +340,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
     } else if (warp < 16) {
         // ============ thread = dk, half of the tile: the state ============
-        const bool mine = lt < DK;
+        const bool mine = 32 * wl < DK;  // of a warp
         const int dvh = dv0 + kLHalf * hf;                        // the thread's first value dimension
         const int64_t row = ((int64_t)h * p.DV + dvh) * DK + lt;  // of [HV, DV, DK]: its row, column dk
         const int64_t slot_elems = (int64_t)p.HV * p.DV * DK;
@@ -308,7 +354,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (mine) {
             if (from_ws) {
                 const int np = blockIdx.y == 0 ? 0 : 1;
-                const float gp = expf((float)piece * ld);
+                const float gp = decay_power(ld, piece);
                 for (int s = np; s <= (int)blockIdx.y; ++s) {
                     const float* src = wsp + (int64_t)s * (kLDv * DK);
 #pragma unroll
@@ -353,15 +399,41 @@ __global__ void __launch_bounds__(kLThreads, 1)
             ok = warp_wait(kUFull + (c & 1), (uint32_t)(c >> 1) & 1u);
             if (!ok) break;
             tc_fence_after();
-            const float gm = pw[min(kLC, n - c * kLC)];
+            const int m = min(kLC, n - c * kLC);
+            const float gm = pw[m];
+            bool slow = false;
 #pragma unroll
             for (int c0 = 0; c0 < kLHalf; c0 += 16) {
                 float u[16];
                 tmem_ld16(lane_base + u_col(c) + kLHalf * hf + c0, u);
                 tmem_wait_ld();
+                // A k that is not finite makes all of its row of the product so, whatever V is (0 too): one number tells.  Parts of an
+                // infinity sum to NaN: the state that such tokens give is then formed from the tokens themselves.
+                if (c0 == 0) slow = __any_sync(0xffffffffu, mine && (odd[c & 3] == c + 1 || !(fabsf(u[0]) <= FLT_MAX)));
+                if (slow) break;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     S[c0 / 2 + e] = __ffma2_rn(make_float2(gm, gm), S[c0 / 2 + e], make_float2(u[2 * e], u[2 * e + 1]));
+            }
+            if (slow) {  // g^m S waits in the place of the product, so that the loop below has the registers
+                const uint32_t at = lane_base + u_col(c) + kLHalf * hf;
+#pragma unroll
+                for (int c0 = 0; c0 < kLHalf; c0 += 8) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(gm * ((e & 1) ? S[(c0 + e) / 2].y : S[(c0 + e) / 2].x));
+                    tmem_st8(at + c0, w);
+                }
+                tmem_wait_st();
+                add_tokens<DK>(p, place, pw, at, c, m);
+#pragma unroll
+                for (int c0 = 0; c0 < kLHalf; c0 += 16) {
+                    float x[16];
+                    tmem_ld16(at + c0, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) S[c0 / 2 + e] = make_float2(x[2 * e], x[2 * e + 1]);
+                }
             }
             tc_fence_before();
             mbar_arrive(bar(kUFree + (c & 1)));

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(LinStream<DK, StT, kMode>::THREADS, 2)
             int* const d = reinterpret_cast<int*>(st + L::D0);
             const int b = d[0], h = d[1], out = d[3], n = d[4];
             if (b < 0) break;
-            const float pw = lane == 0 ? 1.f : expf((float)lane * __int_as_float(d[5]));  // lane e: g^e (up to 8)
+            const float pw = decay_power(__int_as_float(d[5]), lane);  // lane e: g^e (up to 8)
             auto power = [&](int e) { return __shfl_sync(0xffffffffu, pw, e & 31); };
 
             if (warp > W) {  // ---- w_tj = g^(t-j) (k_j . q_t), and whether k is finite ----

@@ -469,6 +469,9 @@ GDN_API int64_t gdn_kv4_attention_workspace(int32_t B, int32_t max_q, int32_t HQ
  * (l2_eps is not read).  out_indices [B], where a call takes it, names the slots that the final states go to, so that the
  * state read stays as it is (a cached prefix); NULL: state_indices.  There -1 writes no state, and anything else outside the
  * pool skips the lane (GDN_ERRBIT_INDEX).  Active lanes write distinct slots, and none that another lane reads.
+ * What is not finite reaches what the recurrence lets it reach and nothing else: a q its own token, a k or v its token and those
+ * behind it, a state its rows.  A state keeps infinities as the recurrence does, by whichever call it comes (but for an infinite k whose
+ * v g^e underflows in a step or in 16 tokens: NaN); o is infinite or NaN there.
  *
  * gdn_linear_decode -- T tokens (1 .. GDN_MAX_T) from state_pool[state_indices[b]]: o, and the final state.
  */

@@ -76,3 +76,73 @@ def test_infinite_values_in_chunk_after_chunk(DK, state, chunks):
         o, s, oa, sa = recurrence(c, before[c.read[0]], slice(0, L))
         where_finite(c.o, o, oa, 2.0 ** -8, "o")
         where_finite(c.pool[c.write[0]], s[-1], sa[-1], 2.0 ** -16 if state == "bf16" else 2.0 ** -24, "state")
+
+
+def as_the_recurrence(x, ref, A, extra, what):
+    """Infinities and NaN of a state are those of the recurrence, what is finite is near it."""
+    assert torch.equal(x.isnan(), ref.isnan()), what
+    assert torch.equal(torch.where(x.isinf(), x.double(), 0), torch.where(ref.isinf(), ref, 0)), what
+    fine = torch.isfinite(ref)
+    near(x[fine], ref[fine], A[fine], extra, what)
+
+
+def put(c, what, at, before):
+    """An infinity of each sign in v, in k (with a 0 of v beside it: NaN) or in a state."""
+    if what == "v":
+        c.v[at, :, 3], c.v[at + 1, :, 9] = INF, -INF
+    elif what == "k":
+        c.k[at, :, 5], c.v[at, :, 2] = -INF, 0.0
+    elif what == "both":
+        c.v[at, :, 3], c.k[at + 2, :, 7] = INF, INF
+        c.v[at + 1, :, 3] = -INF  # meets the first: NaN where k has the same sign
+    else:
+        before[c.read.long(), :, 6, 4], before[c.read.long(), :, 7, 1] = INF, -INF
+        c.pool.copy_(before)
+
+
+@pytest.mark.parametrize("what", ["v", "k", "both", "state"])
+@pytest.mark.parametrize("DK,state,io", [(128, "f32", "bf16"), (128, "bf16", "bf16"), (64, "f32", "bf16"), (64, "bf16", "bf16"), (32, "f32", "bf16"), (64, "f32", "f32")])
+@pytest.mark.parametrize("lens,at", [([300], 20), ([300], 140), ([129, 260], 150), ([1400], 1100), ([1400], 200), ([1400], 1390), ([40], 37)])
+def test_states_of_prompts_keep_infinities(what, DK, state, io, lens, at):
+    """Whole prompts and prompts in pieces; heads that forget slowly, and at once (outside the tensor-core kernel not so soon that v times a
+    power of g underflows beside an infinite k)."""
+    N = sum(lens) + 3
+    cu = [sum(lens[:b]) for b in range(len(lens) + 1)]
+    tensor = io == "bf16" and DK >= 64
+    c = Case((N,), len(lens), 1, 3, DK, 64, io, state, seed=at, log_decay=[-0.002, -0.9, -30.0 if tensor or what in ("v", "state") else -4.0])
+    before = c.pool.clone()
+    put(c, what, at, before)
+    run_prompts(c, cu)
+    for b in range(len(lens)):
+        o, s, oa, sa = recurrence(c, before[c.read[b]], slice(cu[b], cu[b + 1]))
+        as_the_recurrence(c.pool[c.write[b]], s[-1], sa[-1], (2.0 ** -16 if state == "bf16" else 2.0 ** -24) if tensor else 0, f"state {b}")
+        where_finite(c.o[cu[b]:cu[b + 1]], o, oa, 2.0 ** -8 if tensor else 0, f"o of prompt {b}")
+
+
+@pytest.mark.parametrize("what", ["v", "k", "both", "state"])
+@pytest.mark.parametrize("B,T,DK,DV,state,io", [(2, 8, 128, 64, "f32", "bf16"), (2, 16, 128, 64, "bf16", "bf16"), (2, 7, 64, 24, "f32", "bf16"),
+                                                (2, 9, 256, 32, "f32", "f32"), (300, 8, 128, 128, "bf16", "bf16"), (300, 5, 64, 128, "f32", "bf16")])
+def test_states_of_steps_keep_infinities(what, B, T, DK, DV, state, io):
+    c = Case((B, T), B, 1, 3, DK, DV, io, state, seed=T, log_decay=[-0.002, -0.9, -8.0 if what in ("v", "state") else -4.0])
+    before, lane = c.pool.clone(), B // 2
+    slots = c.read.clone()
+    c.read = c.read[lane:lane + 1]
+    flat = Case.__new__(Case)
+    flat.__dict__.update(c.__dict__, q=c.q[lane], k=c.k[lane], v=c.v[lane])
+    put(flat, what, 1, before)
+    o, s, oa, sa = recurrence(flat, before[slots[lane]], slice(0, T))
+    gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, slots, c.o, None, c.err, scale=c.scale)
+    where_finite(c.o[lane], o, oa, 0, "o of verify")
+    states = torch.zeros((B, T, 3, DV, DK), dtype=c.pool.dtype, device="cuda")
+    gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, slots, c.o, states, c.err, scale=c.scale)
+    where_finite(c.o[lane], o, oa, 0, "o beside states")
+    for t in range(T):
+        as_the_recurrence(states[lane, t], s[t], sa[t], 0, f"state after {t}")
+    gdn.gdn_linear_decode(c.q, c.k, c.v, c.ld, c.pool, slots, c.o, c.err, out_indices=c.write, scale=c.scale)
+    where_finite(c.o[lane], o, oa, 0, "o of decode")
+    as_the_recurrence(c.pool[c.write[lane]], s[-1], sa[-1], 0, "state of decode")
+    n = torch.full((B,), T - 1, **I32)
+    gdn.gdn_linear_commit(c.k, c.v, c.ld, c.pool, slots, n, c.err, out_indices=c.write)
+    as_the_recurrence(c.pool[c.write[lane]], s[T - 2], sa[T - 2], 0, "state of commit")
+    others = torch.arange(B, device="cuda") != lane
+    assert bool(torch.isfinite(c.pool[c.write[others].long()]).all()) and bool(torch.isfinite(c.o[others]).all()) and int(c.err) == 0
