@@ -325,17 +325,20 @@ __global__ void __launch_bounds__(kAcceptThreads) gdn_draft_accept_kernel(const 
 }  // namespace
 
 cudaError_t launch_draft_accept(const DraftAcceptParams& p, cudaStream_t s) {
-    // Lanes that fill the GPU: CTAs of 128 threads, up to four a lane (two where lanes alone are 512), of which eight share an SM and some
-    // read while others start, exchange and search.  Fewer lanes: 256 threads, as many CTAs as fill the GPU.  us in graph replays with draft
-    // probabilities, the second form / the first: 128 lanes of 131072 32.4 / 38.3, 160 47.6 / 42.1, 256 54.6 / 50.6; 256 of 5000 12.1 / 9.5;
-    // 512 of 32000 with four CTAs a lane 31.4 / 34.4.  (One lane of 131072: 8 CTAs 15 us a call, 4 19, 2 27.)
-    const bool many = p.B >= 152;
+    // Lanes that fill the GPU: CTAs of 128 threads, up to four a lane (two where those are six an SM), of which eight share an SM and some
+    // read while others start, exchange and search.  Fewer lanes: 256 threads, as many CTAs as fill the GPU.  us in graph replays, the second
+    // form / the first, with draft probabilities: 128 lanes of 131072 32.4 / 38.3, 160 47.6 / 42.1, 256 54.6 / 50.6; 128 of 32000 16.7 / 16.6,
+    // 160 23.1 / 17.7, 256 23.5 / 21.2; 256 of 5000 12.1 / 9.5; without them: 128 of 131072 32.2 / 38.8, 160 44.8 / 41.7, 256 52.5 / 48.3
+    // (of one row each 51.6 / 47.2).  Four CTAs a lane / two: 500 lanes of 32000 35.9 / 30.8, 464 of 131072 83.5 / 83.0.  (One lane of
+    // 131072: 8 CTAs 15 us a call, 4 19, 2 27.)
+    const int64_t sms = sm_count();
+    const bool many = p.B >= sms;
     const int warps = many ? 4 : 8;
     int ncta = 1;
     if (many)
-        while (ncta < 4 && p.V > ncta * 8192 && (int64_t)p.B * ncta < 1024) ncta *= 2;
+        while (ncta < 4 && p.V > ncta * 8192 && (int64_t)p.B * ncta < 6 * sms) ncta *= 2;
     else
-        while (ncta < kAcceptMaxCluster && ((int64_t)p.V > (int64_t)ncta * 65536 || ((int64_t)p.B * ncta < 456 && p.V > ncta * 2048))) ncta *= 2;
+        while (ncta < kAcceptMaxCluster && ((int64_t)p.V > (int64_t)ncta * 65536 || ((int64_t)p.B * ncta < 3 * sms && p.V > ncta * 2048))) ncta *= 2;
     // tiles of two blocks where a warp has more than eight blocks: its sum is formed once a tile (256 lanes of 131072: 59 us against 63)
     int tile = kAcceptBlock;
     if ((int64_t)p.V > (int64_t)tile * warps * ncta * 8) tile *= 2;

@@ -8,6 +8,16 @@
 
 namespace gdn {
 
+// SMs of the current device (0: it cannot be asked)
+inline int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return sms;
+}
+
 // Decode, verify and replay commit share one kernel: decode writes the final state back (pool_out ==
 // pool_in); verify optionally stores every intermediate state (cache != nullptr) and never writes the
 // pool; replay commit runs steps[b] tokens per lane, writes no outputs and writes the state back.
@@ -181,7 +191,7 @@ struct Kv4AttentionParams {
     int32_t* err;
 };
 
-// Linear attention with a decay for each head (gdn_linear.cu, gdn_linear_prefill.cu).
+// Linear attention with a decay for each head (gdn_linear.cuh, gdn_linear_{f32,bf16}.cu, gdn_linear_stream.cuh, gdn_linear_prefill.cu).
 struct LinearParams {
     const void* q;            // nullptr: no outputs (commit)
     const void* k;

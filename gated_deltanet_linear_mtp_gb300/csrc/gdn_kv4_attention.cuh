@@ -258,13 +258,6 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&f)[16]) {
 }
 
 // ---- host ---------------------------------------------------------------------------------------------------
-inline int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 // The codes as TMA sees them: [num_pages][2 HK][page_size][D / 2 bytes], copied by page (a tile at most)
 inline cudaError_t codes_map(const Kv4& kv, int tile, CUtensorMap* map) {
     const EncodeTiledFn fn = encode_tiled_fn();

@@ -752,21 +752,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, kLCols);
 }
 
-int linear_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return 152;
-    }
-    return sms;
-}
-
 // Tokens of a piece (a multiple of the chunk), 0 where prompts stay whole.  Cutting reads K and V once more, so it must at
 // least double the SMs at work.
 int linear_split(int B, int N, int HV, int DV) {
     const int64_t items = (int64_t)B * HV * ((DV + kLDv - 1) / kLDv);
     if (items == 0 || N == 0) return 0;
-    const int64_t times = linear_sms() / items;  // pieces that fill the GPU once
+    const int sms = sm_count();
+    const int64_t times = (sms > 0 ? sms : 152) / items;  // pieces that fill the GPU once
     if (times < 2) return 0;
     const int64_t chunks = (N / B + (int64_t)kLC - 1) / kLC;
     const int64_t per = (chunks + times - 1) / times > 4 ? (chunks + times - 1) / times : 4;

@@ -453,10 +453,8 @@ bool try_linear_stream(const LinearParams& p, cudaStream_t s, cudaError_t& err) 
         if (p.T > kLsTokens || p.cache != nullptr || !p.v_vec || blocks * ROWS >= 2 * (int64_t)p.DV || tiles > 0x7fffffff ||
             (sizeof(StT) == 4 && p.write))
             return false;
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            tiles < 4 * (int64_t)sms)
-            return false;
+        const int sms = sm_count();
+        if (sms == 0 || tiles < 4 * (int64_t)sms) return false;
         if constexpr (sizeof(StT) == 2) {
             if (p.write) {
                 err = p.q == nullptr ? launch_linear_stream<DK, StT, kLinCommit>(p, (uint32_t)tiles, sms, s)

@@ -38,13 +38,6 @@ inline bool chunked_range(int B, int T, int DK, int DV, int HV, int num_slots) {
 constexpr int kStagedMaxTokenBytes = 8;  // T * sizeof(state element) at or below which staging pays
 constexpr int kStagedMinCtasPerSm = 2;
 
-inline int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 template <typename StT, int DK, int KIB>
 bool use_staged(const RecurrentParams& p, int B, int sms) {
     using ST = Staged<DK, StT, KIB>;

@@ -297,8 +297,9 @@ cudaError_t launch_t(const TokenProbsParams& p, cudaStream_t s) {
     // CTAs a row.  Runs of up to 32768 elements where rows fill the GPU (512 rows of 131072 bf16: 4 CTAs 75 us, 2 81, 8 87; of 32768:
     // 1 CTA 19 us, 2 23, 4 30: a CTA's start and the exchange cost some microseconds), of 4096 where they do not (one row of 131072:
     // 8 CTAs 6.7 us, 4 8.7, 1 20.5)
+    const int sms = sm_count();
     int ncta = 1;
-    while (ncta < kProbMaxCluster && ((int64_t)p.V > (int64_t)ncta * 32768 || (rows * ncta < 152 && p.V > ncta * 4096))) ncta *= 2;
+    while (ncta < kProbMaxCluster && ((int64_t)p.V > (int64_t)ncta * 32768 || (rows * ncta < sms && p.V > ncta * 4096))) ncta *= 2;
     const int run = (int)(((int64_t)p.V + ncta * 64 - 1) / (ncta * 64) * 64);
     const unsigned gy = (unsigned)(rows < 65535 ? rows : 65535);  // rows < 2^31: z stays below 2^16
     cudaLaunchConfig_t cfg = {};
