@@ -1,6 +1,7 @@
-// gdn_linear.cuh -- linear attention with a fixed decay for each head, a few tokens at a time on the CUDA cores (sm_103a):
+// gdn_linear.cuh -- linear attention with a fixed decay for each head, a few tokens at a time (sm_103a):
 //     S_t = g S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   g = exp(log_decay[h])
-// for decode, verify, commit and the prompts that the tensor-core kernel does not take.
+// for decode, verify, commit and the prompts that the tensor-core kernel does not take.  bf16 tokens of a step are products on mma.sync (the second
+// kernel below, and the streaming one for many lanes); fp32 tokens, DK 16, DK 256 with fp32 states and prompts are the first kernel's, on the CUDA cores.
 //
 // Over n tokens from a state S_0 the recurrence unrolls to
 //     o_t = scale (g^{t+1} S_0 q_t + sum_{j <= t} w_tj v_j),   w_tj = g^{t-j} (k_j . q_t)
@@ -9,9 +10,10 @@
 // a verify that keeps nothing does a third of the work of the step-by-step form.  Only powers g^e with e >= 0 appear, so no
 // decay overflows, and g^0 is 1 for g = 0 too.  A verify that stores the state after every token goes step by step.
 //
-// A CTA of 4 warps holds RPC rows of one (lane, head) in fp32 registers (the lane layout of Split: 8 columns of RL rows a
-// lane) and takes the tokens in chunks of up to 16 from shared memory.  Bytes bound it: the state is read once and
-// written once.
+// In the first kernel a CTA of 4 warps holds RPC rows of one (lane, head) in fp32 registers (the lane layout of Split: 8 columns of RL rows a
+// lane) and takes the tokens in chunks of up to 16 from shared memory.  Bytes bound a token or two (decode of 128 lanes, D 128, fp32 tokens and
+// states: 118 us, 4.6 TB/s); more tokens are bound by their dot products and shared-memory reads (verify of 128 lanes x 8 with bf16 states 153 us,
+// five times its bytes; prompts of 4 x 2048, HV 32, D 128: 2440 us with fp32 tokens, 2330 with DV 100, 6160 with DK 256).
 #pragma once
 
 #include <type_traits>
@@ -247,9 +249,11 @@ __global__ void __launch_bounds__(Split<DK>::THREADS, Split<DK>::MIN_CTAS_PER_SM
 //   * Factors that are not bf16 go in as three bf16 parts (24 bits, what fp32 holds): w_tj, and the elements of fp32 states.
 //   * A token's q as the product's column for S q is, register by register, its row for q . k.
 // A value that is not finite would reach earlier tokens as 0 times it: then the sum over j is formed term by term.
-// Measured (HK 16, HV 32, D 128): decode of 64 lanes with fp32 states 47.5 us (5.7 TB/s; the lane layout above: 63), verify of 128 x 4 with
-// states kept 110 (6.2 TB/s; 137).  Verify and commit of many lanes wait for loads here and are the streaming kernel's
-// (gdn_linear_stream.cuh); two blocks of rows a warp measured the same or slower (fewer warps).
+// Measured (HK 16, HV 32, D 128, in graph replays): decode of 64 lanes with fp32 states 46.6 us (5.8 TB/s; the lane layout above: 63), verify of
+// 128 x 4 with states kept 100.5 (6.8 TB/s; 137), commit of 128 x 8 with fp32 states 92 (5.9 TB/s); 9 to 16 tokens of 256 lanes, bf16 states: verify
+// 94 to 114, commit 121 to 137, decode 211 to 300, two to three times their bytes (loads behind the slot, stores behind the products).  Verify and
+// commit of many lanes and up to 8 tokens wait for loads here and are the streaming kernel's (gdn_linear_stream.cuh); two blocks of rows a
+// warp measured the same or slower (fewer warps).
 enum { kLinVerify, kLinDecode, kLinKept, kLinCommit };
 constexpr int kLinWarps = 4;
 
@@ -316,9 +320,12 @@ constexpr int linear_mma_smem(int T, bool update) {
     return (update ? T * DK * 4 : 0) + kLinWarps * T * 32;
 }
 
-// NTI: tokens / 8, rounded up
+// NTI: tokens / 8, rounded up.  CTAs an SM: as many as registers hold without spills to speak of.  bf16 states with DK 128 and outputs spilled
+// 48 to 144 bytes with one more: us in graph replays then / now, 256 lanes of 16 tokens verify 155 / 114, decode 311 / 300, 128 lanes of 4 with
+// states kept 107 / 100.5, decode of one lane 4.0 / 3.6; the commit, which does not spill, has it (16 tokens 137 / 147).  fp32 states with DK 64
+// spill 4 to 16 bytes: one CTA less takes 81 instead of 94 for 256 lanes of 16 tokens, but 91.7 instead of 87.9 for their decode.
 template <int DK, typename StT, int NTI, int kMode>
-__global__ void __launch_bounds__(32 * kLinWarps, (sizeof(StT) * DK > 256 ? 4 : 6) - (NTI == 2) - (DK == 256)) gdn_linear_mma_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(32 * kLinWarps, (sizeof(StT) * DK > 256 ? 4 : 6) - (NTI == 2) - (DK == 256) - (kMode != kLinCommit && sizeof(StT) == 2 && DK == 128)) gdn_linear_mma_kernel(const LinearParams p) {
     constexpr int NP = DK / 32;
     constexpr bool kOut = kMode != kLinCommit, kUpdate = kMode != kLinVerify;
     extern __shared__ float4 smem4[];
@@ -596,7 +603,8 @@ cudaError_t launch_linear_dk(const LinearParams& p, cudaStream_t s) {
         if (p.cu_seqlens == nullptr) return p.T <= 8 ? launch_linear_mma<DK, StT, 1>(p, s) : launch_linear_mma<DK, StT, 2>(p, s);
     }
     using SP = Split<DK>;
-    const int CT = p.cu_seqlens != nullptr || p.T > kLinChunk ? kLinChunk : p.T;
+    static_assert(kLinChunk >= GDN_MAX_T, "a step is one chunk");
+    const int CT = p.cu_seqlens != nullptr ? kLinChunk : p.T;
     const size_t smem = sizeof(float) * linear_smem_floats<DK>(CT);
     static_assert(sizeof(float) * linear_smem_floats<DK>(kLinChunk) <= 48 * 1024, "fits the default shared memory");
     const dim3 grid((p.DV + SP::RPC - 1) / SP::RPC, p.HV, p.B);
