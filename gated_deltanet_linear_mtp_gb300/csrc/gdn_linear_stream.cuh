@@ -8,9 +8,9 @@
 //   * The update sum_j (g^(n-1-j) v_j) k_j^T is a product as well: A = v_j g^(n-1-j) in three bf16 parts, two of them side by side as
 //     the 16 columns of one instruction; B = k transposed by its load.  k's words lie permuted in shared memory so that a lane's sums are of
 //     the eight columns of S that it holds.  Values that are not finite take the sum term by term.
-// Measured in graph replays (HK 16, HV 32, D 128, bf16 states): verify of 256 lanes x 8 tokens 45.3 us (6.3 TB/s; a CTA per 64 rows 62.8),
-// its commit 88 (5.6 TB/s of mixed traffic; 101).  Writing the states by bulk copies from shared memory measured the same
-// (88.7).
+// Measured in graph replays (HK 16, HV 32, D 128, bf16 states): verify of 256 lanes x 8 tokens 49.2 us (6.5 TB/s; a CTA per 64 rows 66.8),
+// their commit 91 in place, 96 into other slots (6 and 5.7 TB/s of mixed traffic; 110 in place), decode of 256 lanes 89 and 94 (96 in place);
+// verify of 128 lanes x 8 with fp32 states 47.5 (6.2 TB/s; 56).  Writing the states by bulk copies from shared memory measured the same (88.7 against 88.2).
 #pragma once
 
 #include "gdn_tcgen05.cuh"
@@ -76,11 +76,13 @@ __global__ void __launch_bounds__(LinStream<DK, StT, kMode>::THREADS, 2)
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (NS + s); };
     auto ready = [&](int s) { return bars + 8 * (2 * NS + s); };
-    // bounded: a wait that runs out ends the CTA's work
+    // of a whole warp, bounded: a wait that runs out ends the CTA's work.  Every branch goes by a vote, so that the warp stays together for its
+    // products and transposed loads.
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        bool ok = mbar_try_wait(bar, parity);
-        for (uint32_t i = 0; !ok && i < GDN_WAIT_POLLS && *fail == 0; ++i) ok = mbar_try_wait(bar, parity);
-        return (bool)__all_sync(0xffffffffu, ok);
+        bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+        for (uint32_t i = 0; !ok && i < GDN_WAIT_POLLS && !__any_sync(0xffffffffu, *fail != 0); ++i)
+            ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+        return ok;
     };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3, T = p.T;
     if (tid == 0) {
@@ -441,10 +443,11 @@ cudaError_t launch_linear_stream(const LinearParams& p, uint32_t tiles, int sms,
 }
 
 // Whether the call is the streaming kernel's; false (nothing launched) otherwise.  It takes what it is faster at, where a tile is
-// not half empty and the CTAs get two of them (us in graph replays, streaming / a CTA per 64 rows; HV 32, DV 128): verify of 8 tokens, DK 128,
-// bf16 states: 16 lanes (3.4 tiles an SM) 7.0 / 7.0, 32 lanes 9.0 / 10.5, 128 lanes 25.6 / 31.3; DK 64: 32 lanes 7.3 / 8.3, fp32 states
-// 9.7 / 11.6; DV 64 of DK 128, tiles half empty: commit of 64 lanes 16.9 / 16.7, decode 18.4 / 15.6.  fp32 states that are written leave
-// no room for either: decode of 64 lanes, DK 128, 47.0 / 45.6.
+// not half empty and the CTAs get two of them, four an SM (us in graph replays, streaming / a CTA per 64 rows; HV 32, DV 128, bf16 states, DK
+// 128): verify of 8 tokens 16 lanes (3.4 tiles an SM) 6.6 / 7.1, 20 lanes 7.8 / 7.9, 32 8.8 / 11.2, 128 27.1 / 35.8, of 4 tokens 20 lanes
+// 7.8 / 7.2, 32 9.1 / 9.5, 128 25.3 / 28.8; commit of 20 lanes 10.5 / 11.5; decode of one token 20 lanes 11.3 / 10.8, 32 14.2 / 15.5, 256
+// 88.8 / 96.0.  DK 64, 32 lanes: verify 7.4 / 8.4, with fp32 states 9.7 / 11.6.  DV 64 of DK 128, tiles half empty: commit of 64 lanes 16.9 / 16.7,
+// decode 18.4 / 15.6.  fp32 states that are written leave no room for either: decode of 64 lanes, DK 128, 47.0 / 45.6.
 template <int DK, typename StT>
 bool try_linear_stream(const LinearParams& p, cudaStream_t s, cudaError_t& err) {
     if constexpr (DK >= 64) {
