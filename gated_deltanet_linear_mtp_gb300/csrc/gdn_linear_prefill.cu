@@ -24,13 +24,20 @@
 // instructions).  The only serial chains between chunks are state -> inter -> state and V' -> update -> state; the scores of the
 // next chunk and the intra product fill the tensor cores meanwhile.
 //
-// Measured (D 128): 8 prompts of 8192, HK 16, HV 32, bf16 pool 401 us (4.0 TB/s, 342 TFLOP/s of the recurrence's 4 DK DV a token); a step
-// of one chunk and 64 dv takes about 3950 cycles, of which the products run 2000 and their issue takes 2770, and a CTA's start and end 9 us.
-// Two warps issuing two products each measured the same (400).
+// P and S as bf16 take o to 0.0023 of itself from 64-bit arithmetic, where its own rounding alone leaves 0.0017.  P in two parts, which its
+// place in tensor memory has room for, is 8 more products a chunk: 0.0020, for 419 us instead of 392 in the first case below and 141 instead of 133
+// in the second; S in two parts does not fit beside three of V'.
+//
+// Waits of a warp go by votes (warp_wait): after a lane-by-lane wait the warp can stay in parts, and each would issue its products and commits.
+// Where V or k of a chunk holds what is not finite, o sums P V and the state its tokens one by one: about 66 us a chunk.
+//
+// Measured (D 128, HK 16, HV 32, bf16 pool): 7 prompts of 8192 and an empty one 394 us (3.6 TB/s, 305 TFLOP/s of the recurrence's 4 DK DV a token;
+// three waves of CTAs), 8 of 8192 511 (four), 4 of 2048 76; a step of one chunk and 64 dv takes about 3700 cycles, of which the products run
+// 2000 and their issue takes 2770, and a CTA's start and end 9 us.  Two warps issuing two products each measured the same.
 //
 // Few prompts and heads leave SMs without work: then prompts are cut into pieces (linear_split), a first launch forms what
 // each piece adds to the state (K and V only), and the second starts every piece from the sum of those before it (one prompt of
-// 16384, fp32 pool, HV 16: 136 us on 128 CTAs; whole, with 76 heads on 152 CTAs, 337).
+// 16384, fp32 pool, HV 16: 133 us on 128 CTAs; whole, with 76 heads on 152 CTAs, 337).
 #include <atomic>
 #include <cfloat>
 #include <cstring>
@@ -188,8 +195,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const int hf = (warp >> 2) & 1, wl = warp & 3;  // half of a group, and the warp's quarter of the lanes
 
     // Everything that tells what to do is asked for at once.  Of up to 32 whole prompts a lane asks for one each, and the longest is
-    // taken first, so that no long one is left for the end.  (HV 32, D 64: 32 prompts of 17 to 2048 131 us against 141 in the order of the
-    // lanes, 8 of 17 to 8192 138 against 154; 32 of 1024 each 156 against 150, for the longer start.)
+    // taken first, so that no long one is left for the end.  (HV 32, D 64, fp32 pool, in graph replays, against the order of the lanes: two draws
+    // of 32 prompts of 17 to 2048 tokens 159 and 167 us against 168 and 178, of 8 of 17 to 8192 133 and 161 against 144 and 196; 32 of 1024 149 in
+    // either.  33 prompts go in the lanes' order: a lane each is what a warp has.)
     const bool sorted = piece == 0 && p.B > 1 && p.B <= 32;
     int b = sorted ? min(tid & 31, p.B - 1) : turn;
     int slot = p.indices[b];

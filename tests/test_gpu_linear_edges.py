@@ -146,3 +146,44 @@ def test_states_of_steps_keep_infinities(what, B, T, DK, DV, state, io):
     as_the_recurrence(c.pool[c.write[lane]], s[T - 2], sa[T - 2], 0, "state of commit")
     others = torch.arange(B, device="cuda") != lane
     assert bool(torch.isfinite(c.pool[c.write[others].long()]).all()) and bool(torch.isfinite(c.o[others]).all()) and int(c.err) == 0
+
+
+@pytest.mark.parametrize("kind", ["prompts", "pieces", "verify", "commit"])
+def test_beside_streams_that_take_the_memory(kind):
+    """Copies on other streams make tiles come late, beyond a wait's first try: results are those of a call alone, bit by bit."""
+    if kind in ("prompts", "pieces"):
+        lens = [2048, 130, 777, 1500] if kind == "prompts" else [6000]
+        N = sum(lens)
+        cu = torch.tensor([sum(lens[:b]) for b in range(len(lens) + 1)]).to(**I32)
+        c = Case((N,), len(lens), 8 if kind == "prompts" else 1, 16 if kind == "prompts" else 2, 128, 128, "bf16", "bf16", seed=7)
+        ws = gdn.linear_prefill_workspace(N, c.B, c.HV, c.DK, c.DV)
+
+        def call():
+            gdn.gdn_linear_prefill(c.q, c.k, c.v, c.ld, c.pool, c.read, cu, c.o, ws, None, c.err, out_indices=c.write, scale=c.scale)
+    else:
+        c = Case((128, 8), 128, 8, 16, 128, 128, seed=7)
+        n = torch.full((128,), 5, **I32)
+
+        def call():
+            if kind == "verify":
+                gdn.gdn_linear_verify(c.q, c.k, c.v, c.ld, c.pool, c.read, c.o, None, c.err, scale=c.scale)
+            else:
+                gdn.gdn_linear_commit(c.k, c.v, c.ld, c.pool, c.read, n, c.err, out_indices=c.write)
+    call()
+    torch.cuda.synchronize()
+    o, pool = c.o.clone(), c.pool.clone()
+    big = [torch.ones(1 << 28, device="cuda") for _ in range(4)]
+    others = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(others):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    big[2 * i].copy_(big[2 * i + 1])
+        c.o.fill_(7.25)
+        for _ in range(3):
+            call()
+        torch.cuda.current_stream().synchronize()
+        assert torch.equal(c.pool, pool) and (kind == "commit" or torch.equal(c.o, o))
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
